@@ -66,8 +66,10 @@ typedef enum {
                              smd_workspace_bytes() or not 16-byte aligned    */
     SMD_ERR_GROUP = -9,   /* device status: rows of a group do not share their
                              index list (smd_sparse_mla_decode_grouped)      */
-    SMD_ERR_INDEX = -10   /* device status: a valid entry of the index list
+    SMD_ERR_INDEX = -10,  /* device status: a valid entry of the index list
                              lies outside [0, N) (smd_validate_indices)      */
+    SMD_ERR_PAGES = -11   /* device status: a request was refused for want of
+                             pages, table width or slots (smd_block_tables)  */
 } smd_status;
 
 /* Kernel families. */
@@ -623,6 +625,202 @@ int smd_fp8_mma_probe(int32_t iters, int32_t* status, smd_stream_t stream, int32
 int smd_trace_enabled(void);
 int smd_trace_read(int32_t kernel, uint64_t* host, int32_t n);
 int smd_trace_clear(int32_t kernel);
+
+/* ---- a paged key/value cache in E4M3 -------------------------------------------
+ *
+ * The calls above read one latent row per token from a pool with one scale.
+ * The calls below serve layers whose query heads share a smaller number of
+ * key/value heads: a cache of pages, each holding page_size consecutive
+ * tokens of one request, keys and values in E4M3 with an fp32 scale for each
+ * page and head. smd_block_tables gives pages to requests and slots to
+ * their new tokens; smd_paged_append writes those tokens' keys and values;
+ * smd_block_scores bounds the logits of every page for a query, in the bf16
+ * that smd_topk_select takes; smd_paged_decode attends, over a request's whole
+ * table or over the pages a list names.
+ *
+ * The token of slot s is token s % page_size of page s / page_size. A
+ * request's token t is in page table[r][t / page_size].
+ *
+ * The cache, described once by the caller and completed by
+ * smd_paged_cache_init; the calls read it and keep nothing:
+ *   k, v      E4M3 codes of head_dim columns for each (page, head, token).
+ *             Element (p, h, t, c) is at k + p * k_stride[0] + h * k_stride[1]
+ *             + t * k_stride[2] + c (strides in bytes; pages may hold heads
+ *             outside tokens or tokens outside heads, keys and values may
+ *             share an allocation). Both NULL in a cache that only
+ *             smd_block_scores reads.
+ *             Addresses and strides are multiples of 16 bytes.
+ *   k_scale, v_scale   [pages, heads] float32, positive: a code stands for
+ *             code * scale.
+ *   bounds    [pages, heads, 2, head_dim] bfloat16, or NULL: the largest (0)
+ *             and smallest (1) value of each channel among a page's keys as
+ *             they were before rounding to E4M3. smd_paged_append keeps them,
+ *             smd_block_scores reads them. 16-byte aligned.
+ *   pages     >= 1; pages * page_size < 2^31.
+ *   heads     key/value heads, >= 1.
+ *   page_size tokens of a page, a multiple of 16 up to 256.
+ *   head_dim  64, 128 or 256.
+ *   map       filled in by smd_paged_cache_init (the copy descriptors of k and
+ *             v); a struct whose other fields change is initialised again. */
+typedef struct {
+    uint8_t* k;
+    uint8_t* v;
+    float* k_scale;
+    float* v_scale;
+    uint16_t* bounds;
+    int64_t k_stride[3];
+    int64_t v_stride[3];
+    int32_t pages;
+    int32_t heads;
+    int32_t page_size;
+    int32_t head_dim;
+    uint64_t map[36];
+} smd_paged_cache_t;
+
+/* Checks the description and fills in `map`. Host only: touches no device
+ * memory. Returns SMD_OK, SMD_ERR_NULL (cache is NULL, one of k and v alone,
+ * a scale missing beside them, or neither them nor bounds), SMD_ERR_SHAPE (the
+ * ranges above; a token stride below head_dim, or strides that are not positive or
+ * beyond 2^40), SMD_ERR_ALIGN, SMD_ERR_DEVICE (k and v need the driver's
+ * descriptor encoder). */
+int smd_paged_cache_init(smd_paged_cache_t* cache);
+
+/* Pages and slots of one step, from the requests' lengths.
+ *   lengths     [R] int32: tokens each request holds (>= 0).
+ *   new_tokens  [R] int32: n >= 0: the request gets n more tokens; n < 0: it
+ *               has ended, its pages go back and its length becomes 0.
+ *   table       [R, table_stride] int32: row r's first ceil(length / P) entries
+ *               are its pages (P = page_size); width entries of a row may be
+ *               used. Entries of the pages given now are written; the rest
+ *               is left as it is.
+ *   ring        [pages] int32: the free pages are ring[i % pages] for
+ *               state[0] <= i < state[1]. Pages that go back are written
+ *               after them, by ascending request, then by their order in the
+ *               table; they are not given out by the same call.
+ *   state       [2] int64: pages taken and pages given back so far (both only
+ *               grow; state[1] - state[0] <= pages is the number free).
+ * For each request in turn: need = ceil((length + n) / P) - ceil(length / P)
+ * pages. It is refused (nothing granted, its length kept) when the pages do
+ * not fit its row, when need > 0 and the needs so far, its own among them,
+ * exceed the free pages, or when n > 0 and the tokens so far, its own among
+ * them, exceed T. (A request refused for its row counts in neither sum, one
+ * refused for pages in the first, one refused for T in both.) A refusal writes
+ * SMD_ERR_PAGES to `status`.
+ * Written, g_r being the tokens granted to request r:
+ *   new_lengths [R] int32: length + g_r, 0 for a request that has ended.
+ *   new_state   [2] int64.
+ *   starts      [R + 1] int32: starts[r] = g_0 + .. + g_(r-1).
+ *   slots       [T] int32: the slot of each granted token, request by request;
+ *               -1 past starts[R].
+ *   positions   [T] int32: its position in its request; -1 past starts[R].
+ *               May be NULL.
+ * The outputs must not overlap lengths, new_tokens or state (the step's blocks
+ * read them while others write): a caller alternates two buffers. Bounds: 0
+ * <= R <= 8192, 0 <= T, 1 <= pages, pages * P < 2^31, 1 <= P, 1 <= width <=
+ * table_stride (SMD_ERR_SHAPE). An entry of lengths below 0 or beyond
+ * width * P is clamped. Pointers are device memory, 4-byte aligned (state,
+ * new_state: 8); `status` may be NULL. */
+int smd_block_tables(const int32_t* lengths, const int32_t* new_tokens, int32_t R,
+                     int32_t* table, int64_t table_stride, int32_t width, int32_t* ring,
+                     int32_t pages, const int64_t* state, int32_t page_size, int32_t T,
+                     int32_t* new_lengths, int64_t* new_state, int32_t* starts, int32_t* slots,
+                     int32_t* positions, int32_t* status, smd_stream_t stream);
+
+/* Writes T tokens' keys and values into the cache.
+ *   k, v    [T, heads, head_dim] bfloat16; token t starts at k + t * k_stride
+ *           (elements; a multiple of 8), heads are head_dim apart. 16-byte
+ *           aligned. Slices of a fused projection are fine.
+ *   slots   [T] int32; a negative slot, or one beyond the pool, is skipped.
+ * Tokens that continue one another (slot[t + 1] = slot[t] + 1, same page) form
+ * a run; a page may be in one run of a call. For each run, head and side, o
+ * being the offset of its first token in the page:
+ *   a     = the largest |x| of the run that is not a NaN (an infinity counts as
+ *           the largest finite bfloat16)
+ *   e     = ceil(log2(a / 448)), at least -120
+ *   scale = max(2^e, the page's scale if o > 0)
+ *   tokens before o are kept: code = E4M3(code * old scale / scale)
+ *   the run's tokens:         code = E4M3(x / scale), infinities at +-448, NaN
+ *                             as NaN
+ * A power of two as scale makes both quotients exact, so a kept token loses
+ * nothing but what falls off at the small end; the codes have the same
+ * relative precision with any scale. Tokens of the page after the run are not
+ * kept (a shorter run later writes over rejected tokens). bounds (unless
+ * NULL) becomes the largest and smallest key of each channel, of the run and,
+ * if o > 0, of the bounds before; NaN are passed over, infinities count as
+ * the largest finite values.
+ * T >= 0 (0: no-op). Returns SMD_OK, SMD_ERR_NULL, SMD_ERR_SHAPE,
+ * SMD_ERR_ALIGN, SMD_ERR_DEVICE, SMD_ERR_LAUNCH. */
+int smd_paged_append(const smd_paged_cache_t* cache, const uint16_t* k, int64_t k_stride,
+                     const uint16_t* v, int64_t v_stride, const int32_t* slots, int32_t T,
+                     smd_stream_t stream);
+
+/* An upper bound, up to its rounding, of the products of a row's queries with
+ * the keys of each page: for row b, kv head h and page j of its request,
+ *   score[b, h, j] = BF16(max over the query heads i of h of
+ *                         sum_c max(q[b,i,c] * hi[c], q[b,i,c] * lo[c]))
+ * with hi, lo the bounds of the page; query heads h * Hq / heads and the
+ * Hq / heads - 1 after it are those of kv head h (at most 128 of them).
+ *   q        [B, Hq, head_dim] bfloat16, row b at q + b * q_stride (elements; a
+ *            multiple of 8; rows of heads are head_dim apart), 16-byte aligned,
+ *            finite. B = R * row_group.
+ *   table    [R, table_stride] int32, width entries a row.
+ *   lengths  [R] int32, clamped to [0, width * page_size].
+ *   row_group   G = 1..8: rows r * G + i, i < G, are request r's, and row i
+ *            sees its first n = length - G + 1 + i tokens, so its first
+ *            ceil(n / page_size) pages.
+ *   keep_first, keep_last   >= 0: the scores of that many first and last pages
+ *            that a row sees are +infinity (a select takes them first).
+ *   scores   [B, heads, score_stride] bfloat16, written up to width; the pages
+ *            past those a row sees get NaN, which smd_topk_select passes over.
+ * Table entries outside the pool read nothing and score as zero bounds would.
+ * Returns SMD_OK, SMD_ERR_NULL (also: a cache without bounds), SMD_ERR_SHAPE,
+ * SMD_ERR_ALIGN, SMD_ERR_DEVICE, SMD_ERR_LAUNCH. */
+int smd_block_scores(const uint16_t* q, int64_t q_stride, const smd_paged_cache_t* cache,
+                     const int32_t* table, int64_t table_stride, int32_t width,
+                     const int32_t* lengths, int32_t R, int32_t row_group, int32_t Hq,
+                     int32_t keep_first, int32_t keep_last, uint16_t* scores,
+                     int64_t score_stride, smd_stream_t stream);
+
+/* Bytes of workspace smd_paged_decode needs for this cache on the current
+ * device, whatever the batch. Negative (an smd_status) on failure. */
+int64_t smd_paged_workspace_bytes(const smd_paged_cache_t* cache);
+
+/* Attention over the cache. For row b (verify row i of request r, as in
+ * smd_block_scores) and query head a of kv head h, over the tokens t that the
+ * row sees:
+ *   s_t  = sm_scale * sum_c q[b,a,c] * k[t,h,c]
+ *   lse  = ln sum_t e^(s_t);  out[c] = BF16(sum_t e^(s_t - lse) v[t,h,c])
+ * with k, v the values the codes stand for; a row that sees nothing gets
+ * zeros and -inf. Sums and statistics are fp32; the weights enter the second
+ * product as f16 at 2^14 of the running maximum, the queries the first as f16
+ * at a power of two of each (row, head)'s maximum (exact but for elements
+ * below 2^-30 of it).
+ *   block_lists   NULL: a row sees its first n = length - G + 1 + i tokens.
+ *            Else [B, heads, K] int32 (row b, kv head h): page numbers within
+ *            the request (0 = its first page), the first
+ *            clamp(block_counts[b, h], 0, K) of them; the row sees those
+ *            pages' tokens below n, once for each time a page is listed.
+ *            Numbers outside the row's pages are passed over (such as -1).
+ *   block_counts  [B, heads] int32; NULL: all K.
+ *   out      [B, Hq, head_dim] bfloat16, contiguous, 16-byte aligned.
+ *   lse      [B, Hq] float32; may be NULL.
+ *   workspace     at least smd_paged_workspace_bytes, 16-byte aligned; needs
+ *            no initialisation. Calls that overlap on the GPU must not share
+ *            one.
+ * The other arguments are smd_block_scores'. Codes of tokens that a row does
+ * not see never reach its result, whatever they are. Table entries outside the
+ * pool read nothing (their tokens count as zeros). The keys are cut by the
+ * lengths of the whole batch and the device's SM count, in a fixed order, so
+ * equal calls give equal bits, but a request's bits may change with the
+ * others in its batch. Returns SMD_OK, SMD_ERR_NULL, SMD_ERR_SHAPE,
+ * SMD_ERR_ALIGN, SMD_ERR_WORKSPACE, SMD_ERR_DEVICE, SMD_ERR_LAUNCH;
+ * SMD_ERR_TIMEOUT in `status` (optional) if a bounded wait runs out. */
+int smd_paged_decode(const uint16_t* q, int64_t q_stride, const smd_paged_cache_t* cache,
+                     const int32_t* table, int64_t table_stride, int32_t width,
+                     const int32_t* lengths, int32_t R, int32_t row_group, int32_t Hq,
+                     float sm_scale, const int32_t* block_lists, const int32_t* block_counts,
+                     int32_t K, uint16_t* out, float* lse, int32_t* status, void* workspace,
+                     int64_t workspace_bytes, smd_stream_t stream);
 
 /* Static text for a status code. */
 const char* smd_status_str(int status);

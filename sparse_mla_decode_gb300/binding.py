@@ -23,6 +23,7 @@ SMD_ERR_DEVICE = -7
 SMD_ERR_WORKSPACE = -8
 SMD_ERR_GROUP = -9
 SMD_ERR_INDEX = -10
+SMD_ERR_PAGES = -11
 
 SMD_KERNEL_AUTO = 0
 SMD_KERNEL_MMA = 1
@@ -57,6 +58,16 @@ class SmdOptions(ctypes.Structure):
                 ("library_scratch", ctypes.c_int32), ("reserved", ctypes.c_int32),
                 ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64),
                 ("status", ctypes.c_void_p), ("force", ctypes.POINTER(SmdPlan))]
+
+
+class SmdPagedCache(ctypes.Structure):
+    """smd_paged_cache_t."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("bounds", ctypes.c_void_p),
+                ("k_stride", ctypes.c_int64 * 3), ("v_stride", ctypes.c_int64 * 3),
+                ("pages", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("map", ctypes.c_uint64 * 36)]
 
 
 class SmdError(RuntimeError):
@@ -182,6 +193,23 @@ def lib() -> ctypes.CDLL:
             so.smd_trace_read.restype = ctypes.c_int
             so.smd_trace_clear.argtypes = [ctypes.c_int32]
             so.smd_trace_clear.restype = ctypes.c_int
+            ptr, i32, i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
+            cache = ctypes.POINTER(SmdPagedCache)
+            so.smd_paged_cache_init.argtypes = [cache]
+            so.smd_paged_cache_init.restype = ctypes.c_int
+            so.smd_block_tables.argtypes = [ptr, ptr, i32, ptr, i64, i32, ptr, i32, ptr, i32, i32,
+                                            ptr, ptr, ptr, ptr, ptr, ptr, ptr]
+            so.smd_block_tables.restype = ctypes.c_int
+            so.smd_paged_append.argtypes = [cache, ptr, i64, ptr, i64, ptr, i32, ptr]
+            so.smd_paged_append.restype = ctypes.c_int
+            rows = [ptr, i64, cache, ptr, i64, i32, ptr, i32, i32, i32]
+            so.smd_block_scores.argtypes = rows + [i32, i32, ptr, i64, ptr]
+            so.smd_block_scores.restype = ctypes.c_int
+            so.smd_paged_workspace_bytes.argtypes = [cache]
+            so.smd_paged_workspace_bytes.restype = i64
+            so.smd_paged_decode.argtypes = rows + [ctypes.c_float, ptr, ptr, i32, ptr, ptr, ptr,
+                                                   ptr, i64, ptr]
+            so.smd_paged_decode.restype = ctypes.c_int
             so.smd_status_str.argtypes = [ctypes.c_int]
             so.smd_version.restype = ctypes.c_int
             so.smd_version.argtypes = []
@@ -813,3 +841,263 @@ def topk_select_host(logits, K: int, row_ends=None, indices=None, counts=None, s
     if rc != SMD_OK:
         raise SmdError(rc, "smd_topk_select_host")
     return indices, counts
+
+
+# ---- the paged cache ------------------------------------------------------------------
+
+class PagedCache:
+    """A paged key/value cache in E4M3 (smd_paged_cache_t), over the caller's
+    tensors, which it keeps alive.
+
+    k, v: [pages, heads, page_size, head_dim] E4M3 (uint8 or float8_e4m3fn), any
+    strides in 16-byte steps with contiguous columns (a token-major pool is
+    passed as ``pool.transpose(1, 2)``); k_scale, v_scale: [pages, heads]
+    float32; bounds: [pages, heads, 2, head_dim] bfloat16 or None. A cache that
+    only block_scores reads may leave k, v and the scales out (then
+    ``page_size`` says how many tokens a page holds)."""
+
+    def __init__(self, k=None, v=None, k_scale=None, v_scale=None, bounds=None, page_size=None):
+        import torch
+
+        c = SmdPagedCache()
+        shape = None
+        for name, t in (("k", k), ("v", v)):
+            if t is None:
+                continue
+            t = _bytes_view(t, name)
+            if t.dim() != 4 or t.stride(3) != 1:
+                raise ValueError(f"{name} must be [pages, heads, page_size, head_dim] with "
+                                 "contiguous columns")
+            if shape is not None and tuple(t.shape) != shape:
+                raise ValueError("k and v must have one shape")
+            shape = tuple(t.shape)
+            setattr(c, name, _ptr(t))
+            setattr(c, name + "_stride", (ctypes.c_int64 * 3)(*t.stride()[:3]))
+        if shape is None:
+            if bounds is None or page_size is None:
+                raise ValueError("a cache without k and v needs bounds and page_size")
+            shape = (bounds.shape[0], bounds.shape[1], int(page_size), bounds.shape[3])
+        elif page_size is not None and int(page_size) != shape[2]:
+            raise ValueError(f"page_size {page_size} is not that of k and v ({shape[2]})")
+        for name, t, want, dtype in (
+                ("k_scale", k_scale, shape[:2], torch.float32),
+                ("v_scale", v_scale, shape[:2], torch.float32),
+                ("bounds", bounds, (shape[0], shape[1], 2, shape[3]), torch.bfloat16)):
+            if t is None:
+                continue
+            if tuple(t.shape) != tuple(want) or t.dtype != dtype or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {want}")
+            setattr(c, name, _ptr(t))
+        for name, t in (("k", k), ("v", v), ("k_scale", k_scale), ("v_scale", v_scale),
+                        ("bounds", bounds)):
+            if t is not None and not t.is_cuda:
+                raise ValueError(f"{name} must be a CUDA tensor")
+        c.pages, c.heads, c.page_size, c.head_dim = (int(x) for x in shape)
+        rc = lib().smd_paged_cache_init(ctypes.byref(c))
+        if rc != SMD_OK:
+            raise SmdError(rc, "smd_paged_cache_init")
+        self.k, self.v, self.k_scale, self.v_scale, self.bounds = k, v, k_scale, v_scale, bounds
+        self.pages, self.heads, self.page_size, self.head_dim = (int(x) for x in shape)
+        self.c, self.ref = c, ctypes.byref(c)
+
+    @classmethod
+    def empty(cls, pages: int, heads: int, page_size: int, head_dim: int, bounds: bool = True,
+              device="cuda"):
+        """A cache of newly allocated tensors (zero scales: nothing written yet)."""
+        import torch
+
+        def codes():
+            return torch.zeros((pages, heads, page_size, head_dim), dtype=torch.uint8, device=device)
+
+        def scale():
+            return torch.zeros((pages, heads), dtype=torch.float32, device=device)
+
+        b = torch.zeros((pages, heads, 2, head_dim), dtype=torch.bfloat16, device=device) \
+            if bounds else None
+        return cls(codes(), codes(), scale(), scale(), b)
+
+
+def _stream(stream, t) -> int:
+    import torch
+
+    if stream is None:
+        return torch.cuda.current_stream(t.device).cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _vector(t, name: str, dtype, n: int | None = None):
+    if not t.is_cuda or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor")
+    if n is not None and t.numel() < n:
+        raise ValueError(f"{name} must have at least {n} elements")
+
+
+def block_tables(lengths, new_tokens, table, ring, state, page_size: int, max_tokens: int | None = None,
+                 new_lengths=None, new_state=None, starts=None, slots=None, positions=None,
+                 status=None, stream=None):
+    """Pages and slots of a step (smd_block_tables). lengths, new_tokens [R],
+    ring [pages] int32, table [R, width] int32 (written in place where pages
+    are given), state [2] int64, all CUDA tensors; a new_tokens below 0 ends
+    the request. ``max_tokens``: the slots to make room for, if ``slots`` is not
+    given. Returns (new_lengths [R], new_state [2], starts [R + 1], slots [T],
+    positions [T]); the outputs may be given, and may not be the inputs."""
+    import torch
+
+    R = lengths.numel()
+    _vector(lengths, "lengths", torch.int32)
+    _vector(new_tokens, "new_tokens", torch.int32, R)
+    _vector(ring, "ring", torch.int32)
+    _vector(state, "state", torch.int64, 2)
+    if not table.is_cuda or table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] < R \
+            or table.stride(1) != 1:
+        raise ValueError("table must be an int32 CUDA tensor [>= R, width] with contiguous rows")
+    if slots is None:
+        if max_tokens is None:
+            raise ValueError("block_tables needs slots or max_tokens")
+        slots = torch.empty(int(max_tokens), dtype=torch.int32, device=lengths.device)
+    T = slots.numel()
+
+    def made(t, name, dtype, n):
+        if t is None:
+            return torch.empty(n, dtype=dtype, device=lengths.device)
+        _vector(t, name, dtype, n)
+        return t
+
+    new_lengths = made(new_lengths, "new_lengths", torch.int32, R)
+    new_state = made(new_state, "new_state", torch.int64, 2)
+    starts = made(starts, "starts", torch.int32, R + 1)
+    slots = made(slots, "slots", torch.int32, T)
+    positions = made(positions, "positions", torch.int32, T)
+    if new_lengths.data_ptr() == lengths.data_ptr() and R or new_state.data_ptr() == state.data_ptr():
+        raise ValueError("new_lengths and new_state may not be lengths and state")
+    rc = lib().smd_block_tables(
+        lengths.data_ptr(), new_tokens.data_ptr(), R, table.data_ptr(), table.stride(0),
+        table.shape[1], ring.data_ptr(), ring.numel(), state.data_ptr(), page_size, T,
+        new_lengths.data_ptr(), new_state.data_ptr(), starts.data_ptr(), slots.data_ptr(),
+        positions.data_ptr(), _ptr(status), _stream(stream, lengths))
+    if rc != SMD_OK:
+        raise SmdError(rc, "smd_block_tables")
+    return new_lengths, new_state, starts, slots, positions
+
+
+def paged_append(cache: PagedCache, k, v, slots, stream=None) -> None:
+    """Writes new keys and values into the cache (smd_paged_append). k, v
+    [T, heads, head_dim] bfloat16 CUDA tensors whose tokens may lie apart
+    (slices of a fused projection); slots [T] int32."""
+    import torch
+
+    _vector(slots, "slots", torch.int32)
+    T = slots.numel()
+    for name, t in (("k", k), ("v", v)):
+        if not t.is_cuda or t.dtype != torch.bfloat16 or tuple(t.shape) != (
+                T, cache.heads, cache.head_dim):
+            raise ValueError(f"{name} must be a bfloat16 CUDA tensor "
+                             f"[{T}, {cache.heads}, {cache.head_dim}]")
+        if t.stride(2) != 1 or (cache.heads > 1 and t.stride(1) != cache.head_dim):
+            raise ValueError(f"{name}: a token's heads must be contiguous")
+    row = cache.heads * cache.head_dim
+    rc = lib().smd_paged_append(cache.ref, k.data_ptr(), k.stride(0) if T > 1 else row, v.data_ptr(),
+                                v.stride(0) if T > 1 else row, slots.data_ptr(), T,
+                                _stream(stream, slots))
+    if rc != SMD_OK:
+        raise SmdError(rc, "smd_paged_append")
+
+
+def _paged_rows(q, cache, table, lengths, row_group):
+    import torch
+
+    R = lengths.numel()
+    _vector(lengths, "lengths", torch.int32)
+    if not q.is_cuda or q.dtype != torch.bfloat16 or q.dim() != 3 or q.shape[0] != R * row_group \
+            or q.shape[2] != cache.head_dim:
+        raise ValueError(f"q must be a bfloat16 CUDA tensor [{R} * {row_group}, Hq, {cache.head_dim}]")
+    if q.stride(2) != 1 or (q.shape[1] > 1 and q.stride(1) != cache.head_dim):
+        raise ValueError("q: a row's heads must be contiguous")
+    if not table.is_cuda or table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] < R \
+            or table.stride(1) != 1:
+        raise ValueError("table must be an int32 CUDA tensor [>= R, width] with contiguous rows")
+    width = table.shape[1]
+    return (q.data_ptr(), q.stride(0) if q.shape[0] > 1 else q.shape[1] * q.shape[2], cache.ref,
+            table.data_ptr(), table.stride(0) if table.shape[0] > 1 else width, width,
+            lengths.data_ptr(), R, row_group, q.shape[1])
+
+
+def block_scores(q, cache: PagedCache, table, lengths, row_group: int = 1, keep_first: int = 0,
+                 keep_last: int = 0, out=None, stream=None):
+    """The score of each page for each row and kv head (smd_block_scores): an
+    upper bound of q . k over the page's keys, the largest over the kv head's
+    query heads. q [R * row_group, Hq, head_dim] bfloat16, table [R, width] and
+    lengths [R] int32. Returns bfloat16 [R * row_group, heads, width], NaN past
+    the pages a row sees; ``scores.flatten(0, 1)`` goes to topk_select."""
+    import torch
+
+    args = _paged_rows(q, cache, table, lengths, row_group)
+    B, width = q.shape[0], table.shape[1]
+    if out is None:  # rows of a multiple of 8 scores: topk_select reads them in 16-byte pieces
+        out = torch.empty((B, cache.heads, (width + 7) // 8 * 8), dtype=torch.bfloat16,
+                          device=q.device)[:, :, :width]
+    if not out.is_cuda or out.dtype != torch.bfloat16 or tuple(out.shape) != (B, cache.heads, width) \
+            or out.stride(2) != 1 or (B > 1 and out.stride(0) != cache.heads * out.stride(1)):
+        raise ValueError(f"out must be a bfloat16 CUDA tensor [{B}, {cache.heads}, {width}] with "
+                         "evenly spaced rows")
+    stride = out.stride(1) if cache.heads > 1 else out.stride(0) if B > 1 else width
+    rc = lib().smd_block_scores(*args, keep_first, keep_last, out.data_ptr(), stride,
+                                _stream(stream, q))
+    if rc != SMD_OK:
+        raise SmdError(rc, "smd_block_scores")
+    return out
+
+
+def paged_workspace_bytes(cache: PagedCache) -> int:
+    """Bytes of workspace paged_decode needs for this cache, whatever the batch."""
+    n = int(lib().smd_paged_workspace_bytes(cache.ref))
+    if n < 0:
+        raise SmdError(n, "smd_paged_workspace_bytes")
+    return n
+
+
+def paged_decode(q, cache: PagedCache, table, lengths, sm_scale: float, row_group: int = 1,
+                 block_lists=None, block_counts=None, out=None, lse=None, status=None,
+                 workspace=None, stream=None):
+    """Attention over the cache (smd_paged_decode). q [R * row_group, Hq,
+    head_dim] bfloat16 (rows may lie apart), table [R, width] and lengths [R]
+    int32; block_lists [R * row_group, heads, K] int32: the pages of its request
+    that each row and kv head attends (topk_select's output on block_scores),
+    the first block_counts [R * row_group, heads] of them; None: all of its
+    tokens. ``workspace``: a CUDA tensor of paged_workspace_bytes(cache) bytes
+    (allocated here if None). Returns (out [R * row_group, Hq, head_dim]
+    bfloat16, lse [R * row_group, Hq] float32)."""
+    import torch
+
+    args = _paged_rows(q, cache, table, lengths, row_group)
+    B, Hq = q.shape[0], q.shape[1]
+    K = 0
+    if block_lists is not None:
+        _vector(block_lists, "block_lists", torch.int32)
+        if block_lists.dim() != 3 or tuple(block_lists.shape[:2]) != (B, cache.heads):
+            raise ValueError(f"block_lists must be [{B}, {cache.heads}, K]")
+        K = block_lists.shape[2]
+        if block_counts is not None:
+            _vector(block_counts, "block_counts", torch.int32, B * cache.heads)
+    elif block_counts is not None:
+        raise ValueError("block_counts without block_lists")
+    if out is None:
+        out = torch.empty((B, Hq, cache.head_dim), dtype=torch.bfloat16, device=q.device)
+    elif tuple(out.shape) != (B, Hq, cache.head_dim):
+        raise ValueError(f"out must be [{B}, {Hq}, {cache.head_dim}]")
+    _vector(out, "out", torch.bfloat16)
+    if lse is None:
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+    _vector(lse, "lse", torch.float32, B * Hq)
+    if workspace is None:
+        workspace = torch.empty(paged_workspace_bytes(cache), dtype=torch.uint8, device=q.device)
+    elif not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    rc = lib().smd_paged_decode(
+        *args, sm_scale, _ptr(block_lists) if K or block_lists is None else workspace.data_ptr(),
+        _ptr(block_counts), K, out.data_ptr(), lse.data_ptr(),
+        _ptr(status), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        _stream(stream, q))
+    if rc != SMD_OK:
+        raise SmdError(rc, "smd_paged_decode")
+    return out, lse

@@ -906,6 +906,8 @@ const char* smd_status_str(int status) {
             return "rows of a group do not share their index list (device status)";
         case SMD_ERR_INDEX:
             return "a valid entry of the index list lies outside [0, N) (device status)";
+        case SMD_ERR_PAGES:
+            return "a request was refused for want of pages, table width or slots (device status)";
         default:
             return "unknown status";
     }
