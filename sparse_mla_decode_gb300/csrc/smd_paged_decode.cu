@@ -9,12 +9,14 @@
 // 4 D M FLOPs done with them, 2 M FLOPs a byte: HBM for the M <= 32 of decode
 // rows. So the kernel is built to keep copies in flight, and the products go
 // to mma.sync m16n8k16 with f16 operands: E4M3 codes convert to f16 exactly,
-// and M = 8 or 16 rows would leave most of a 128-lane tcgen05 tile empty.
+// and 8 or 16 rows would leave most of a 128-lane tcgen05 tile empty. Tokens (for
+// the logits) and columns (for the output) are the MMA's 16 rows, query rows
+// its 8 columns, so that 8 query heads fill it.
 //
 // A warp is a worker of its own: it walks tiles of KT tokens of one (page,
 // head) through a ring of ST slots that its own lanes fill with tensor copies
 // (K and V of a tile: one barrier), and holds the tile's softmax state and its
-// M x D accumulators in registers. No CTA barrier is passed until the tokens
+// D x M accumulators in registers. No CTA barrier is passed until the tokens
 // of a unit (a request's kv head) end, where the CTA's warps join their
 // states through shared memory (the slots they have just consumed).
 //
@@ -27,19 +29,23 @@
 // of token g, columns 16 c + 4 i ..; the contraction index of the MMA is
 // permuted to take them as they are (slots 2i, 2i+1, 2i+8, 2i+9 are columns 4i
 // .. 4i+3), and the query fragments are read in the same order. V comes by
-// transposing ldmatrix as two codes each of tokens 2i and 2i+1; one byte
-// permute pairs the tokens, and the even and odd columns of a 16-column chunk
-// go to two MMAs, whose results leave a lane 4 consecutive columns.
+// transposing ldmatrix as codes 16 c + 2 g and + 1 of tokens 2i and 2i+1; one
+// byte permute pairs the tokens, and MMA rows g and g + 8 are those two columns.
+// The weights leave the first product with a token a lane and enter the second
+// with a query row a lane: movmatrix transposes their 8 x 8 blocks.
 //
 // Rounding: q enters as f16 after a power of two per row that puts its largest
 // element in [2^14, 2^15) (bf16 has fewer bits than f16, so this is exact down
-// to 2^-30 of the largest); the weights enter as f16 at 2^14 of the running
-// maximum, 11 bits, below the 8 of the bf16 output; their sum is of the fp32
-// weights; accumulators, maxima and sums are fp32. V's scale multiplies the
-// weights relative to the largest scale met so far (exact for powers of two),
-// so f16 never sees its range.
+// to 2^-30 of the largest); the weights enter as f16, 11 bits, below the 8 of
+// the bf16 output, relative to a maximum that is moved only when it has grown
+// by more than 2^8 (so at 2^7 to 2^15); their sum is of the fp32 weights;
+// accumulators, maxima and sums are fp32. V's scale multiplies the weights
+// relative to the largest scale met so far (exact for powers of two), so f16
+// never sees its range.
 #include <atomic>
 #include <cstring>
+#include <cstdlib>
+#include <cstdlib>
 
 #include "smd_internal.h"
 #include "smd_paged.h"
@@ -52,8 +58,10 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxEntries = 1024;  // requests (or (row, kv head) lists) of one launch
 constexpr int kNoPos = 0x3fffffff; // the position of tokens that no row sees
-constexpr float kPShift = 14.0f;   // weights are formed at 2^14 of the maximum
+constexpr float kPShift = 7.0f;    // weights are formed at 2^7 of the maximum kept
+constexpr float kSlack = 8.0f;     // which is moved when a logit exceeds it by 2^8
 constexpr int kJoinRows = 4;       // rows of a unit that a CTA of the join takes
+constexpr int kUnitCost = 8;       // what ending a unit costs a CTA, in tiles
 
 struct PagedParams {
     const uint16_t* q;
@@ -133,6 +141,10 @@ __device__ __forceinline__ void lds64(uint32_t addr, uint32_t& a, uint32_t& b) {
     asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(a), "=r"(b) : "r"(addr) : "memory");
 }
 
+__device__ __forceinline__ void sts64(uint32_t addr, uint32_t a, uint32_t b) {
+    asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
+}
+
 __device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
     asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
@@ -146,18 +158,28 @@ __device__ __forceinline__ float4 lds_f4(uint32_t addr) {
     return v;
 }
 
-// The sizes of one instantiation: D columns, MT tiles of 16 query rows, KT
-// tokens a tile, ST slots of a warp's ring.
-template <int D, int MT, int KT, int ST>
+// Transposes the 8 x 8 block of 16-bit elements whose row g holds its elements
+// 2i, 2i + 1 in lane 4 g + i.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
+// The sizes of one instantiation: D columns, RT tiles of 8 query rows, KT
+// tokens a tile, ST slots of a warp's ring, CTAs an SM holds.
+template <int D_, int RT_, int KT_, int ST_, int CTAS_>
 struct Shape {
-    static constexpr int rows = 16 * MT;
+    static constexpr int D = D_, RT = RT_, KT = KT_, ST = ST_, CTAS = CTAS_;
+    static constexpr int rows = 8 * RT;
     static constexpr int row_bytes = D < 128 ? D : 128;  // of a copy box
     static constexpr int side = KT * D;                  // bytes of a tile's K, and of its V
     static constexpr int slot = 2 * side;
     static constexpr int q_pitch = 2 * D + 32;           // 8-byte reads of 4 rows hit 4 bank groups
     static constexpr int off_q = kWarps * ST * slot;
     static constexpr int off_qf = off_q + rows * q_pitch;         // [rows] logit factors
-    static constexpr int off_ml = off_qf + rows * 4;              // [warps][rows] maximum, sum
+    static constexpr int off_lim = off_qf + rows * 4;             // [rows] tokens that a row sees
+    static constexpr int off_ml = off_lim + rows * 4;             // [warps][rows] maximum, sum
     static constexpr int off_meta = off_ml + kWarps * rows * 8;   // [warps][ST][8] words
     static constexpr int off_bar = off_meta + kWarps * ST * 32;
     static constexpr int off_scan = off_bar + kWarps * ST * 8;    // [warps + 1] words
@@ -195,15 +217,14 @@ struct Tile {
     float ks[NH], vs[NH];
 };
 
-template <int D, int MT, int KT, int ST>
-__global__ void __launch_bounds__(kThreads, (D == 256 || (D == 128 && MT == 2)) ? 2 : 3)
+template <typename S>
+__global__ void __launch_bounds__(kThreads, S::CTAS)
     paged_decode_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
                         const __grid_constant__ CUtensorMap vmap) {
-    using S = Shape<D, MT, KT, ST>;
-    constexpr int NT = KT / 8;    // key tiles of an MMA
-    constexpr int NH = KT / 16;   // k-steps of the second product
+    constexpr int D = S::D, RT = S::RT, KT = S::KT, ST = S::ST;
+    constexpr int NH = KT / 16;   // 16-token halves of a tile
     constexpr int NC = D / 16;    // 16-column chunks
-    constexpr bool kQRegs = MT == 1 && D <= 128;  // query fragments stay in registers
+    constexpr bool kQRegs = RT * D <= 256;  // query fragments stay in registers
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
     uint8_t* const gbase = smem_raw + (base - smem_addr(smem_raw));
@@ -211,10 +232,10 @@ __global__ void __launch_bounds__(kThreads, (D == 256 || (D == 128 && MT == 2)) 
     int32_t* const prefix = reinterpret_cast<int32_t*>(gbase + S::off_prefix);
     float2* const ml = reinterpret_cast<float2*>(gbase + S::off_ml);
     float* const qf = reinterpret_cast<float*>(gbase + S::off_qf);
+    int32_t* const lims = reinterpret_cast<int32_t*>(gbase + S::off_lim);
     const uint32_t ring = base + warp * ST * S::slot;
     const uint32_t bars = base + S::off_bar + warp * ST * 8;
-    volatile uint32_t* const meta =
-        reinterpret_cast<uint32_t*>(gbase + S::off_meta) + warp * ST * 8;
+    const uint32_t meta = base + S::off_meta + warp * ST * 32;  // ks, vs, pos of each half
 
     if (lane == 0) {
         for (int s = 0; s < ST; ++s) mbar_init(bars + 8 * s, 1);
@@ -260,23 +281,34 @@ __global__ void __launch_bounds__(kThreads, (D == 256 || (D == 128 && MT == 2)) 
     }
     __syncthreads();
 
-    const int grid = static_cast<int>(gridDim.x);
-    const int per = max((total + grid - 1) / grid, kWarps);
-    const int t0 = min(static_cast<int>(blockIdx.x) * per, total), t1 = min(t0 + per, total);
-    if (tid == 0) {
-        p.desc[2 * blockIdx.x] = -1;
-    }
-    if (t0 >= t1) return;
-
-    const auto find_entry = [&](int t) {  // the entry of tile t (< total)
-        int lo = 0, hi = p.entries;       // prefix[lo] <= t < prefix[hi]
+    // The grid is cut evenly by cost: each unit counts kUnitCost besides its tiles, laid
+    // before them, so unit u of the batch starts its tiles kUnitCost (u + 1) further on.
+    const auto find = [&](int t, int unit_cost) {  // the entry at t (below the last one's end)
+        int lo = 0, hi = p.entries;
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if (prefix[mid] <= t) lo = mid;
+            if (prefix[mid] + unit_cost * p.x_units * mid <= t) lo = mid;
             else hi = mid;
         }
         return lo;
     };
+    const auto find_entry = [&](int t) { return find(t, 0); };
+    const int cost = total + kUnitCost * p.x_units * p.entries;
+    const int grid = static_cast<int>(gridDim.x);
+    const int per = max((cost + grid - 1) / grid, kWarps + kUnitCost);
+    const auto tiles_before = [&](int64_t at) {  // tiles that lie before a cost position
+        if (at >= cost) return total;
+        const int c = static_cast<int>(at), e = find(c, kUnitCost);
+        const int nt = (prefix[e + 1] - prefix[e]) / p.x_units;
+        const int rem = c - prefix[e] - kUnitCost * p.x_units * e, x = rem / (nt + kUnitCost);
+        return prefix[e] + x * nt + max(rem - x * (nt + kUnitCost) - kUnitCost, 0);
+    };
+    const int64_t at0 = static_cast<int64_t>(blockIdx.x) * per;
+    const int t0 = tiles_before(at0), t1 = tiles_before(at0 + per);
+    if (tid == 0) {
+        p.desc[2 * blockIdx.x] = -1;
+    }
+    if (t0 >= t1) return;
 
     // Lane l resolves tile 32 * (k / 32) + l of this warp's tiles.
     Tile<NH> td;
@@ -288,7 +320,8 @@ __global__ void __launch_bounds__(kThreads, (D == 256 || (D == 128 && MT == 2)) 
             td.page[h] = -1;
             td.off[h] = 0;
             td.pos[h] = kNoPos;
-            td.ks[h] = td.vs[h] = 0.0f;
+            td.ks[h] = 1.0f;
+            td.vs[h] = 0.0f;
         }
         td.head = 0;
         if (t >= t1) return;
@@ -322,14 +355,13 @@ __global__ void __launch_bounds__(kThreads, (D == 256 || (D == 128 && MT == 2)) 
     const auto issue = [&](int kk) {
         if (kk >= my_tiles) return;
         if ((kk & 31) == 0) resolve(kk + lane);
-        fence_proxy_async();
-        __syncwarp();
         if (lane == (kk & 31)) {
             const int s = kk % ST;
             const uint32_t bar = bars + 8 * s, dst = ring + s * S::slot;
             mbar_arrive_expect_tx(bar, S::slot);
-            const int step = p.box == 16 ? 1 : NH;
-            for (int h = 0; h < NH; h += step) {
+#pragma unroll
+            for (int h = 0; h < NH; ++h) {
+                if (h > 0 && p.box != 16) break;
 #pragma unroll
                 for (int sub = 0; sub < (D > 128 ? 2 : 1); ++sub) {
                     const uint32_t at = dst + sub * KT * 128 + h * 16 * S::row_bytes;
@@ -338,12 +370,8 @@ __global__ void __launch_bounds__(kThreads, (D == 256 || (D == 128 && MT == 2)) 
                                 bar);
                 }
             }
-#pragma unroll
-            for (int h = 0; h < NH; ++h) {
-                meta[8 * s + 3 * h] = __float_as_uint(td.ks[h]);
-                meta[8 * s + 3 * h + 1] = __float_as_uint(td.vs[h]);
-                meta[8 * s + 3 * h + 2] = static_cast<uint32_t>(td.pos[h]);
-            }
+            sts_v4(meta + 32 * s, make_float4(td.ks[0], td.ks[NH - 1], td.vs[0], td.vs[NH - 1]));
+            sts64(meta + 32 * s + 16, td.pos[0], td.pos[NH - 1]);
         }
         __syncwarp();
     };
@@ -353,9 +381,12 @@ __global__ void __launch_bounds__(kThreads, (D == 256 || (D == 128 && MT == 2)) 
         const int i = p.lists != nullptr ? b % p.G : m / p.g;
         return max(len - p.G + 1 + i, 0);
     };
-    // The unit's queries as f16 in shared memory, with each row's logit factor.
+    // The unit's queries as f16 in shared memory, with each row's logit factor
+    // (positive: a negative softmax scale turns the query's sign) and limit.
     const auto load_q = [&](int e, int x) {
-        const int rt = x % p.row_tiles;
+        const int rt = x % p.row_tiles, u_b = p.lists != nullptr ? e / p.heads : e * p.G;
+        const int u_len =
+            max(min(p.lengths[p.lists != nullptr ? u_b / p.G : e], p.width * p.page_size), 0);
         const int head = p.lists != nullptr ? e % p.heads : x / p.row_tiles;
         constexpr int kPieces = D / 8;
         for (int idx = tid; idx < S::rows * kPieces; idx += kThreads) {
@@ -381,13 +412,17 @@ __global__ void __launch_bounds__(kThreads, (D == 256 || (D == 128 && MT == 2)) 
             // up = 2^(14 - exponent of a), within what a float holds
             const int ex = static_cast<int>(__float_as_uint(a) >> 23);
             const int ue = min(14 + 127 - ex + 127, 253);
-            const float up = a > 0.0f && ex < 255 ? __uint_as_float(static_cast<uint32_t>(ue) << 23) : 1.0f;
+            float up = a > 0.0f && ex < 255 ? __uint_as_float(static_cast<uint32_t>(ue) << 23) : 1.0f;
+            if (c == 0) {
+                qf[m] = fabsf(p.scale_log2) / up;
+                lims[m] = mm < p.rows ? row_limit(mm, u_b, u_len) : 0;
+            }
+            if (p.scale_log2 < 0.0f) up = -up;
             const uint32_t at = base + S::off_q + m * S::q_pitch + 16 * c;
             asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at),
                          "r"(f16x2(f[0] * up, f[1] * up)), "r"(f16x2(f[2] * up, f[3] * up)),
                          "r"(f16x2(f[4] * up, f[5] * up)), "r"(f16x2(f[6] * up, f[7] * up))
                          : "memory");
-            if (c == 0) qf[m] = p.scale_log2 / up;
         }
     };
 
@@ -407,37 +442,30 @@ __global__ void __launch_bounds__(kThreads, (D == 256 || (D == 128 && MT == 2)) 
         const int nt = (prefix[e + 1] - prefix[e]) / p.x_units, x = (t - prefix[e]) / nt;
         const int u0 = prefix[e] + x * nt, u1 = u0 + nt, tend = min(u1, t1);
         const int rt = x % p.row_tiles, b0 = p.lists != nullptr ? e / p.heads : e * p.G;
-        const int r = p.lists != nullptr ? b0 / p.G : e;
-        const int len = max(min(p.lengths[r], p.width * p.page_size), 0);
         const int m_real = min(p.rows - rt * S::rows, S::rows);
-        const int min_lim = row_limit(rt * S::rows, b0, len);
-        const int max_lim = row_limit(rt * S::rows + m_real - 1, b0, len);
-        int lim[MT][2];
-        float fac[MT][2], m[MT][2], l[MT][2], o[MT][NC][2][4], vref = 0.0f;
-        uint32_t qa[kQRegs ? NC : 1][4];
+        const int min_lim = lims[0], max_lim = lims[m_real - 1];
+        float m[RT][2], l[RT][2], o[RT][NC][4], vref = 0.0f;
+        uint32_t qb[kQRegs ? RT : 1][kQRegs ? NC : 1][2];
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
+        for (int n = 0; n < RT; ++n)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int row = 16 * i + 8 * j + qr;
-                lim[i][j] = row_limit(rt * S::rows + min(row, m_real - 1), b0, len);
-                fac[i][j] = qf[row];
-                m[i][j] = -INFINITY;
-                l[i][j] = 0.0f;
+            for (int y = 0; y < 2; ++y) {
+                m[n][y] = -INFINITY;
+                l[n][y] = 0.0f;
             }
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
+        for (int n = 0; n < RT; ++n)
 #pragma unroll
             for (int c = 0; c < NC; ++c)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) o[i][c][j >> 2][j & 3] = 0.0f;
+                for (int j = 0; j < 4; ++j) o[n][c][j] = 0.0f;
         const uint32_t q_at = base + S::off_q + qr * S::q_pitch + 8 * qi;
         if (kQRegs) {
 #pragma unroll
-            for (int c = 0; c < (kQRegs ? NC : 0); ++c) {
-                lds64(q_at + 32 * c, qa[c][0], qa[c][2]);
-                lds64(q_at + 8 * S::q_pitch + 32 * c, qa[c][1], qa[c][3]);
-            }
+            for (int n = 0; n < (kQRegs ? RT : 0); ++n)
+#pragma unroll
+                for (int c = 0; c < NC; ++c)
+                    lds64(q_at + n * 8 * S::q_pitch + 32 * c, qb[n][c][0], qb[n][c][1]);
         }
 
 #pragma unroll 1
@@ -447,71 +475,64 @@ __global__ void __launch_bounds__(kThreads, (D == 256 || (D == 128 && MT == 2)) 
             mbar_wait(bars + 8 * slot, (k / ST) & 1, ok, p.status, kWaitBudgetNs);
             const uint32_t ks_at = ring + slot * S::slot, vs_at = ks_at + S::side;
 
-            // logits
-            float s[MT][NT][4];
+            // logits: token 16 h + g (+ 8 for j >= 2), query row 8 n + 2 i + (j & 1)
+            float s[NH][RT][4];
 #pragma unroll
-            for (int i = 0; i < MT; ++i)
+            for (int h = 0; h < NH; ++h)
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                for (int n = 0; n < RT; ++n)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) s[i][n][j] = 0.0f;
+                    for (int j = 0; j < 4; ++j) s[h][n][j] = 0.0f;
 #pragma unroll
-            for (int c0 = 0; c0 < NC; c0 += 4 / NT) {
+            for (int c0 = 0; c0 < NC; c0 += 2 / NH) {
                 uint32_t kr[4];
-                const int row = lane % KT, cc = c0 + lane / KT;
-                ldsm4(ks_at + piece<D, KT>(row, cc), kr);
+                ldsm4(ks_at + piece<D, KT>(lane % KT, c0 + lane / KT), kr);
+                uint32_t a[2][4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int c = c0 + j / NT, n = j % NT;
+                for (int z = 0; z < 2; ++z) {
+                    e4m3_to_f16(kr[2 * z], a[z][0], a[z][2]);
+                    e4m3_to_f16(kr[2 * z + 1], a[z][1], a[z][3]);
+                }
+#pragma unroll
+                for (int n = 0; n < RT; ++n) {
                     uint32_t b0v, b1v;
-                    e4m3_to_f16(kr[j], b0v, b1v);
 #pragma unroll
-                    for (int i = 0; i < MT; ++i) {
-                        uint32_t a[4];
+                    for (int z = 0; z < 2; ++z) {
+                        const int h = z % NH, c = c0 + z / NH;
                         if (kQRegs) {
-#pragma unroll
-                            for (int z = 0; z < 4; ++z) a[z] = qa[kQRegs ? c : 0][z];
-                        } else {
-                            lds64(q_at + i * 16 * S::q_pitch + 32 * c, a[0], a[2]);
-                            lds64(q_at + (i * 16 + 8) * S::q_pitch + 32 * c, a[1], a[3]);
+                            b0v = qb[kQRegs ? n : 0][kQRegs ? c : 0][0];
+                            b1v = qb[kQRegs ? n : 0][kQRegs ? c : 0][1];
+                        } else if (z == 0 || NH == 1) {
+                            lds64(q_at + n * 8 * S::q_pitch + 32 * c, b0v, b1v);
                         }
-                        mma_f16(s[i][n], a[0], a[1], a[2], a[3], b0v, b1v);
+                        mma_f16(s[h][n], a[z][0], a[z][1], a[z][2], a[z][3], b0v, b1v);
                     }
                 }
             }
 
-            // scale, mask
-            float ks[NH], vs[NH];
-            int pos[NH];
+            const float4 sc = lds_f4(meta + 32 * slot);
+            const float ks[2] = {sc.x, sc.y}, vs[2] = {sc.z, sc.w};
+            uint32_t up0, up1;
+            lds64(meta + 32 * slot + 16, up0, up1);
+            const int pos[2] = {static_cast<int>(up0), static_cast<int>(up1)};
+            if (max(pos[0], pos[1]) + 15 >= min_lim) {
+                // Tokens that a row does not see.
 #pragma unroll
-            for (int h = 0; h < NH; ++h) {
-                ks[h] = __uint_as_float(meta[8 * slot + 3 * h]);
-                vs[h] = __uint_as_float(meta[8 * slot + 3 * h + 1]);
-                pos[h] = static_cast<int>(meta[8 * slot + 3 * h + 2]);
-            }
+                for (int n = 0; n < RT; ++n)
 #pragma unroll
-            for (int i = 0; i < MT; ++i)
+                    for (int y = 0; y < 2; ++y) {
+                        const int lim = lims[8 * n + 2 * qi + y];
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                        for (int h = 0; h < NH; ++h)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) s[i][n][j] *= fac[i][j >> 1] * ks[n >> 1];
-            bool tail = false;
-#pragma unroll
-            for (int h = 0; h < NH; ++h) tail = tail || pos[h] + 15 >= min_lim;
-            if (tail) {
-#pragma unroll
-                for (int i = 0; i < MT; ++i)
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            if (pos[n >> 1] + 8 * (n & 1) + 2 * qi + (j & 1) >= lim[i][j >> 1])
-                                s[i][n][j] = -INFINITY;
+                            for (int z = 0; z < 2; ++z)
+                                if (pos[h] + qr + 8 * z >= lim) s[h][n][2 * z + y] = -INFINITY;
+                    }
                 // V of tokens that no row sees becomes 0 (0 times a NaN would not be).
-#pragma unroll
+#pragma unroll 1
                 for (int z = lane; z < KT * NC; z += 32) {
                     const int j = z / NC;
-                    if (pos[NH == 1 ? 0 : j >> 4] + (j & 15) >= max_lim)
+                    if ((j < 16 ? pos[0] : pos[1]) + (j & 15) >= max_lim)
                         sts_zero16(vs_at + piece<D, KT>(j, z % NC));
                 }
                 // V of tokens that some rows see and others do not: a NaN goes to the rows
@@ -519,57 +540,72 @@ __global__ void __launch_bounds__(kThreads, (D == 256 || (D == 128 && MT == 2)) 
                 if (min_lim < max_lim) {
 #pragma unroll 1
                     for (int j = 0; j < KT; ++j) {
-                        const int at = pos[NH == 1 ? 0 : j >> 4] + (j & 15);
+                        const int at = (j < 16 ? pos[0] : pos[1]) + (j & 15);
                         if (at < min_lim || at >= max_lim) continue;
+                        bool nan = false;
+#pragma unroll 1
+                        for (int z = lane; z < 4 * NC; z += 32) {
+                            const uint32_t w = lds_u32(vs_at + piece<D, KT>(j, z >> 2) + 4 * (z & 3));
+                            nan = nan || (((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0;
+                        }
+                        if (!__any_sync(0xffffffffu, nan)) continue;
 #pragma unroll
                         for (int c = 0; c < NC; ++c) {
-                            const uint32_t a = vs_at + piece<D, KT>(j, c) + 4 * qi;
+                            const uint32_t a = vs_at + piece<D, KT>(j, c) + 4 * (qr >> 1);
                             const uint32_t w = lds_u32(a);
-                            uint32_t nan = 0;
 #pragma unroll
-                            for (int z = 0; z < 4; ++z)
-                                if (((w >> (8 * z)) & 0x7fu) == 0x7fu) {
-                                    nan |= 0xffu << (8 * z);
+                            for (int z = 0; z < 2; ++z)
+                                if (((w >> (16 * (qr & 1) + 8 * z)) & 0x7fu) == 0x7fu)
 #pragma unroll
-                                    for (int i = 0; i < MT; ++i)
+                                    for (int n = 0; n < RT; ++n)
 #pragma unroll
                                         for (int y = 0; y < 2; ++y)
-                                            if (at < lim[i][y])
-                                                o[i][c][z & 1][2 * y + (z >> 1)] = NAN;
-                                }
+                                            if (at < lims[8 * n + 2 * qi + y])
+                                                o[n][c][2 * z + y] = NAN;
+                            const uint32_t bad = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
                             __syncwarp();
-                            if (nan != 0 && qr == 0) sts32(a, w & ~nan);
+                            if ((lane & 7) == 0) sts32(a, w & ~((bad >> 7) * 0xffu));
                         }
                     }
                 }
+                fence_proxy_async();  // before the slot is copied into again
                 __syncwarp();
             }
 
-            // the running maximum
+            // The maximum stays while no logit exceeds it by more than kSlack.
+            float f[NH][RT][2], v[RT][2];
+            bool moved = false;
 #pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                float alpha[2];
-                bool moved = false;
+            for (int n = 0; n < RT; ++n)
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
-                    float v = m[i][y];
+                    const float fac = qf[8 * n + 2 * qi + y];
+                    v[n][y] = -INFINITY;
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
-                        v = fmaxf(v, fmaxf(s[i][n][2 * y], s[i][n][2 * y + 1]));
-                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-                    alpha[y] = v > m[i][y] ? ex2_approx(m[i][y] - v) : 1.0f;
-                    moved = moved || v > m[i][y];
-                    m[i][y] = v;
+                    for (int h = 0; h < NH; ++h) {
+                        f[h][n][y] = fmaxf(fac * ks[h], 1.17549435e-38f);
+                        v[n][y] = fmaxf(v[n][y], fmaxf(s[h][n][y], s[h][n][2 + y]) * f[h][n][y]);
+                    }
+                    moved = moved || v[n][y] > m[n][y] + kSlack;
                 }
-                if (__any_sync(0xffffffffu, moved)) {
-                    l[i][0] *= alpha[0];
-                    l[i][1] *= alpha[1];
+            if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-                    for (int c = 0; c < NC; ++c)
+                for (int n = 0; n < RT; ++n)
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) o[i][c][j >> 2][j & 3] *= alpha[(j >> 1) & 1];
-                }
+                    for (int y = 0; y < 2; ++y) {
+                        float top = fmaxf(m[n][y], v[n][y]);
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                        const float alpha = top > m[n][y] ? ex2_approx(m[n][y] - top) : 1.0f;
+                        m[n][y] = top;
+                        l[n][y] *= alpha;
+#pragma unroll
+                        for (int c = 0; c < NC; ++c) {
+                            o[n][c][y] *= alpha;
+                            o[n][c][2 + y] *= alpha;
+                        }
+                    }
             }
 
             // weights and the second product
@@ -579,33 +615,29 @@ __global__ void __launch_bounds__(kThreads, (D == 256 || (D == 128 && MT == 2)) 
                     const float down = vref / vs[h];
                     vref = vs[h];
 #pragma unroll
-                    for (int i = 0; i < MT; ++i)
+                    for (int n = 0; n < RT; ++n)
 #pragma unroll
                         for (int c = 0; c < NC; ++c)
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) o[i][c][j >> 2][j & 3] *= down;
+                            for (int j = 0; j < 4; ++j) o[n][c][j] *= down;
                 }
                 const float ratio = vref > 0.0f ? vs[h] / vref : 0.0f;
-                uint32_t pa[MT][4];
+                uint32_t pb[RT][2];
 #pragma unroll
-                for (int i = 0; i < MT; ++i) {
-                    float w[2][4];
+                for (int n = 0; n < RT; ++n) {
+                    float w[4];
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
-                        const float top = m[i][y] == -INFINITY ? 0.0f : m[i][y] - kPShift;
+                        const float top = m[n][y] == -INFINITY ? 0.0f : m[n][y] - kPShift;
 #pragma unroll
-                        for (int n = 0; n < 2; ++n)
-#pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                const float pv = ex2_approx(s[i][2 * h + n][2 * y + j] - top);
-                                l[i][y] += pv;
-                                w[n][2 * y + j] = pv * ratio;
-                            }
+                        for (int z = 0; z < 2; ++z) {
+                            const float pv = ex2_approx(fmaf(s[h][n][2 * z + y], f[h][n][y], -top));
+                            l[n][y] += pv;
+                            w[2 * z + y] = pv * ratio;
+                        }
                     }
-                    pa[i][0] = f16x2(w[0][0], w[0][1]);
-                    pa[i][1] = f16x2(w[0][2], w[0][3]);
-                    pa[i][2] = f16x2(w[1][0], w[1][1]);
-                    pa[i][3] = f16x2(w[1][2], w[1][3]);
+                    pb[n][0] = transpose8x8(f16x2(w[0], w[1]));
+                    pb[n][1] = transpose8x8(f16x2(w[2], w[3]));
                 }
 #pragma unroll
                 for (int c = 0; c < NC; c += 2) {
@@ -613,14 +645,12 @@ __global__ void __launch_bounds__(kThreads, (D == 256 || (D == 128 && MT == 2)) 
                     ldsm4_t(vs_at + piece<D, KT>(16 * h + (lane & 15), c + (lane >> 4)), vr);
 #pragma unroll
                     for (int z = 0; z < 2; ++z) {
-                        uint32_t e0, e1, o0, o1;
-                        e4m3_to_f16(__byte_perm(vr[2 * z], 0, 0x3120), e0, o0);
-                        e4m3_to_f16(__byte_perm(vr[2 * z + 1], 0, 0x3120), e1, o1);
+                        uint32_t a[4];
+                        e4m3_to_f16(__byte_perm(vr[2 * z], 0, 0x3120), a[0], a[1]);
+                        e4m3_to_f16(__byte_perm(vr[2 * z + 1], 0, 0x3120), a[2], a[3]);
 #pragma unroll
-                        for (int i = 0; i < MT; ++i) {
-                            mma_f16(o[i][c + z][0], pa[i][0], pa[i][1], pa[i][2], pa[i][3], e0, e1);
-                            mma_f16(o[i][c + z][1], pa[i][0], pa[i][1], pa[i][2], pa[i][3], o0, o1);
-                        }
+                        for (int n = 0; n < RT; ++n)
+                            mma_f16(o[n][c + z], a[0], a[1], a[2], a[3], pb[n][0], pb[n][1]);
                     }
                 }
             }
@@ -630,63 +660,65 @@ __global__ void __launch_bounds__(kThreads, (D == 256 || (D == 128 && MT == 2)) 
         // The warps' states become the CTA's. Warp w holds tiles of this unit if one of
         // its turns fell into [t, tend); the slot it consumed last takes its accumulators.
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
+        for (int n = 0; n < RT; ++n)
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
-                float v = l[i][y];
-                v += __shfl_xor_sync(0xffffffffu, v, 1);
-                v += __shfl_xor_sync(0xffffffffu, v, 2);
-                if (qi == 0) ml[warp * S::rows + 16 * i + 8 * y + qr] = make_float2(m[i][y], v);
+                float v = l[n][y];
+                v += __shfl_xor_sync(0xffffffffu, v, 4);
+                v += __shfl_xor_sync(0xffffffffu, v, 8);
+                v += __shfl_xor_sync(0xffffffffu, v, 16);
+                if (qr == 0) ml[warp * S::rows + 8 * n + 2 * qi + y] = make_float2(m[n][y], v);
             }
         __syncthreads();
         const bool mine = k > 0 && t0 + warp + kWarps * (k - 1) >= t;
-        float wgt[MT][2];
+        float wgt[RT][2];
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
+        for (int n = 0; n < RT; ++n)
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
                 float top = -INFINITY;
+#pragma unroll
                 for (int w = 0; w < kWarps; ++w)
-                    top = fmaxf(top, ml[w * S::rows + 16 * i + 8 * y + qr].x);
-                wgt[i][y] = m[i][y] == -INFINITY ? 0.0f : vref * ex2_approx(m[i][y] - top);
+                    top = fmaxf(top, ml[w * S::rows + 8 * n + 2 * qi + y].x);
+                wgt[n][y] = m[n][y] == -INFINITY ? 0.0f : vref * ex2_approx(m[n][y] - top);
             }
         const bool whole = u0 >= t0 && u1 <= t1;
         const int part_at = (2 * static_cast<int>(blockIdx.x) + (u0 >= t0 ? 1 : 0)) * S::rows;
         if (!whole && u0 >= t0 && tid == 0) {
             p.desc[2 * blockIdx.x] = e * p.x_units + x;
-            p.desc[2 * blockIdx.x + 1] = (u1 - 1) / per;
+            // the CTA that holds the unit's last tile
+            p.desc[2 * blockIdx.x + 1] = (u1 - 1 + kUnitCost * (e * p.x_units + x + 1)) / per;
         }
-        constexpr int kCols = S::slot / 64;  // columns of 16 rows that a slot holds in fp32
+        constexpr int kRound = RT < KT / 16 ? RT : KT / 16;  // row tiles that a slot holds in fp32
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-            for (int c0 = 0; c0 < D; c0 += kCols) {
+        for (int n0 = 0; n0 < RT; n0 += kRound) {
                 if (mine) {
                     const uint32_t buf = ring + ((k - 1) % ST) * S::slot;
 #pragma unroll
-                    for (int c = 0; c < kCols / 16; ++c) {
-                        const float(&v)[2][4] = o[i][c0 / 16 + c];
+                    for (int n = 0; n < kRound; ++n)
 #pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            const uint32_t unit = 4 * c + qi;
-                            const float w = wgt[i][y];
-                            float4 f = make_float4(v[0][2 * y] * w, v[1][2 * y] * w,
-                                                   v[0][2 * y + 1] * w, v[1][2 * y + 1] * w);
-                            sts_v4(buf + (8 * y + qr) * kCols * 4 + ((unit ^ ((qr & 1) << 2)) << 4), f);
+                        for (int c = 0; c < NC; ++c) {
+                            const float(&v)[4] = o[n0 + n][c];
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {
+                                const uint32_t unit = (4 * c + (qr >> 1)) ^ (qi << 1);
+                                const float w = wgt[n0 + n][y];
+                                sts64(buf + (8 * n + 2 * qi + y) * D * 4 + (unit << 4) + 8 * (qr & 1),
+                                      __float_as_uint(v[y] * w), __float_as_uint(v[2 + y] * w));
+                            }
                         }
-                    }
                     fence_proxy_async();
                 }
                 __syncthreads();
-                if (i == 0 && c0 == 0 && tend < t1) {
+                if (n0 == 0 && tend < t1) {
                     // The next unit's queries: every warp is past its tiles of this one.
                     int en = e;
                     while (prefix[en + 1] <= tend) ++en;
                     const int ntn = (prefix[en + 1] - prefix[en]) / p.x_units;
                     load_q(en, (tend - prefix[en]) / ntn);
                 }
-                for (int idx = tid; idx < 16 * (kCols / 4); idx += kThreads) {
-                    const int row = idx / (kCols / 4), unit = idx % (kCols / 4), mm = 16 * i + row;
+                for (int idx = tid; idx < 8 * kRound * (D / 4); idx += kThreads) {
+                    const int row = idx / (D / 4), unit = idx % (D / 4), mm = 8 * n0 + row;
                     if (mm >= m_real) continue;
                     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                     float top = -INFINITY, sum = 0.0f;
@@ -698,14 +730,14 @@ __global__ void __launch_bounds__(kThreads, (D == 256 || (D == 128 && MT == 2)) 
                         const float2 s = ml[w * S::rows + mm];
                         sum += s.y * (s.x == -INFINITY ? 0.0f : ex2_approx(s.x - top));  // a NaN stays one
                         const float4 f =
-                            lds_f4(base + (w * ST + last % ST) * S::slot + row * kCols * 4 +
-                                   ((unit ^ ((row & 1) << 2)) << 4));
+                            lds_f4(base + (w * ST + last % ST) * S::slot + row * D * 4 +
+                                   ((unit ^ (((row >> 1) & 3) << 1)) << 4));
                         acc.x += f.x;
                         acc.y += f.y;
                         acc.z += f.z;
                         acc.w += f.w;
                     }
-                    const int col = c0 + 4 * unit;
+                    const int col = 4 * unit;
                     if (whole) {
                         const int ma = rt * S::rows + mm;
                         const int b = p.lists != nullptr ? b0 : b0 + ma / p.g;
@@ -802,17 +834,17 @@ __global__ void __launch_bounds__(2 * kJoinRows * 32) paged_join_kernel(const Pa
 }
 
 constexpr int kMaxDevices = 64;
+constexpr int kWaves = 1;       // CTAs launched for each that an SM holds
+constexpr int kGridPerSm = 6;   // most CTAs for each SM (the workspace has room for them)
 
-template <int D, int MT, int KT, int ST>
+template <typename S>
 int launch_decode(PagedParams p, const CUtensorMap& kmap, const CUtensorMap& vmap, int sms,
                   int64_t tiles, smd_stream_t stream) {
-    using S = Shape<D, MT, KT, ST>;
-    constexpr int kResident = (D == 256 || (D == 128 && MT == 2)) ? 2 : 3;
-    static_assert(kResident * (S::smem(kMaxEntries) + 1024) <= 228 * 1024, "CTAs of an SM");
+    static_assert(S::CTAS * (S::smem(kMaxEntries) + 1024) <= 228 * 1024, "CTAs of an SM");
     static std::atomic<bool> ready[kMaxDevices];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return SMD_ERR_DEVICE;
-    auto kernel = paged_decode_kernel<D, MT, KT, ST>;
+    auto kernel = paged_decode_kernel<S>;
     if (!ready[dev]) {
         if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  S::smem(kMaxEntries)) != cudaSuccess) {
@@ -822,23 +854,26 @@ int launch_decode(PagedParams p, const CUtensorMap& kmap, const CUtensorMap& vma
         ready[dev] = true;
     }
     // At least kWarps tiles a CTA, so that each warp has one.
-    const int64_t most = static_cast<int64_t>(sms) * kResident, want = (tiles + kWarps - 1) / kWarps;
-    const int grid = static_cast<int>(want < most ? want : most);
+    const int64_t most = static_cast<int64_t>(sms) * kGridPerSm;
+    const int64_t want = (tiles + kWarps - 1) / kWarps;
+    const char* ev = getenv("SMD_W"); int64_t grid = static_cast<int64_t>(sms) * S::CTAS * (ev ? atoi(ev) : kWaves);
+    if (grid > most) grid = most;
+    if (grid > want) grid = want;
     p.part = reinterpret_cast<float*>(p.desc) + 4 * most;  // 16-byte aligned
-    p.part_ml = p.part + most * 2 * S::rows * D;
-    int rc = launch_pdl(kernel, dim3(grid), kThreads, S::smem(p.entries), stream, p, kmap, vmap);
+    p.part_ml = p.part + most * 2 * S::rows * S::D;
+    int rc = launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), kThreads, S::smem(p.entries),
+                        stream, p, kmap, vmap);
     if (rc != SMD_OK) return rc;
     const int join_rows = p.rows < S::rows ? p.rows : S::rows;
-    return launch_pdl(paged_join_kernel<D>, dim3(grid, (join_rows + kJoinRows - 1) / kJoinRows),
+    return launch_pdl(paged_join_kernel<S::D>,
+                      dim3(static_cast<unsigned>(grid), (join_rows + kJoinRows - 1) / kJoinRows),
                       2 * kJoinRows * 32, 0, stream, p, static_cast<int>(S::rows));
 }
 
-// Workspace of the widest instantiation at D columns: a CTA's descriptor and two
-// partials of its rows.
+// A CTA's descriptor and two partials of up to 32 rows (16 at 256 columns).
 int64_t workspace_bytes(int sms, int D) {
-    const int64_t three = 3 * 16, two = 2 * 32;
-    const int64_t rows = sms * (D == 64 ? 3 * 32 : D == 128 ? (three > two ? three : two) : 2 * 16);
-    return 4 * (4 * 3 * static_cast<int64_t>(sms) + 2 * rows * (D + 2));
+    const int64_t most = static_cast<int64_t>(sms) * kGridPerSm;
+    return 4 * most * (4 + 2 * (D == 256 ? 16 : 32) * (D + 2));
 }
 
 }  // namespace
@@ -882,7 +917,8 @@ extern "C" int smd_paged_decode(const uint16_t* q, int64_t q_stride, const smd_p
 
     const bool lists = block_lists != nullptr;
     const int g = Hq / cache->heads, rows = lists ? g : row_group * g;
-    const int MT = D == 256 || rows <= 16 ? 1 : 2, KT = D == 256 ? 16 : 32;
+    const int most_tiles = D == 256 ? 2 : 4;  // of 8 rows: what the registers hold
+    const int RT = rows <= 8 ? 1 : rows <= 16 ? 2 : most_tiles, KT = D == 256 ? 16 : 32;
     PagedParams p{};
     p.q_stride = q_stride;
     p.table_stride = table_stride;
@@ -892,7 +928,7 @@ extern "C" int smd_paged_decode(const uint16_t* q, int64_t q_stride, const smd_p
     p.pages = cache->pages;
     p.heads = cache->heads;
     p.page_size = P;
-    p.row_tiles = (rows + 16 * MT - 1) / (16 * MT);
+    p.row_tiles = (rows + 8 * RT - 1) / (8 * RT);
     p.x_units = lists ? p.row_tiles : cache->heads * p.row_tiles;
     p.G = row_group;
     p.g = g;
@@ -926,14 +962,19 @@ extern "C" int smd_paged_decode(const uint16_t* q, int64_t q_stride, const smd_p
         p.out = out + row * Hq * D;
         p.lse = lse != nullptr ? lse + row * Hq : nullptr;
         const int64_t tiles = n * per_request;
+        const auto launch = [&](auto shape) {
+            return launch_decode<decltype(shape)>(p, maps[0], maps[1], sms, tiles, stream);
+        };
         if (D == 64)
-            rc = MT == 1 ? launch_decode<64, 1, 32, 4>(p, maps[0], maps[1], sms, tiles, stream)
-                         : launch_decode<64, 2, 32, 3>(p, maps[0], maps[1], sms, tiles, stream);
+            rc = RT == 1   ? launch(Shape<64, 1, 32, 4, 3>{})
+                 : RT == 2 ? launch(Shape<64, 2, 32, 4, 3>{})
+                           : launch(Shape<64, 4, 32, 4, 2>{});
         else if (D == 128)
-            rc = MT == 1 ? launch_decode<128, 1, 32, 2>(p, maps[0], maps[1], sms, tiles, stream)
-                         : launch_decode<128, 2, 32, 3>(p, maps[0], maps[1], sms, tiles, stream);
+            rc = RT == 1   ? launch(Shape<128, 1, 32, 2, 3>{})
+                 : RT == 2 ? launch(Shape<128, 2, 32, 2, 3>{})
+                           : launch(Shape<128, 4, 32, 3, 2>{});
         else
-            rc = launch_decode<256, 1, 16, 3>(p, maps[0], maps[1], sms, tiles, stream);
+            rc = RT == 1 ? launch(Shape<256, 1, 16, 2, 3>{}) : launch(Shape<256, 2, 16, 3, 2>{});
         if (rc != SMD_OK) return rc;
     }
     return SMD_OK;
