@@ -804,9 +804,11 @@ int64_t smd_paged_workspace_bytes(const smd_paged_cache_t* cache);
  *   block_counts  [B, heads] int32; NULL: all K.
  *   out      [B, Hq, head_dim] bfloat16, contiguous, 16-byte aligned.
  *   lse      [B, Hq] float32; may be NULL.
- *   workspace     at least smd_paged_workspace_bytes, 16-byte aligned; needs
- *            no initialisation. Calls that overlap on the GPU must not share
- *            one.
+ *   workspace     at least smd_paged_workspace_bytes, 16-byte aligned, zeroed
+ *            once before its first use: it holds counts that every call
+ *            leaves at zero. Calls that overlap on the GPU must not share
+ *            one. A call that reported an error in `status` may leave counts
+ *            behind: zero it again.
  * The other arguments are smd_block_scores'. Codes of tokens that a row does
  * not see never reach its result, whatever they are. Table entries outside the
  * pool read nothing (their tokens count as zeros). The keys are cut by the

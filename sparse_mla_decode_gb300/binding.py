@@ -1064,8 +1064,8 @@ def paged_decode(q, cache: PagedCache, table, lengths, sm_scale: float, row_grou
     int32; block_lists [R * row_group, heads, K] int32: the pages of its request
     that each row and kv head attends (topk_select's output on block_scores),
     the first block_counts [R * row_group, heads] of them; None: all of its
-    tokens. ``workspace``: a CUDA tensor of paged_workspace_bytes(cache) bytes
-    (allocated here if None). Returns (out [R * row_group, Hq, head_dim]
+    tokens. ``workspace``: a CUDA tensor of paged_workspace_bytes(cache) bytes,
+    zeroed once before its first use (allocated here if None). Returns (out [R * row_group, Hq, head_dim]
     bfloat16, lse [R * row_group, Hq] float32)."""
     import torch
 
@@ -1090,7 +1090,7 @@ def paged_decode(q, cache: PagedCache, table, lengths, sm_scale: float, row_grou
         lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
     _vector(lse, "lse", torch.float32, B * Hq)
     if workspace is None:
-        workspace = torch.empty(paged_workspace_bytes(cache), dtype=torch.uint8, device=q.device)
+        workspace = torch.zeros(paged_workspace_bytes(cache), dtype=torch.uint8, device=q.device)
     elif not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
     rc = lib().smd_paged_decode(

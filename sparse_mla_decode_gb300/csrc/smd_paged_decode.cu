@@ -16,14 +16,16 @@
 // A warp is a worker of its own: it walks tiles of KT tokens of one (page,
 // head) through a ring of ST slots that its own lanes fill with tensor copies
 // (K and V of a tile: one barrier), and holds the tile's softmax state and its
-// D x M accumulators in registers. No CTA barrier is passed until the tokens
-// of a unit (a request's kv head) end, where the CTA's warps join their
-// states through shared memory (the slots they have just consumed).
-//
-// The tiles of all units, laid end to end, are cut evenly over the grid, so a
-// batch of mixed lengths loads every SM alike; a unit cut by a CTA boundary
-// leaves fp32 partials in the workspace, joined in CTA order by a second
-// kernel (run-to-run the same bits; no atomics, no flags).
+// D x M accumulators in registers. The tiles of all units (a request's kv
+// head), laid end to end, are cut evenly over the warps of the grid, so a batch
+// of mixed lengths loads every SM alike and no warp waits for another before it
+// is through. A unit inside one warp's range is written by it. A unit that cuts
+// divide is joined in order, in three steps: the CTA's warps through shared
+// memory (the ring of a warp that is through holds its accumulators), then up
+// to 32 neighbouring CTAs, then those groups, through fp32 partials in the
+// workspace. Each of the last two is done by the CTA that arrives last, by a
+// count, so nothing waits and no second kernel is needed; who joins depends on
+// timing, what is added to what does not: run to run the bits are the same.
 //
 // Operand layouts (lane = 4 g + i): K comes by ldmatrix as 4 consecutive codes
 // of token g, columns 16 c + 4 i ..; the contraction index of the MMA is
@@ -60,8 +62,9 @@ constexpr int kMaxEntries = 1024;  // requests (or (row, kv head) lists) of one 
 constexpr int kNoPos = 0x3fffffff; // the position of tokens that no row sees
 constexpr float kPShift = 7.0f;    // weights are formed at 2^7 of the maximum kept
 constexpr float kSlack = 8.0f;     // which is moved when a logit exceeds it by 2^8
-constexpr int kJoinRows = 4;       // rows of a unit that a CTA of the join takes
-constexpr int kUnitCost = 8;       // what ending a unit costs a CTA, in tiles
+constexpr int kUnitCost = 2;       // what a unit's begin and end cost a warp, in tiles
+constexpr int kMinTiles = 1;       // least tiles of a warp
+constexpr int kFan = 32;           // neighbouring CTAs of a first join
 
 struct PagedParams {
     const uint16_t* q;
@@ -77,6 +80,7 @@ struct PagedParams {
     int32_t x_units;    // units of an entry: (kv heads x) row tiles
     int32_t row_tiles;
     int32_t G, g, Hq;   // verify rows; query heads of a kv head; query heads
+    uint32_t g_magic;   // ceil(2^20 / g): m / g = (m * g_magic) >> 20 for m < 1024, g <= 128
     int32_t rows;       // query rows of a unit before tiling: G * g, or g with lists
     float scale_log2;   // sm_scale * log2 e
     const int32_t* lists;
@@ -85,9 +89,13 @@ struct PagedParams {
     uint16_t* out;
     float* lse;
     int32_t* status;
-    int32_t* desc;      // [grid][2]: the unit a CTA starts and does not end, its last CTA
-    float* part;        // [grid][2][rows of a tile][D]
-    float* part_ml;     // [grid][2][rows of a tile][2]: maximum, sum
+    int32_t workers;    // warps of the grid
+    int32_t* arrived;   // [2][2 CTAs]: arrivals at the joins of CTAs, 0 between calls
+    float* head;        // [workers][rows of a tile][D]: the end of a unit begun by a warp before
+    float* part;        // [CTAs][4][rows of a tile][D]: the unit that the CTA goes on with, and
+                        // what its group of CTAs has of it; the same of the unit that it begins
+    float2* head_ml;    // the same without columns: maximum, sum
+    float2* part_ml;
     int32_t box;        // tokens of a copy box
 };
 
@@ -137,6 +145,10 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* map, int x
         : "memory");
 }
 
+__device__ __forceinline__ void prefetch_map(const void* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
 __device__ __forceinline__ void lds64(uint32_t addr, uint32_t& a, uint32_t& b) {
     asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(a), "=r"(b) : "r"(addr) : "memory");
 }
@@ -158,6 +170,14 @@ __device__ __forceinline__ float4 lds_f4(uint32_t addr) {
     return v;
 }
 
+__device__ __forceinline__ float bf_lo(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
+
+// ln of the sum of e^logits, from a maximum (base 2) and the sum of the weights at it.
+__device__ __forceinline__ float natural_lse(float top, float sum) {
+    return sum == 0.0f ? -INFINITY : 0.69314718055994531f * (top - kPShift + log2f(sum));
+}
+
 // Transposes the 8 x 8 block of 16-bit elements whose row g holds its elements
 // 2i, 2i + 1 in lane 4 g + i.
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
@@ -175,16 +195,16 @@ struct Shape {
     static constexpr int row_bytes = D < 128 ? D : 128;  // of a copy box
     static constexpr int side = KT * D;                  // bytes of a tile's K, and of its V
     static constexpr int slot = 2 * side;
-    static constexpr int q_pitch = 2 * D + 32;           // 8-byte reads of 4 rows hit 4 bank groups
-    static constexpr int off_q = kWarps * ST * slot;
-    static constexpr int off_qf = off_q + rows * q_pitch;         // [rows] logit factors
-    static constexpr int off_lim = off_qf + rows * 4;             // [rows] tokens that a row sees
-    static constexpr int off_ml = off_lim + rows * 4;             // [warps][rows] maximum, sum
-    static constexpr int off_meta = off_ml + kWarps * rows * 8;   // [warps][ST][8] words
-    static constexpr int off_bar = off_meta + kWarps * ST * 32;
-    static constexpr int off_scan = off_bar + kWarps * ST * 8;    // [warps + 1] words
-    static constexpr int off_prefix = off_scan + 32;              // [entries + 1]
-    static constexpr int smem(int entries) { return off_prefix + 4 * (entries + 1) + 1024; }
+    static constexpr bool q_regs = rows * D <= 2048;     // query fragments stay in registers
+    static constexpr int off_q = kWarps * ST * slot;     // else here: [warps][RT][D / 16][32] pairs
+    static constexpr int off_meta = off_q + (q_regs ? 0 : kWarps * rows * D * 2);
+    static constexpr int off_bar = off_meta + kWarps * ST * 32;   // [warps][ST]
+    static constexpr int off_scan = off_bar + kWarps * ST * 8;    // [warps] words
+    static constexpr int off_ml = off_scan + 32;                  // [warps][rows] maximum, sum
+    static constexpr int off_left = off_ml + kWarps * rows * 8;   // [warps] what a warp leaves
+    static constexpr int off_prefix = off_left + kWarps * 64;     // [entries + 1], then [entries] lengths
+    static_assert(rows * D * 4 <= ST * slot, "a warp's accumulators fit its ring");
+    static constexpr int smem(int entries) { return off_prefix + 4 * (2 * entries + 1) + 1024; }
 };
 
 // Byte offset of 16-byte piece c of token `row` in a side of a slot, as the
@@ -195,26 +215,69 @@ __device__ __forceinline__ uint32_t piece(int row, int c) {
     return (c >> 3) * (KT * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
 }
 
-// The tokens an entry's units walk, in tiles of KT; at least one tile, so that
-// a unit without tokens still writes its zeros.
-template <int KT>
-__device__ __forceinline__ int entry_tiles(const PagedParams& p, int e) {
-    int n;
-    if (p.lists != nullptr) {
-        int c = p.counts != nullptr ? p.counts[e] : p.K;
-        n = max(min(c, p.K), 0) * p.page_size;
-    } else {
-        n = max(min(p.lengths[e], p.width * p.page_size), 0);
-    }
-    return max((n + KT - 1) / KT, 1);
-}
-
 // One tile's tokens: for each 16 of them the page, the offset in it, the first
 // token's position in its request and the scales.
 template <int NH>
 struct Tile {
     int page[NH], off[NH], pos[NH], head;
     float ks[NH], vs[NH];
+};
+
+// A unit's row tile: its query rows as rows of the batch and query heads, and the
+// CTAs that hold its first and last tile.
+struct Unit {
+    int b0, head, m0, m_real, first_cta, last_cta;
+    __device__ __forceinline__ int verify_row(const PagedParams& p, int m) const {
+        return static_cast<int>((static_cast<uint32_t>(m0 + m) * p.g_magic) >> 20);
+    }
+    __device__ __forceinline__ int64_t b(const PagedParams& p, int m) const {
+        return p.lists != nullptr ? b0 : b0 + verify_row(p, m);
+    }
+    __device__ __forceinline__ int a(const PagedParams& p, int m) const {
+        return head * p.g + m0 + m - verify_row(p, m) * p.g;
+    }
+};
+
+// Four columns of one row, done: out and lse.
+__device__ __forceinline__ void write_row(const PagedParams& p, const Unit& u, int D, int row,
+                                          int col, float4 v, float top, float sum) {
+    const int64_t at = u.b(p, row) * p.Hq + u.a(p, row);
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    *reinterpret_cast<uint2*>(p.out + at * D + col) =
+        make_uint2(bf16x2(v.x * inv, v.y * inv), bf16x2(v.z * inv, v.w * inv));
+    if (col == 0 && p.lse != nullptr) p.lse[at] = natural_lse(top, sum);
+}
+
+// Adds N partials (maximum and sum, four of their columns; none: -infinity, 0) to
+// another, in order.
+template <int N>
+__device__ __forceinline__ void add_partials(float4& acc, float& top, float& sum, const float4 (&v)[N],
+                                             const float2 (&ml)[N]) {
+    float to = top;
+#pragma unroll
+    for (int z = 0; z < N; ++z) to = fmaxf(to, ml[z].x);
+    const float keep = top == -INFINITY ? 0.0f : ex2_approx(top - to);
+    top = to;
+    sum *= keep;
+    acc.x *= keep, acc.y *= keep, acc.z *= keep, acc.w *= keep;
+#pragma unroll
+    for (int z = 0; z < N; ++z) {
+        const float w = ml[z].x == -INFINITY ? 0.0f : ex2_approx(ml[z].x - to);
+        sum += ml[z].y * w;  // a NaN stays one
+        acc.x += v[z].x * w;
+        acc.y += v[z].y * w;
+        acc.z += v[z].z * w;
+        acc.w += v[z].w * w;
+    }
+}
+
+// What a warp leaves to its CTA: the unit whose end it held (its partial is in
+// PagedParams::head) and the unit that goes on after it (in its ring).
+struct Left {
+    int32_t ended, open;   // the unit's number, or -1
+    int32_t open_begins;   // the open unit begins in this warp's range
+    int32_t pad;
+    Unit ended_unit, open_unit;
 };
 
 template <typename S>
@@ -224,19 +287,22 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
     constexpr int D = S::D, RT = S::RT, KT = S::KT, ST = S::ST;
     constexpr int NH = KT / 16;   // 16-token halves of a tile
     constexpr int NC = D / 16;    // 16-column chunks
-    constexpr bool kQRegs = RT * D <= 256;  // query fragments stay in registers
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
     uint8_t* const gbase = smem_raw + (base - smem_addr(smem_raw));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, qr = lane >> 2, qi = lane & 3;
     int32_t* const prefix = reinterpret_cast<int32_t*>(gbase + S::off_prefix);
-    float2* const ml = reinterpret_cast<float2*>(gbase + S::off_ml);
-    float* const qf = reinterpret_cast<float*>(gbase + S::off_qf);
-    int32_t* const lims = reinterpret_cast<int32_t*>(gbase + S::off_lim);
+    int32_t* const lens = prefix + p.entries + 1;
     const uint32_t ring = base + warp * ST * S::slot;
     const uint32_t bars = base + S::off_bar + warp * ST * 8;
     const uint32_t meta = base + S::off_meta + warp * ST * 32;  // ks, vs, pos of each half
+    const uint32_t q_at = base + S::off_q + warp * S::rows * D * 2 + 8 * lane;
+    const bool lists = p.lists != nullptr;
 
+    if (tid == 0) {
+        prefetch_map(&kmap);
+        prefetch_map(&vmap);
+    }
     if (lane == 0) {
         for (int s = 0; s < ST; ++s) mbar_init(bars + 8 * s, 1);
         fence_mbar_init();
@@ -245,16 +311,29 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
     pdl_entry();
     fence_proxy_async_global();  // the cache may have been written by the kernel before
 
-    // Prefix sums of the entries' tiles.
-    constexpr int kPer = kMaxEntries / kThreads;
+    // Prefix sums of the entries' tiles: at least one for each unit, so that one without
+    // tokens still writes its zeros.
     int total;
     {
+        const auto tiles_of = [&](int e) {
+            if (e >= p.entries) return 0;
+            const int len = max(min(p.lengths[lists ? e / (p.heads * p.G) : e], p.width * p.page_size), 0);
+            int n = len;
+            if (lists) n = max(min(p.counts != nullptr ? p.counts[e] : p.K, p.K), 0) * p.page_size;
+            lens[e] = len;
+            return max((n + KT - 1) / KT, 1) * p.x_units;
+        };
+        constexpr int kPer = kMaxEntries / kThreads;
         int v[kPer], sum = 0;
+        const int each = p.entries <= kThreads ? 1 : kPer;  // entries of a thread
+        if (each == 1) {
+            v[0] = sum = tiles_of(tid);
+        } else {
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-            const int e = tid * kPer + j;
-            v[j] = e < p.entries ? entry_tiles<KT>(p, e) * p.x_units : 0;
-            sum += v[j];
+            for (int j = 0; j < kPer; ++j) {
+                v[j] = tiles_of(tid * kPer + j);
+                sum += v[j];
+            }
         }
         int inc = sum;
 #pragma unroll
@@ -267,17 +346,22 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
         __syncthreads();
         int before = inc - sum;
         total = 0;
+#pragma unroll
         for (int w = 0; w < kWarps; ++w) {
             if (w < warp) before += scan[w];
             total += scan[w];
         }
+        if (each == 1) {
+            if (tid < p.entries) prefix[tid] = before;
+        } else {
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-            const int e = tid * kPer + j;
-            if (e <= p.entries) prefix[e] = before;
-            before += v[j];
+            for (int j = 0; j < kPer; ++j) {
+                const int e = tid * kPer + j;
+                if (e < p.entries) prefix[e] = before;
+                before += v[j];
+            }
         }
-        if (tid == kThreads - 1 && p.entries == kMaxEntries) prefix[kMaxEntries] = before;
+        if (tid == 0) prefix[p.entries] = total;
     }
     __syncthreads();
 
@@ -294,8 +378,8 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
     };
     const auto find_entry = [&](int t) { return find(t, 0); };
     const int cost = total + kUnitCost * p.x_units * p.entries;
-    const int grid = static_cast<int>(gridDim.x);
-    const int per = max((cost + grid - 1) / grid, kWarps + kUnitCost);
+    const int worker = static_cast<int>(blockIdx.x) * kWarps + warp;
+    const int per = max((cost + p.workers - 1) / p.workers, kMinTiles + kUnitCost);
     const auto tiles_before = [&](int64_t at) {  // tiles that lie before a cost position
         if (at >= cost) return total;
         const int c = static_cast<int>(at), e = find(c, kUnitCost);
@@ -303,18 +387,13 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
         const int rem = c - prefix[e] - kUnitCost * p.x_units * e, x = rem / (nt + kUnitCost);
         return prefix[e] + x * nt + max(rem - x * (nt + kUnitCost) - kUnitCost, 0);
     };
-    const int64_t at0 = static_cast<int64_t>(blockIdx.x) * per;
-    const int t0 = tiles_before(at0), t1 = tiles_before(at0 + per);
-    if (tid == 0) {
-        p.desc[2 * blockIdx.x] = -1;
-    }
-    if (t0 >= t1) return;
+    const int cut = tiles_before(static_cast<int64_t>(worker + (lane & 1)) * per);
+    const int t0 = __shfl_sync(0xffffffffu, cut, 0), t1 = __shfl_sync(0xffffffffu, cut, 1);
 
-    // Lane l resolves tile 32 * (k / 32) + l of this warp's tiles.
+    // Lane l resolves tile t0 + 32 * (k / 32) + l.
     Tile<NH> td;
-    const int my_tiles = (t1 - t0 - warp + kWarps - 1) / kWarps;
     const auto resolve = [&](int kk) {
-        const int t = t0 + warp + kWarps * kk;
+        const int t = t0 + kk;
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
             td.page[h] = -1;
@@ -327,16 +406,15 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
         if (t >= t1) return;
         const int e = find_entry(t), nt = (prefix[e + 1] - prefix[e]) / p.x_units;
         const int rem = t - prefix[e], x = rem / nt, first = (rem - x * nt) * KT;
-        const int b = p.lists != nullptr ? e / p.heads : e;      // row, or request
-        const int r = p.lists != nullptr ? b / p.G : e;
-        td.head = p.lists != nullptr ? e - b * p.heads : x / p.row_tiles;
-        const int len = max(min(p.lengths[r], p.width * p.page_size), 0);
+        const int b = lists ? e / p.heads : e;  // row, or request
+        const int r = lists ? b / p.G : e, len = lens[e];
+        td.head = lists ? e - b * p.heads : x / p.row_tiles;
         const int32_t* const row = p.table + static_cast<int64_t>(r) * p.table_stride;
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
             int blk = (first + 16 * h) / p.page_size;
             const int off = first + 16 * h - blk * p.page_size;
-            if (p.lists != nullptr) {
+            if (lists) {
                 const int c = p.counts != nullptr ? max(min(p.counts[e], p.K), 0) : p.K;
                 blk = blk < c ? p.lists[static_cast<int64_t>(e) * p.K + blk] : -1;
             }
@@ -351,10 +429,12 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
             td.vs[h] = p.v_scale[static_cast<int64_t>(pg) * p.heads + td.head];
         }
     };
-    // Fills the slot of this warp's tile kk; all lanes call it in order of kk.
+    // Fills the slot of tile t0 + kk; called in order of kk.
     const auto issue = [&](int kk) {
-        if (kk >= my_tiles) return;
-        if ((kk & 31) == 0) resolve(kk + lane);
+        if (t0 + kk >= t1) return;
+        // The first tiles' copies go out before the other lanes look their tiles up.
+        if (kk == 0 || kk == ST || (kk & 31) == 0)
+            resolve(kk == 0 && lane >= ST ? t1 - t0 : (kk & ~31) + lane);
         if (lane == (kk & 31)) {
             const int s = kk % ST;
             const uint32_t bar = bars + 8 * s, dst = ring + s * S::slot;
@@ -376,76 +456,81 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
         __syncwarp();
     };
 
-    // Row m (of the unit, before tiling): verify row and query head.
-    const auto row_limit = [&](int m, int b, int len) {
-        const int i = p.lists != nullptr ? b % p.G : m / p.g;
-        return max(len - p.G + 1 + i, 0);
-    };
-    // The unit's queries as f16 in shared memory, with each row's logit factor
-    // (positive: a negative softmax scale turns the query's sign) and limit.
-    const auto load_q = [&](int e, int x) {
-        const int rt = x % p.row_tiles, u_b = p.lists != nullptr ? e / p.heads : e * p.G;
-        const int u_len =
-            max(min(p.lengths[p.lists != nullptr ? u_b / p.G : e], p.width * p.page_size), 0);
-        const int head = p.lists != nullptr ? e % p.heads : x / p.row_tiles;
-        constexpr int kPieces = D / 8;
-        for (int idx = tid; idx < S::rows * kPieces; idx += kThreads) {
-            const int m = idx / kPieces, c = idx % kPieces, mm = rt * S::rows + m;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (mm < p.rows) {
-                const int64_t b = p.lists != nullptr ? e / p.heads
-                                                     : static_cast<int64_t>(e) * p.G + mm / p.g;
-                v = *reinterpret_cast<const uint4*>(p.q + b * p.q_stride +
-                                                    static_cast<int64_t>(head * p.g + mm % p.g) * D +
-                                                    8 * c);
-            }
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            float f[8], a = 0.0f;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                f[2 * j] = __uint_as_float(w[j] << 16);
-                f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-                a = fmaxf(a, fmaxf(fabsf(f[2 * j]), fabsf(f[2 * j + 1])));
-            }
-#pragma unroll
-            for (int o = 1; o < kPieces; o <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-            // up = 2^(14 - exponent of a), within what a float holds
-            const int ex = static_cast<int>(__float_as_uint(a) >> 23);
-            const int ue = min(14 + 127 - ex + 127, 253);
-            float up = a > 0.0f && ex < 255 ? __uint_as_float(static_cast<uint32_t>(ue) << 23) : 1.0f;
-            if (c == 0) {
-                qf[m] = fabsf(p.scale_log2) / up;
-                lims[m] = mm < p.rows ? row_limit(mm, u_b, u_len) : 0;
-            }
-            if (p.scale_log2 < 0.0f) up = -up;
-            const uint32_t at = base + S::off_q + m * S::q_pitch + 16 * c;
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at),
-                         "r"(f16x2(f[0] * up, f[1] * up)), "r"(f16x2(f[2] * up, f[3] * up)),
-                         "r"(f16x2(f[4] * up, f[5] * up)), "r"(f16x2(f[6] * up, f[7] * up))
-                         : "memory");
-        }
-    };
-
+    float2* const s_ml = reinterpret_cast<float2*>(gbase + S::off_ml);
+    Left* const s_left = reinterpret_cast<Left*>(gbase + S::off_left);
+    if (lane == 0) s_left[warp].ended = s_left[warp].open = -1;
     bool ok = true;
-    int k = 0, t = t0, e = find_entry(t0);
+    int k = 0, t = t0, e = t0 < t1 ? find(t0, 0) : 0;
 #pragma unroll 1
-    for (int s = 0; s < ST - 1; ++s) issue(s);
-    {
-        const int nt = (prefix[e + 1] - prefix[e]) / p.x_units;
-        load_q(e, (t0 - prefix[e]) / nt);
-    }
-    __syncthreads();
+    for (int s = 0; s < ST; ++s) issue(s);
 
 #pragma unroll 1
     while (t < t1) {
         while (prefix[e + 1] <= t) ++e;
         const int nt = (prefix[e + 1] - prefix[e]) / p.x_units, x = (t - prefix[e]) / nt;
         const int u0 = prefix[e] + x * nt, u1 = u0 + nt, tend = min(u1, t1);
-        const int rt = x % p.row_tiles, b0 = p.lists != nullptr ? e / p.heads : e * p.G;
-        const int m_real = min(p.rows - rt * S::rows, S::rows);
-        const int min_lim = lims[0], max_lim = lims[m_real - 1];
+        const int len = lens[e], b0 = lists ? e / p.heads : e * p.G;
+        Unit u;
+        {
+            const int rt = x % p.row_tiles;
+            u.b0 = b0;
+            u.head = lists ? e - b0 * p.heads : x / p.row_tiles;
+            u.m0 = rt * S::rows;
+            u.m_real = min(p.rows - u.m0, S::rows);
+        }
+        const int m_real = u.m_real;
+        // The tokens that row m of the tile sees.
+        const auto row_limit = [&](int m) {
+            return max(len - p.G + 1 + (lists ? b0 % p.G : u.verify_row(p, m)), 0);
+        };
+        const int min_lim = row_limit(0), max_lim = row_limit(m_real - 1);
+
+        // The queries of row 8 n + g, columns 16 c + 4 i .., as f16; the logit factor of
+        // rows 8 n + 2 i + y (positive: a negative softmax scale turns the query's sign).
+        uint32_t qb[S::q_regs ? RT : 1][S::q_regs ? NC : 1][2];
+        float fac[RT][2];
+#pragma unroll
+        for (int n = 0; n < RT; ++n) {
+            uint2 w[NC];
+            const int m = 8 * n + qr;
+#pragma unroll
+            for (int c = 0; c < NC; ++c) w[c] = make_uint2(0, 0);
+            if (m < m_real) {
+                const uint16_t* const row =
+                    p.q + u.b(p, m) * p.q_stride + static_cast<int64_t>(u.a(p, m)) * D + 4 * qi;
+#pragma unroll
+                for (int c = 0; c < NC; ++c)
+                    w[c] = __ldg(reinterpret_cast<const uint2*>(row + 16 * c));
+            }
+            float a = 0.0f;
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                a = fmaxf(a, fmaxf(fabsf(bf_lo(w[c].x)), fabsf(bf_hi(w[c].x))));
+                a = fmaxf(a, fmaxf(fabsf(bf_lo(w[c].y)), fabsf(bf_hi(w[c].y))));
+            }
+            a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
+            a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
+            // up = 2^(14 - exponent of a), within what a float holds
+            const int ex = static_cast<int>(__float_as_uint(a) >> 23);
+            const int ue = min(14 + 127 - ex + 127, 253);
+            float up = a > 0.0f && ex < 255 ? __uint_as_float(static_cast<uint32_t>(ue) << 23) : 1.0f;
+            const float own = fabsf(p.scale_log2) / up;
+            fac[n][0] = __shfl_sync(0xffffffffu, own, 8 * qi);
+            fac[n][1] = __shfl_sync(0xffffffffu, own, 8 * qi + 4);
+            if (p.scale_log2 < 0.0f) up = -up;
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                const uint32_t f0 = f16x2(bf_lo(w[c].x) * up, bf_hi(w[c].x) * up);
+                const uint32_t f1 = f16x2(bf_lo(w[c].y) * up, bf_hi(w[c].y) * up);
+                if (S::q_regs) {
+                    qb[S::q_regs ? n : 0][S::q_regs ? c : 0][0] = f0;
+                    qb[S::q_regs ? n : 0][S::q_regs ? c : 0][1] = f1;
+                } else {
+                    sts64(q_at + (n * NC + c) * 256, f0, f1);  // read by this lane only
+                }
+            }
+        }
         float m[RT][2], l[RT][2], o[RT][NC][4], vref = 0.0f;
-        uint32_t qb[kQRegs ? RT : 1][kQRegs ? NC : 1][2];
 #pragma unroll
         for (int n = 0; n < RT; ++n)
 #pragma unroll
@@ -459,18 +544,10 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
             for (int c = 0; c < NC; ++c)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) o[n][c][j] = 0.0f;
-        const uint32_t q_at = base + S::off_q + qr * S::q_pitch + 8 * qi;
-        if (kQRegs) {
-#pragma unroll
-            for (int n = 0; n < (kQRegs ? RT : 0); ++n)
-#pragma unroll
-                for (int c = 0; c < NC; ++c)
-                    lds64(q_at + n * 8 * S::q_pitch + 32 * c, qb[n][c][0], qb[n][c][1]);
-        }
 
 #pragma unroll 1
-        for (; t0 + warp + kWarps * k < tend; ++k) {
-            issue(k + ST - 1);
+        for (; t < tend; ++t, ++k) {
+            if (k > 0) issue(k + ST - 1);
             const int slot = k % ST;
             mbar_wait(bars + 8 * slot, (k / ST) & 1, ok, p.status, kWaitBudgetNs);
             const uint32_t ks_at = ring + slot * S::slot, vs_at = ks_at + S::side;
@@ -499,11 +576,11 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
 #pragma unroll
                     for (int z = 0; z < 2; ++z) {
                         const int h = z % NH, c = c0 + z / NH;
-                        if (kQRegs) {
-                            b0v = qb[kQRegs ? n : 0][kQRegs ? c : 0][0];
-                            b1v = qb[kQRegs ? n : 0][kQRegs ? c : 0][1];
+                        if (S::q_regs) {
+                            b0v = qb[S::q_regs ? n : 0][S::q_regs ? c : 0][0];
+                            b1v = qb[S::q_regs ? n : 0][S::q_regs ? c : 0][1];
                         } else if (z == 0 || NH == 1) {
-                            lds64(q_at + n * 8 * S::q_pitch + 32 * c, b0v, b1v);
+                            lds64(q_at + (n * NC + c) * 256, b0v, b1v);
                         }
                         mma_f16(s[h][n], a[z][0], a[z][1], a[z][2], a[z][3], b0v, b1v);
                     }
@@ -521,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
                 for (int n = 0; n < RT; ++n)
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
-                        const int lim = lims[8 * n + 2 * qi + y];
+                        const int lim = row_limit(min(8 * n + 2 * qi + y, m_real - 1));
 #pragma unroll
                         for (int h = 0; h < NH; ++h)
 #pragma unroll
@@ -560,7 +637,7 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
                                     for (int n = 0; n < RT; ++n)
 #pragma unroll
                                         for (int y = 0; y < 2; ++y)
-                                            if (at < lims[8 * n + 2 * qi + y])
+                                            if (at < row_limit(8 * n + 2 * qi + y))
                                                 o[n][c][2 * z + y] = NAN;
                             const uint32_t bad = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
                             __syncwarp();
@@ -579,11 +656,10 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
             for (int n = 0; n < RT; ++n)
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
-                    const float fac = qf[8 * n + 2 * qi + y];
                     v[n][y] = -INFINITY;
 #pragma unroll
                     for (int h = 0; h < NH; ++h) {
-                        f[h][n][y] = fmaxf(fac * ks[h], 1.17549435e-38f);
+                        f[h][n][y] = fmaxf(fac[n][y] * ks[h], 1.17549435e-38f);
                         v[n][y] = fmaxf(v[n][y], fmaxf(s[h][n][y], s[h][n][2 + y]) * f[h][n][y]);
                     }
                     moved = moved || v[n][y] > m[n][y] + kSlack;
@@ -657,190 +733,223 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
             __syncwarp();
         }
 
-        // The warps' states become the CTA's. Warp w holds tiles of this unit if one of
-        // its turns fell into [t, tend); the slot it consumed last takes its accumulators.
-#pragma unroll
-        for (int n = 0; n < RT; ++n)
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                float v = l[n][y];
-                v += __shfl_xor_sync(0xffffffffu, v, 4);
-                v += __shfl_xor_sync(0xffffffffu, v, 8);
-                v += __shfl_xor_sync(0xffffffffu, v, 16);
-                if (qr == 0) ml[warp * S::rows + 8 * n + 2 * qi + y] = make_float2(m[n][y], v);
+        // The unit's rows, or this warp's part of them.
+        const bool whole = u0 >= t0 && u1 <= t1, open = u1 > t1;
+        if (!whole) {
+            const int unit = e * p.x_units + x, at = u0 + kUnitCost * (unit + 1);  // its first tile
+            u.first_cta = at / per / kWarps;
+            u.last_cta = (at + nt - 1) / per / kWarps;
+            Left* const left = s_left + warp;
+            if (lane == 0 && open) {
+                left->open = unit;
+                left->open_begins = u0 >= t0;
+                left->open_unit = u;
+            } else if (lane == 0) {
+                left->ended = unit;
+                left->ended_unit = u;
             }
-        __syncthreads();
-        const bool mine = k > 0 && t0 + warp + kWarps * (k - 1) >= t;
-        float wgt[RT][2];
-#pragma unroll
-        for (int n = 0; n < RT; ++n)
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                float top = -INFINITY;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w)
-                    top = fmaxf(top, ml[w * S::rows + 8 * n + 2 * qi + y].x);
-                wgt[n][y] = m[n][y] == -INFINITY ? 0.0f : vref * ex2_approx(m[n][y] - top);
-            }
-        const bool whole = u0 >= t0 && u1 <= t1;
-        const int part_at = (2 * static_cast<int>(blockIdx.x) + (u0 >= t0 ? 1 : 0)) * S::rows;
-        if (!whole && u0 >= t0 && tid == 0) {
-            p.desc[2 * blockIdx.x] = e * p.x_units + x;
-            // the CTA that holds the unit's last tile
-            p.desc[2 * blockIdx.x + 1] = (u1 - 1 + kUnitCost * (e * p.x_units + x + 1)) / per;
         }
-        constexpr int kRound = RT < KT / 16 ? RT : KT / 16;  // row tiles that a slot holds in fp32
 #pragma unroll
-        for (int n0 = 0; n0 < RT; n0 += kRound) {
-                if (mine) {
-                    const uint32_t buf = ring + ((k - 1) % ST) * S::slot;
+        for (int n = 0; n < RT; ++n)
 #pragma unroll
-                    for (int n = 0; n < kRound; ++n)
+            for (int y = 0; y < 2; ++y) {
+                float sum = l[n][y];
+                sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+                const int row = 8 * n + 2 * qi + y;
+                if (row >= m_real) continue;
+                if (whole) {
+                    const int64_t at = u.b(p, row) * p.Hq + u.a(p, row);
+                    const float w = sum == 0.0f ? 0.0f : vref / sum;
+                    uint32_t* const out = reinterpret_cast<uint32_t*>(p.out + at * D) + qr;
 #pragma unroll
-                        for (int c = 0; c < NC; ++c) {
-                            const float(&v)[4] = o[n0 + n][c];
+                    for (int c = 0; c < NC; ++c)
+                        out[8 * c] = bf16x2(o[n][c][y] * w, o[n][c][2 + y] * w);
+                    if (qr == 0 && p.lse != nullptr) p.lse[at] = natural_lse(m[n][y], sum);
+                } else if (open) {
+                    // every tile of the ring has been consumed
 #pragma unroll
-                            for (int y = 0; y < 2; ++y) {
-                                const uint32_t unit = (4 * c + (qr >> 1)) ^ (qi << 1);
-                                const float w = wgt[n0 + n][y];
-                                sts64(buf + (8 * n + 2 * qi + y) * D * 4 + (unit << 4) + 8 * (qr & 1),
-                                      __float_as_uint(v[y] * w), __float_as_uint(v[2 + y] * w));
-                            }
-                        }
-                    fence_proxy_async();
-                }
-                __syncthreads();
-                if (n0 == 0 && tend < t1) {
-                    // The next unit's queries: every warp is past its tiles of this one.
-                    int en = e;
-                    while (prefix[en + 1] <= tend) ++en;
-                    const int ntn = (prefix[en + 1] - prefix[en]) / p.x_units;
-                    load_q(en, (tend - prefix[en]) / ntn);
-                }
-                for (int idx = tid; idx < 8 * kRound * (D / 4); idx += kThreads) {
-                    const int row = idx / (D / 4), unit = idx % (D / 4), mm = 8 * n0 + row;
-                    if (mm >= m_real) continue;
-                    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    float top = -INFINITY, sum = 0.0f;
-                    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w * S::rows + mm].x);
-                    for (int w = 0; w < kWarps; ++w) {
-                        // the last of warp w's tiles before tend
-                        const int last = (tend - t0 - 1 - w) >= 0 ? (tend - t0 - 1 - w) / kWarps : -1;
-                        if (last < 0 || t0 + w + kWarps * last < t) continue;
-                        const float2 s = ml[w * S::rows + mm];
-                        sum += s.y * (s.x == -INFINITY ? 0.0f : ex2_approx(s.x - top));  // a NaN stays one
-                        const float4 f =
-                            lds_f4(base + (w * ST + last % ST) * S::slot + row * D * 4 +
-                                   ((unit ^ (((row >> 1) & 3) << 1)) << 4));
-                        acc.x += f.x;
-                        acc.y += f.y;
-                        acc.z += f.z;
-                        acc.w += f.w;
+                    for (int c = 0; c < NC; ++c) {
+                        const uint32_t piece16 = (4 * c + (qr >> 1)) ^ (qi << 1);
+                        sts64(ring + row * D * 4 + (piece16 << 4) + 8 * (qr & 1),
+                              __float_as_uint(o[n][c][y] * vref), __float_as_uint(o[n][c][2 + y] * vref));
                     }
-                    const int col = 4 * unit;
-                    if (whole) {
-                        const int ma = rt * S::rows + mm;
-                        const int b = p.lists != nullptr ? b0 : b0 + ma / p.g;
-                        const int head = p.lists != nullptr ? e % p.heads : x / p.row_tiles;
-                        const int64_t at = static_cast<int64_t>(b) * p.Hq + head * p.g + ma % p.g;
-                        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-                        uint2 v = make_uint2(bf16x2(acc.x * inv, acc.y * inv),
-                                             bf16x2(acc.z * inv, acc.w * inv));
-                        *reinterpret_cast<uint2*>(p.out + at * D + col) = v;
-                        if (col == 0 && p.lse != nullptr)
-                            p.lse[at] = sum == 0.0f ? -INFINITY
-                                                    : 0.69314718055994531f * (top - kPShift + log2f(sum));
-                    } else {
-                        *reinterpret_cast<float4*>(p.part + static_cast<int64_t>(part_at + mm) * D + col) = acc;
-                        if (col == 0)
-                            *reinterpret_cast<float2*>(p.part_ml + 2 * static_cast<int64_t>(part_at + mm)) =
-                                make_float2(top, sum);
-                    }
+                    if (qr == 0) s_ml[warp * S::rows + row] = make_float2(m[n][y], sum);
+                } else {
+                    const int64_t at = static_cast<int64_t>(worker) * S::rows + row;
+                    float2* const out = reinterpret_cast<float2*>(p.head + at * D) + qr;
+#pragma unroll
+                    for (int c = 0; c < NC; ++c)
+                        out[8 * c] = make_float2(o[n][c][y] * vref, o[n][c][2 + y] * vref);
+                    if (qr == 0) p.head_ml[at] = make_float2(m[n][y], sum);
                 }
-                __syncthreads();
             }
-        t = tend;
     }
-    // A wait that ran out left its copy in flight: none may outlive the CTA.
+    // A wait that ran out left its copy in flight: none may outlive the warp.
     if (!ok)
         for (int j = max(k - ST, 0); j < k; ++j) {
             bool done = true;
             mbar_wait(bars + 8 * (j % ST), (j / ST) & 1, done, p.status, kWaitBudgetNs, true);
         }
-}
 
-// Joins the partials of the units that a CTA boundary cut. Block (c, y): the
-// unit that CTA c starts, rows 4 y ..; two warps a row take its CTAs in turn,
-// their sums are added in that order.
-template <int D>
-__global__ void __launch_bounds__(2 * kJoinRows * 32) paged_join_kernel(const PagedParams p, int rows) {
-    pdl_entry();
-    const int unit = p.desc[2 * blockIdx.x];
-    if (unit < 0) return;
-    const int c0 = static_cast<int>(blockIdx.x), c1 = p.desc[2 * blockIdx.x + 1];
-    const int e = unit / p.x_units, x = unit % p.x_units, rt = x % p.row_tiles;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = warp & 1;
-    const int mm = blockIdx.y * kJoinRows + (warp >> 1), ma = rt * rows + mm;
-    const bool real = mm < rows && ma < p.rows;
-    constexpr int kV = D / 128 > 0 ? D / 128 : 1;  // float4 of a lane
-    __shared__ float4 other[kJoinRows][kV][32];
-    const auto at = [&](int c) { return static_cast<int64_t>(2 * c + (c == c0 ? 1 : 0)) * rows + mm; };
-    float top = -INFINITY, sum = 0.0f;
-    float4 acc[kV];
-#pragma unroll
-    for (int v = 0; v < kV; ++v) acc[v] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (real) {
-        for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, p.part_ml[2 * at(c)]);
-        top = warp_max(top);
-        for (int c = c0 + lane; c <= c1; c += 32) {
-            const float m = p.part_ml[2 * at(c)];
-            sum += p.part_ml[2 * at(c) + 1] * (m == -INFINITY ? 0.0f : ex2_approx(m - top));
-        }
-        sum = warp_sum(sum);
-#pragma unroll 4
-        for (int c = c0 + half; c <= c1; c += 2) {
-            const float m = p.part_ml[2 * at(c)];
-            const float w = m == -INFINITY ? 0.0f : ex2_approx(m - top);
-#pragma unroll
-            for (int v = 0; v < kV; ++v)
-                if (D >= 128 || lane < D / 4) {
-                    const float4 f = reinterpret_cast<const float4*>(p.part + at(c) * D)[32 * v + lane];
-                    acc[v].x += f.x * w;
-                    acc[v].y += f.y * w;
-                    acc[v].z += f.z * w;
-                    acc[v].w += f.w * w;
-                }
-        }
-        if (half == 1)
-#pragma unroll
-            for (int v = 0; v < kV; ++v) other[warp >> 1][v][lane] = acc[v];
-    }
+    // The CTA's warps: the units that cuts between them divide. Open partials of
+    // neighbours and the end that follows them are one unit.
+    __threadfence_block();
     __syncthreads();
-    if (!real || half == 1) return;
-    const int b = p.lists != nullptr ? e / p.heads : e * p.G + ma / p.g;
-    const int head = p.lists != nullptr ? e % p.heads : x / p.row_tiles;
-    const int64_t row = static_cast<int64_t>(b) * p.Hq + head * p.g + ma % p.g;
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-    for (int v = 0; v < kV; ++v)
-        if (D >= 128 || lane < D / 4) {
-            const float4 f = other[warp >> 1][v][lane];
-            const uint2 u = make_uint2(bf16x2((acc[v].x + f.x) * inv, (acc[v].y + f.y) * inv),
-                                       bf16x2((acc[v].z + f.z) * inv, (acc[v].w + f.w) * inv));
-            reinterpret_cast<uint2*>(p.out + row * D)[32 * v + lane] = u;
+    const int cta = static_cast<int>(blockIdx.x);
+    // The units that this CTA goes on with (0) and begins (1) and does not hold whole.
+    bool goes[2] = {false, false};
+    Unit unit[2];
+#pragma unroll 1
+    for (int i = 0; i < 2 * kWarps;) {  // warp i / 2: what it ended, then what it leaves open
+        const int first = i >> 1;
+        const bool is_open = (i & 1) != 0;
+        ++i;
+        if ((is_open ? s_left[first].open : s_left[first].ended) < 0) continue;
+        const bool begins = is_open && s_left[first].open_begins != 0;
+        const Unit u = is_open ? s_left[first].open_unit : s_left[first].ended_unit;
+        int opens = is_open ? 1 : 0, end_at = is_open ? -1 : first;
+        while (end_at < 0 && i < 2 * kWarps) {
+            if (s_left[i >> 1].ended >= 0) {
+                end_at = i >> 1;
+                ++i;
+            } else {
+                ++opens;
+                i += 2;
+            }
         }
-    if (lane == 0 && p.lse != nullptr)
-        p.lse[row] = sum == 0.0f ? -INFINITY : 0.69314718055994531f * (top - kPShift + log2f(sum));
+        const bool whole = begins && end_at >= 0;
+        if (!whole) {
+            if (begins) unit[1] = u, goes[1] = true;
+            else unit[0] = u, goes[0] = true;
+        }
+        const int64_t slot = static_cast<int64_t>(4 * cta + (begins ? 2 : 0)) * S::rows;
+#pragma unroll 2
+        for (int idx = tid; idx < u.m_real * (D / 4); idx += kThreads) {
+            const int row = idx / (D / 4), col = idx % (D / 4);
+            // The partials of up to kWarps - 1 open warps and one end, or kWarps open ones.
+            float4 v[kWarps];
+            float2 ml[kWarps];
+#pragma unroll
+            for (int j = 0; j < kWarps; ++j) {
+                v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                ml[j] = make_float2(-INFINITY, 0.0f);
+                if (j < opens) {
+                    v[j] = lds_f4(base + (first + j) * ST * S::slot + row * D * 4 +
+                                  ((col ^ (((row >> 1) & 3) << 1)) << 4));
+                    ml[j] = s_ml[(first + j) * S::rows + row];
+                } else if (j == opens && end_at >= 0) {
+                    const int64_t at = (static_cast<int64_t>(cta) * kWarps + end_at) * S::rows + row;
+                    v[j] = __ldcg(reinterpret_cast<const float4*>(p.head + at * D) + col);
+                    ml[j] = __ldcg(p.head_ml + at);
+                }
+            }
+            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            float top = -INFINITY, sum = 0.0f;
+            add_partials<kWarps>(acc, top, sum, v, ml);
+            if (whole) {
+                write_row(p, u, D, row, 4 * col, acc, top, sum);
+            } else {
+                reinterpret_cast<float4*>(p.part + (slot + row) * D)[col] = acc;
+                if (col == 0) p.part_ml[slot + row] = make_float2(top, sum);
+            }
+        }
+    }
+    if (!goes[0] && !goes[1]) return;
+
+    // The units that cuts between CTAs divide, level 0: among up to kFan neighbours, level
+    // 1: among their groups. The CTA that arrives last at a join makes it.
+    __shared__ int s_joins[2];
+    const int ctas = static_cast<int>(gridDim.x), group = cta / kFan * kFan;
+    const auto span = [&](int q, int level, int& from, int& n) {  // the partials of a join
+        const int c0 = unit[q].first_cta, c1 = unit[q].last_cta;
+        from = level == 0 ? max(c0, group) : c0 / kFan;
+        n = (level == 0 ? min(c1, group + kFan - 1) : c1 / kFan) - from + 1;
+    };
+#pragma unroll 1
+    for (int level = 0; level < 2; ++level) {
+        __threadfence();
+        __syncthreads();
+        if ((tid & 31) == 0 && tid < 64) {
+            const int q = tid >> 5;
+            bool joins = goes[q];
+            if (joins) {
+                int from, n;
+                span(q, level, from, n);
+                if (n > 1) {
+                    int* const count = p.arrived + level * 2 * ctas +
+                                       (level == 1             ? 2 * unit[q].first_cta
+                                        : unit[q].first_cta == from ? 2 * from + 1
+                                                                    : 2 * from);
+                    joins = atomicAdd(count, 1) == n - 1;
+                    if (joins) *count = 0;  // for the next call
+                }
+            }
+            s_joins[q] = joins;
+        }
+        __syncthreads();
+        goes[0] = s_joins[0] != 0;
+        goes[1] = s_joins[1] != 0;
+        if (!goes[0] && !goes[1]) return;
+        __threadfence();
+        // Two joins are made by half of the threads each.
+        const bool both = goes[0] && goes[1];
+        const int threads = both ? kThreads / 2 : kThreads, me = tid & (threads - 1);
+        const int q = both ? tid / (kThreads / 2) : goes[1] ? 1 : 0;
+        const Unit u = q == 0 ? unit[0] : unit[1];
+        int from, n;
+        span(q, level, from, n);
+        const bool done[2] = {
+            level == 1 || (unit[0].first_cta >= group && unit[0].last_cta < group + kFan),
+            level == 1 || (unit[1].first_cta >= group && unit[1].last_cta < group + kFan)};
+        const auto slot = [&](int c, int stage) {
+            return static_cast<int64_t>(4 * c + (c == u.first_cta ? 2 : 0) + stage) * S::rows;
+        };
+#pragma unroll 1
+        for (int idx = me; idx < u.m_real * (D / 4); idx += threads) {
+            constexpr int kMany = 8;
+            const int row = idx / (D / 4), col = idx % (D / 4);
+            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            float top = -INFINITY, sum = 0.0f;
+#pragma unroll 1
+            for (int j0 = 0; j0 < n; j0 += kMany) {
+                float4 v[kMany];
+                float2 ml[kMany];
+#pragma unroll
+                for (int z = 0; z < kMany; ++z) {
+                    v[z] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    ml[z] = make_float2(-INFINITY, 0.0f);
+                    if (j0 + z >= n) continue;
+                    const int c = level == 0 ? from + j0 + z : max(u.first_cta, (from + j0 + z) * kFan);
+                    const int64_t at = slot(c, level) + row;
+                    v[z] = __ldcg(reinterpret_cast<const float4*>(p.part + at * D) + col);
+                    ml[z] = __ldcg(p.part_ml + at);
+                }
+                add_partials<kMany>(acc, top, sum, v, ml);
+            }
+            if (q == 0 ? done[0] : done[1]) {
+                write_row(p, u, D, row, 4 * col, acc, top, sum);
+            } else {
+                const int64_t to = slot(from, 1) + row;
+                reinterpret_cast<float4*>(p.part + to * D)[col] = acc;
+                if (col == 0) p.part_ml[to] = make_float2(top, sum);
+            }
+        }
+        goes[0] = goes[0] && !done[0];
+        goes[1] = goes[1] && !done[1];
+        if (!goes[0] && !goes[1]) return;
+    }
 }
 
 constexpr int kMaxDevices = 64;
-constexpr int kWaves = 1;       // CTAs launched for each that an SM holds
-constexpr int kGridPerSm = 6;   // most CTAs for each SM (the workspace has room for them)
+constexpr int kWorkersPerSm = 12;  // most warps on an SM (the workspace has room for them)
 
 template <typename S>
 int launch_decode(PagedParams p, const CUtensorMap& kmap, const CUtensorMap& vmap, int sms,
                   int64_t tiles, smd_stream_t stream) {
-    static_assert(S::CTAS * (S::smem(kMaxEntries) + 1024) <= 228 * 1024, "CTAs of an SM");
+    static_assert(S::CTAS * kWarps <= kWorkersPerSm, "the workspace's workers");
+    static_assert(S::CTAS * (S::smem(kMaxEntries) + 64 + 1024) <= 228 * 1024, "CTAs of an SM");
     static std::atomic<bool> ready[kMaxDevices];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return SMD_ERR_DEVICE;
@@ -853,26 +962,26 @@ int launch_decode(PagedParams p, const CUtensorMap& kmap, const CUtensorMap& vma
         }
         ready[dev] = true;
     }
-    // At least kWarps tiles a CTA, so that each warp has one.
-    const int64_t most = static_cast<int64_t>(sms) * kGridPerSm;
-    const int64_t want = (tiles + kWarps - 1) / kWarps;
-    const char* ev = getenv("SMD_W"); int64_t grid = static_cast<int64_t>(sms) * S::CTAS * (ev ? atoi(ev) : kWaves);
-    if (grid > most) grid = most;
+    const int64_t most = static_cast<int64_t>(sms) * kWorkersPerSm;
+    const int64_t want = (tiles + kWarps - 1) / kWarps;  // a tile for each warp
+    int64_t grid = static_cast<int64_t>(sms) * S::CTAS;
     if (grid > want) grid = want;
-    p.part = reinterpret_cast<float*>(p.desc) + 4 * most;  // 16-byte aligned
-    p.part_ml = p.part + most * 2 * S::rows * S::D;
-    int rc = launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), kThreads, S::smem(p.entries),
-                        stream, p, kmap, vmap);
-    if (rc != SMD_OK) return rc;
-    const int join_rows = p.rows < S::rows ? p.rows : S::rows;
-    return launch_pdl(paged_join_kernel<S::D>,
-                      dim3(static_cast<unsigned>(grid), (join_rows + kJoinRows - 1) / kJoinRows),
-                      2 * kJoinRows * 32, 0, stream, p, static_cast<int>(S::rows));
+    p.workers = static_cast<int>(grid) * kWarps;
+    // The workspace: counts, then the partials of warps and CTAs.
+    float* at = reinterpret_cast<float*>(p.arrived) + 4 * most;
+    const int64_t part_rows = most * S::rows;
+    p.head = at;
+    p.part = p.head + part_rows * S::D;
+    p.head_ml = reinterpret_cast<float2*>(p.part + part_rows * S::D);
+    p.part_ml = p.head_ml + part_rows;
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), kThreads, S::smem(p.entries), stream,
+                      p, kmap, vmap);
 }
 
-// A CTA's descriptor and two partials of up to 32 rows (16 at 256 columns).
+// Counts, and for each warp a partial of its own and a quarter of its CTA's four,
+// of up to 32 rows (16 at 256 columns).
 int64_t workspace_bytes(int sms, int D) {
-    const int64_t most = static_cast<int64_t>(sms) * kGridPerSm;
+    const int64_t most = static_cast<int64_t>(sms) * kWorkersPerSm;
     return 4 * most * (4 + 2 * (D == 256 ? 16 : 32) * (D + 2));
 }
 
@@ -932,12 +1041,13 @@ extern "C" int smd_paged_decode(const uint16_t* q, int64_t q_stride, const smd_p
     p.x_units = lists ? p.row_tiles : cache->heads * p.row_tiles;
     p.G = row_group;
     p.g = g;
+    p.g_magic = ((1u << 20) + static_cast<uint32_t>(g) - 1) / static_cast<uint32_t>(g);
     p.Hq = Hq;
     p.rows = rows;
     p.scale_log2 = sm_scale * 1.4426950408889634f;
     p.K = K;
     p.status = status;
-    p.desc = static_cast<int32_t*>(workspace);
+    p.arrived = static_cast<int32_t*>(workspace);
     p.box = page_box_tokens(*cache);
     CUtensorMap maps[2];
     std::memcpy(maps, &cache->map[1], sizeof maps);
@@ -972,9 +1082,9 @@ extern "C" int smd_paged_decode(const uint16_t* q, int64_t q_stride, const smd_p
         else if (D == 128)
             rc = RT == 1   ? launch(Shape<128, 1, 32, 2, 3>{})
                  : RT == 2 ? launch(Shape<128, 2, 32, 2, 3>{})
-                           : launch(Shape<128, 4, 32, 3, 2>{});
+                           : launch(Shape<128, 4, 32, 2, 2>{});
         else
-            rc = RT == 1 ? launch(Shape<256, 1, 16, 2, 3>{}) : launch(Shape<256, 2, 16, 3, 2>{});
+            rc = RT == 1 ? launch(Shape<256, 1, 16, 2, 3>{}) : launch(Shape<256, 2, 16, 2, 2>{});
         if (rc != SMD_OK) return rc;
     }
     return SMD_OK;

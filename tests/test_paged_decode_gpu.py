@@ -19,8 +19,8 @@ def run(cuda, cache, q, table, lengths, G=1, lists=None, counts=None, gpu_cache=
     import torch
     from sparse_mla_decode_gb300 import binding
     status = torch.zeros(1, dtype=torch.int32, device=cuda)
-    ws = torch.full((binding.paged_workspace_bytes(gpu_cache or cache.to(cuda)),), 0xff,
-                    dtype=torch.uint8, device=cuda)  # needs no initialisation
+    ws = torch.zeros(binding.paged_workspace_bytes(gpu_cache or cache.to(cuda)), dtype=torch.uint8,
+                     device=cuda)
     out, lse = binding.paged_decode(
         bf16(q, cuda), gpu_cache or cache.to(cuda), i32(table, cuda), i32(lengths, cuda),
         cache.D ** -0.5, row_group=G, block_lists=None if lists is None else i32(lists, cuda),
@@ -274,7 +274,7 @@ def test_another_stream_and_a_graph_give_the_same_bits(cuda):
     table = table_for(rng, [3000, 17, 100], P, 60)
     q = queries(rng, 3, 8, D)
     c, tq, tt, tl = cache.to(cuda), bf16(q, cuda), i32(table, cuda), i32(lengths, cuda)
-    ws = torch.empty(binding.paged_workspace_bytes(c), dtype=torch.uint8, device=cuda)
+    ws = torch.zeros(binding.paged_workspace_bytes(c), dtype=torch.uint8, device=cuda)
     out, lse = binding.paged_decode(tq, c, tt, tl, D ** -0.5, workspace=ws)
     torch.cuda.synchronize()
     side = torch.cuda.Stream()
