@@ -8,12 +8,17 @@
 // so a page stays if any of them may need it; one bf16 rounding at the end.
 //
 // What bounds it: 4 D bytes of bounds for each (page, head), read once, 4 D M
-// FLOPs with them: HBM. So nothing is staged: a warp takes 8 pages (the columns
-// of the MMA), a lane reads 16-byte pieces of one page's bounds straight into
-// the operand registers. The contraction index is permuted to allow it: lane
-// 4 g + i holds columns 32 j + 8 i .. + 7 of page g, and the query fragments,
-// in shared memory, are read in the same order. The M query rows pass over
-// these registers 16 at a time.
+// FLOPs with them: HBM. So nothing is staged: a warp takes 16 pages (the rows of
+// the MMA), a lane reads 16-byte pieces of two pages' bounds straight into the
+// operand registers. The contraction index is permuted to allow it: lane
+// 4 g + i holds columns 32 j + 8 i .. + 7 of pages g and g + 8, and the query
+// fragments q+ and q-, in shared memory in the order of the lanes, are made to
+// match. The query rows pass over these registers 8 at a time.
+//
+// Measured (GB300): 48 requests of 8192 .. 131072 tokens in pages of 64, 8 heads of
+// 128 columns: 35 us for 8 query rows a head (84% of the copy rate for the 201
+// MB), 40 us for 16 rows, 95 us for 64 rows, where each 8 more rows cost 8 us of
+// MMAs and of shared-memory reads.
 #include "smd_internal.h"
 #include "smd_paged.h"
 #include "smd_ptx.cuh"
@@ -23,8 +28,10 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kSteps = 4;                          // groups of 8 pages of a warp
-constexpr int kPagesPerBlock = 8 * kWarps * kSteps;
+constexpr int kGroup = 16 * kWarps;  // pages that a block's warps take at once
+// Such turns of a block: the waits for length, page and query are paid once a block. The
+// 201 MB above take 42 us at one turn, 36 at two, 35 at four, 38 at eight (too few blocks).
+constexpr int kMostSteps = 4;
 
 struct ScoreParams {
     const uint16_t* q;
@@ -39,9 +46,10 @@ struct ScoreParams {
     int32_t keep_first, keep_last;
     uint16_t* scores;
     int64_t score_stride;
-    int32_t lanes;      // rows of the MMA that one verify row takes: a power of two up to 16
-    int32_t parts;      // MMAs that one verify row takes (more than 16 query heads)
-    int32_t m_tiles;    // MMAs over all rows
+    int32_t cols;       // columns of the MMA that one verify row takes: a power of two up to 8
+    int32_t parts;      // MMAs that one verify row takes (more than 8 query heads)
+    int32_t tiles;      // MMAs over all rows
+    int32_t steps;      // turns of a block
 };
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -64,28 +72,16 @@ __device__ __forceinline__ uint32_t neg2(uint32_t v) {
     return r;
 }
 
-// Query row of MMA row `s` of tile mt: verify row i and head j of the group.
-// Rows beyond the heads repeat the last one, which leaves the maximum as it is.
-__device__ __forceinline__ void row_of(const ScoreParams& p, int mt, int s, int& i, int& j) {
-    if (p.parts > 1) {
-        i = p.i0 + mt / p.parts;
-        j = (mt % p.parts) * 16 + s;
-    } else {
-        i = p.i0 + mt * (16 / p.lanes) + s / p.lanes;
-        j = s % p.lanes;
-    }
-    i = min(i, p.i_end - 1);
-    j = min(j, p.g - 1);
-}
-
 template <int D>
 __global__ void __launch_bounds__(kThreads) block_scores_kernel(const ScoreParams p) {
-    constexpr int kPitch = 2 * D + 64;  // 16-byte reads of two rows hit different banks
-    constexpr int kJ = D / 32;          // 16-byte pieces of a lane, per bound
+    constexpr int kJ = D / 32;  // 16-byte pieces of a lane, per bound and page
     extern __shared__ __align__(16) uint8_t smem[];
+    // [tiles][kJ][sign][32 lanes]: the second operand's registers of two MMAs
+    uint4* const qs = reinterpret_cast<uint4*>(smem);
+    __shared__ int s_sees[kPagedMaxGroup];  // pages that a verify row sees
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, gi = lane & 3;
     const int head = blockIdx.y, r = blockIdx.z + p.r0;
-    const int first = blockIdx.x * kPagesPerBlock + warp * 8 * kSteps;
+    const int block0 = blockIdx.x * kGroup * p.steps, block1 = block0 + kGroup * p.steps;
     pdl_entry();
     const int len = max(min(p.lengths[r], p.width * p.P), 0);
     const int have = (len + p.P - 1) / p.P;  // pages that the last verify row sees
@@ -94,125 +90,154 @@ __global__ void __launch_bounds__(kThreads) block_scores_kernel(const ScoreParam
     // Pages that no row sees: NaN.
     for (int i = p.i0; i < p.i_end; ++i) {
         uint16_t* const row = p.scores + ((b0 + i) * p.heads + head) * p.score_stride;
-        for (int c = max(have, static_cast<int>(blockIdx.x) * kPagesPerBlock) + tid;
-             c < min(static_cast<int>(blockIdx.x + 1) * kPagesPerBlock, p.width); c += kThreads)
+        for (int c = max(have, block0) + tid; c < min(block1, p.width); c += kThreads)
             row[c] = 0x7fffu;
     }
-    if (static_cast<int>(blockIdx.x) * kPagesPerBlock >= have) return;
+    if (block0 >= have) return;
 
-    int page[kSteps];
+    // The pages of a turn, one turn ahead of the bounds; those are on their way while the
+    // products of the turn before (at first, while the queries) are dealt with.
+    int page[2];
+    const auto look_up = [&](int c0) {
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-        const int c = first + 8 * s + gr;
-        page[s] = c < have ? p.table[r * p.table_stride + c] : -1;
-    }
-    for (int idx = tid; idx < p.m_tiles * 16 * (D / 8); idx += kThreads) {
-        const int row = idx / (D / 8), c = idx % (D / 8);
-        int i, j;
-        row_of(p, row >> 4, row & 15, i, j);
-        *reinterpret_cast<uint4*>(smem + row * kPitch + 16 * c) = *reinterpret_cast<const uint4*>(
-            p.q + (b0 + i) * p.q_stride + static_cast<int64_t>(head * p.g + j) * D + 8 * c);
+        for (int z = 0; z < 2; ++z) {
+            const int c = c0 + 8 * z + gr;
+            page[z] = c < min(have, block1) ? p.table[r * p.table_stride + c] : -1;
+        }
+    };
+    uint4 hi[2][kJ], lo[2][kJ];
+    const auto load = [&]() {
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+            const int pg = page[z];
+#pragma unroll
+            for (int j = 0; j < kJ; ++j) hi[z][j] = lo[z][j] = make_uint4(0, 0, 0, 0);
+            if (pg >= 0 && pg < p.pages) {
+                const uint4* const b = reinterpret_cast<const uint4*>(
+                    p.bounds + (static_cast<int64_t>(pg) * p.heads + head) * 2 * D + 8 * gi);
+#pragma unroll
+                for (int j = 0; j < kJ; ++j) {
+                    hi[z][j] = __ldcs(b + 4 * j);
+                    lo[z][j] = __ldcs(b + D / 8 + 4 * j);
+                }
+            }
+        }
+    };
+    look_up(block0 + 16 * warp);
+    load();
+    look_up(block0 + 16 * warp + kGroup);
+    if (tid < p.i_end - p.i0)
+        s_sees[tid] = (max(len - p.G + 1 + p.i0 + tid, 0) + p.P - 1) / p.P;
+    for (int idx = tid; idx < p.tiles * kJ * 32; idx += kThreads) {
+        // Column l / 4 of a tile, the pieces of lane l. Columns beyond the heads repeat the
+        // last one, which leaves the maximum as it is.
+        const int l = idx & 31, j = (idx >> 5) % kJ, tile = (idx >> 5) / kJ;
+        int i, a;
+        if (p.parts > 1) {
+            i = tile / p.parts;
+            a = (tile % p.parts) * 8 + (l >> 2);
+        } else {
+            i = (tile * 8 + (l >> 2)) / p.cols;
+            a = (l >> 2) % p.cols;
+        }
+        i = min(p.i0 + i, p.i_end - 1);
+        a = min(a, p.g - 1);
+        const uint4 v = *reinterpret_cast<const uint4*>(
+            p.q + (b0 + i) * p.q_stride + static_cast<int64_t>(head * p.g + a) * D + 32 * j + 8 * (l & 3));
+        uint4* const to = qs + static_cast<int64_t>(tile * kJ + j) * 64 + l;
+        to[0] = make_uint4(pos2(v.x), pos2(v.y), pos2(v.z), pos2(v.w));
+        to[32] = make_uint4(neg2(v.x), neg2(v.y), neg2(v.z), neg2(v.w));
     }
     __syncthreads();
 
 #pragma unroll 1
-    for (int s = 0; s < kSteps; ++s) {
-        const int c0 = first + 8 * s;
-        if (c0 >= have) break;
-        uint4 hi[kJ], lo[kJ];
-        const int pg = page[s];
-        if (pg >= 0 && pg < p.pages) {
-            const uint4* const b = reinterpret_cast<const uint4*>(
-                p.bounds + (static_cast<int64_t>(pg) * p.heads + head) * 2 * D + 8 * gi);
-#pragma unroll
-            for (int j = 0; j < kJ; ++j) {
-                hi[j] = __ldcs(b + 4 * j);
-                lo[j] = __ldcs(b + D / 8 + 4 * j);
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < kJ; ++j) hi[j] = lo[j] = make_uint4(0, 0, 0, 0);
-        }
-        float run[4];
+    for (int c0 = block0 + 16 * warp; c0 < min(have, block1); c0 += kGroup) {
+        float run[2] = {0.0f, 0.0f};
 #pragma unroll 1
-        for (int mt = 0; mt < p.m_tiles; ++mt) {
-            float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            const uint8_t* const q0 = smem + (mt * 16 + gr) * kPitch + 16 * gi;
+        for (int tile = 0; tile < p.tiles; ++tile) {
+            // page g: columns 2 i, 2 i + 1; page g + 8. Four sums, so that the MMAs do not wait
+            // for one another.
+            float d[4] = {}, d1[4] = {}, d2[4] = {}, d3[4] = {};
+            const uint4* const q = qs + static_cast<int64_t>(tile) * kJ * 64 + lane;
 #pragma unroll
             for (int j = 0; j < kJ; ++j) {
-                const uint4 x = *reinterpret_cast<const uint4*>(q0 + 64 * j);
-                const uint4 y = *reinterpret_cast<const uint4*>(q0 + 8 * kPitch + 64 * j);
-                mma_bf16(d, pos2(x.x), pos2(y.x), pos2(x.y), pos2(y.y), hi[j].x, hi[j].y);
-                mma_bf16(d, neg2(x.x), neg2(y.x), neg2(x.y), neg2(y.y), lo[j].x, lo[j].y);
-                mma_bf16(d, pos2(x.z), pos2(y.z), pos2(x.w), pos2(y.w), hi[j].z, hi[j].w);
-                mma_bf16(d, neg2(x.z), neg2(y.z), neg2(x.w), neg2(y.w), lo[j].z, lo[j].w);
+                const uint4 a = q[j * 64], b = q[j * 64 + 32];
+                mma_bf16(d, hi[0][j].x, hi[1][j].x, hi[0][j].y, hi[1][j].y, a.x, a.y);
+                mma_bf16(d1, hi[0][j].z, hi[1][j].z, hi[0][j].w, hi[1][j].w, a.z, a.w);
+                mma_bf16(d2, lo[0][j].x, lo[1][j].x, lo[0][j].y, lo[1][j].y, b.x, b.y);
+                mma_bf16(d3, lo[0][j].z, lo[1][j].z, lo[0][j].w, lo[1][j].w, b.z, b.w);
             }
-            // The largest over a verify row's MMA rows: lanes of equal gi, and for
-            // 16 of them both halves.
 #pragma unroll
-            for (int o = 4; o < 32; o <<= 1) {
-                if (o >= 4 * p.lanes) break;
-#pragma unroll
-                for (int z = 0; z < 4; ++z) d[z] = fmaxf(d[z], __shfl_xor_sync(0xffffffffu, d[z], o));
+            for (int z = 0; z < 4; ++z) d[z] = (d[z] + d1[z]) + (d2[z] + d3[z]);
+            // The largest over a verify row's columns.
+            if (p.cols >= 2) {
+                d[0] = fmaxf(d[0], d[1]);
+                d[2] = fmaxf(d[2], d[3]);
             }
-            if (p.lanes == 16) {
-                d[0] = d[2] = fmaxf(d[0], d[2]);
-                d[1] = d[3] = fmaxf(d[1], d[3]);
+            if (p.cols >= 4) {
+                d[0] = fmaxf(d[0], __shfl_xor_sync(0xffffffffu, d[0], 1));
+                d[2] = fmaxf(d[2], __shfl_xor_sync(0xffffffffu, d[2], 1));
             }
+            if (p.cols >= 8) {
+                d[0] = fmaxf(d[0], __shfl_xor_sync(0xffffffffu, d[0], 2));
+                d[2] = fmaxf(d[2], __shfl_xor_sync(0xffffffffu, d[2], 2));
+            }
+            int i = (tile * 8 + 2 * gi) / p.cols;
             if (p.parts > 1) {
-                const int part = mt % p.parts;
-#pragma unroll
-                for (int z = 0; z < 4; ++z) run[z] = part == 0 ? d[z] : fmaxf(run[z], d[z]);
+                i = tile / p.parts;
+                const int part = tile - i * p.parts;
+                run[0] = part == 0 ? d[0] : fmaxf(run[0], d[0]);
+                run[1] = part == 0 ? d[2] : fmaxf(run[1], d[2]);
                 if (part + 1 < p.parts) continue;
-#pragma unroll
-                for (int z = 0; z < 4; ++z) d[z] = run[z];
+                d[0] = run[0];
+                d[2] = run[1];
             }
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                if (y == 1 && p.lanes == 16) break;
-                const int row = 8 * y + gr;
-                const int i =
-                    p.i0 + (p.parts > 1 ? mt / p.parts : mt * (16 / p.lanes) + row / p.lanes);
-                if (row % p.lanes != 0 || i >= p.i_end) continue;
-                const int sees = (max(len - p.G + 1 + i, 0) + p.P - 1) / p.P;
-                uint16_t* const out =
-                    p.scores + ((b0 + i) * p.heads + head) * p.score_stride + c0 + 2 * gi;
+            if ((2 * gi & (p.cols - 1)) != 0) continue;
+            for (int y = 0; y < (p.cols == 1 ? 2 : 1); ++y, ++i) {
+                if (p.i0 + i >= p.i_end) break;
+                const int sees = s_sees[i];
+                uint16_t* const out = p.scores + ((b0 + p.i0 + i) * p.heads + head) * p.score_stride;
 #pragma unroll
                 for (int z = 0; z < 2; ++z) {
-                    const int c = c0 + 2 * gi + z;
-                    if (c >= have) continue;
-                    uint16_t v = static_cast<uint16_t>(bf16x2(d[2 * y + z], 0.0f) & 0xffffu);
+                    const int c = c0 + 8 * z + gr;
+                    uint16_t v = static_cast<uint16_t>(bf16x2(y == 0 ? d[2 * z] : d[2 * z + 1], 0.0f));
                     if (c < p.keep_first || c >= sees - p.keep_last) v = 0x7f80u;
                     if (c >= sees) v = 0x7fffu;
-                    out[z] = v;
+                    if (c < have) out[c] = v;
                 }
             }
         }
+        load();
+        look_up(c0 + 2 * kGroup);
     }
 }
 
 template <int D>
-int launch_scores(ScoreParams p, int R, smd_stream_t stream) {
-    constexpr int kTile = 16 * (2 * D + 64), kMost = 176 * 1024;  // shared bytes of an MMA's rows
-    static_assert(kMost / kTile >= kPagedMaxHeads / 16, "a verify row's query heads fit");
-    if (p.m_tiles * kTile > 48 * 1024 &&
+int launch_scores(ScoreParams p, int R, int sms, smd_stream_t stream) {
+    constexpr int kTile = 32 * D, kMost = 176 * 1024;  // shared bytes of an MMA's columns
+    static_assert(kMost / kTile >= kPagedMaxHeads / 8, "a verify row's query heads fit");
+    if (p.tiles * kTile > 48 * 1024 &&
         cudaFuncSetAttribute(block_scores_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kMost) != cudaSuccess) {
         (void)cudaGetLastError();
         return SMD_ERR_DEVICE;
     }
-    const unsigned gx = static_cast<unsigned>((p.width + kPagesPerBlock - 1) / kPagesPerBlock);
+    // Turns of a block: few where there are few pages, so that the blocks still fill the device.
+    const int64_t groups = (static_cast<int64_t>(p.width) + kGroup - 1) / kGroup;
+    p.steps = kMostSteps;
+    while (p.steps > 1 && groups / p.steps * p.heads * R < 8ll * sms) p.steps /= 2;
+    const unsigned gx = static_cast<unsigned>((groups + p.steps - 1) / p.steps);
     // Verify rows of one launch: all of them, unless many query heads fill the shared memory.
-    const int rows = p.m_tiles * kTile <= kMost ? p.G : kMost / kTile / p.parts;
+    const int rows = p.tiles * kTile <= kMost ? p.G : kMost / kTile / p.parts;
     for (p.i0 = 0; p.i0 < p.G; p.i0 += rows) {
         p.i_end = p.i0 + rows < p.G ? p.i0 + rows : p.G;
         const int n = p.i_end - p.i0;
-        p.m_tiles = p.parts > 1 ? n * p.parts : (n * p.lanes + 15) / 16;
+        p.tiles = p.parts > 1 ? n * p.parts : (n * p.cols + 7) / 8;
         for (p.r0 = 0; p.r0 < R; p.r0 += 65535) {
             const int z = R - p.r0 < 65535 ? R - p.r0 : 65535;
             const int rc = launch_pdl(
                 block_scores_kernel<D>, dim3(gx, static_cast<unsigned>(p.heads), static_cast<unsigned>(z)),
-                kThreads, static_cast<size_t>(p.m_tiles) * kTile, stream, p);
+                kThreads, static_cast<size_t>(p.tiles) * kTile, stream, p);
             if (rc != SMD_OK) return rc;
         }
     }
@@ -237,7 +262,8 @@ extern "C" int smd_block_scores(const uint16_t* q, int64_t q_stride, const smd_p
     if (skip) return SMD_OK;
     if (scores == nullptr) return SMD_ERR_NULL;
     if (!aligned(scores, 2)) return SMD_ERR_ALIGN;
-    if (device_sms() <= 0) return SMD_ERR_DEVICE;
+    const int sms = device_sms();
+    if (sms <= 0) return SMD_ERR_DEVICE;
     ScoreParams p{};
     p.q = q;
     p.q_stride = q_stride;
@@ -255,11 +281,11 @@ extern "C" int smd_block_scores(const uint16_t* q, int64_t q_stride, const smd_p
     p.keep_last = keep_last;
     p.scores = scores;
     p.score_stride = score_stride;
-    p.lanes = 1;
-    while (p.lanes < p.g && p.lanes < 16) p.lanes *= 2;
-    p.parts = (p.g + 15) / 16;
-    p.m_tiles = p.parts > 1 ? p.G * p.parts : (p.G * p.lanes + 15) / 16;
-    return cache->head_dim == 64    ? launch_scores<64>(p, R, stream)
-           : cache->head_dim == 128 ? launch_scores<128>(p, R, stream)
-                                    : launch_scores<256>(p, R, stream);
+    p.cols = 1;
+    while (p.cols < p.g && p.cols < 8) p.cols *= 2;
+    p.parts = (p.g + 7) / 8;
+    p.tiles = p.parts > 1 ? p.G * p.parts : (p.G * p.cols + 7) / 8;
+    return cache->head_dim == 64    ? launch_scores<64>(p, R, sms, stream)
+           : cache->head_dim == 128 ? launch_scores<128>(p, R, sms, stream)
+                                    : launch_scores<256>(p, R, sms, stream);
 }
