@@ -917,11 +917,14 @@ class PagedCache:
         return cls(codes(), codes(), scale(), scale(), b)
 
 
-def _stream(stream, t) -> int:
-    import torch
+def _so() -> ctypes.CDLL:
+    return _lib if _lib is not None else lib()  # no lock once it is loaded
 
+
+def _stream(stream, t) -> int:
     if stream is None:
-        return torch.cuda.current_stream(t.device).cuda_stream
+        import torch
+        return torch._C._cuda_getCurrentRawStream(t.device.index)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -930,6 +933,14 @@ def _vector(t, name: str, dtype, n: int | None = None):
         raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor")
     if n is not None and t.numel() < n:
         raise ValueError(f"{name} must have at least {n} elements")
+
+
+def _output(t, name: str, dtype, n: int, like):
+    if t is None:
+        import torch
+        return torch.empty(n, dtype=dtype, device=like.device)
+    _vector(t, name, dtype, n)
+    return t
 
 
 def block_tables(lengths, new_tokens, table, ring, state, page_size: int, max_tokens: int | None = None,
@@ -957,20 +968,14 @@ def block_tables(lengths, new_tokens, table, ring, state, page_size: int, max_to
         slots = torch.empty(int(max_tokens), dtype=torch.int32, device=lengths.device)
     T = slots.numel()
 
-    def made(t, name, dtype, n):
-        if t is None:
-            return torch.empty(n, dtype=dtype, device=lengths.device)
-        _vector(t, name, dtype, n)
-        return t
-
-    new_lengths = made(new_lengths, "new_lengths", torch.int32, R)
-    new_state = made(new_state, "new_state", torch.int64, 2)
-    starts = made(starts, "starts", torch.int32, R + 1)
-    slots = made(slots, "slots", torch.int32, T)
-    positions = made(positions, "positions", torch.int32, T)
+    new_lengths = _output(new_lengths, "new_lengths", torch.int32, R, lengths)
+    new_state = _output(new_state, "new_state", torch.int64, 2, lengths)
+    starts = _output(starts, "starts", torch.int32, R + 1, lengths)
+    _vector(slots, "slots", torch.int32)
+    positions = _output(positions, "positions", torch.int32, T, lengths)
     if new_lengths.data_ptr() == lengths.data_ptr() and R or new_state.data_ptr() == state.data_ptr():
         raise ValueError("new_lengths and new_state may not be lengths and state")
-    rc = lib().smd_block_tables(
+    rc = _so().smd_block_tables(
         lengths.data_ptr(), new_tokens.data_ptr(), R, table.data_ptr(), table.stride(0),
         table.shape[1], ring.data_ptr(), ring.numel(), state.data_ptr(), page_size, T,
         new_lengths.data_ptr(), new_state.data_ptr(), starts.data_ptr(), slots.data_ptr(),
@@ -996,7 +1001,7 @@ def paged_append(cache: PagedCache, k, v, slots, stream=None) -> None:
         if t.stride(2) != 1 or (cache.heads > 1 and t.stride(1) != cache.head_dim):
             raise ValueError(f"{name}: a token's heads must be contiguous")
     row = cache.heads * cache.head_dim
-    rc = lib().smd_paged_append(cache.ref, k.data_ptr(), k.stride(0) if T > 1 else row, v.data_ptr(),
+    rc = _so().smd_paged_append(cache.ref, k.data_ptr(), k.stride(0) if T > 1 else row, v.data_ptr(),
                                 v.stride(0) if T > 1 else row, slots.data_ptr(), T,
                                 _stream(stream, slots))
     if rc != SMD_OK:
@@ -1041,7 +1046,7 @@ def block_scores(q, cache: PagedCache, table, lengths, row_group: int = 1, keep_
         raise ValueError(f"out must be a bfloat16 CUDA tensor [{B}, {cache.heads}, {width}] with "
                          "evenly spaced rows")
     stride = out.stride(1) if cache.heads > 1 else out.stride(0) if B > 1 else width
-    rc = lib().smd_block_scores(*args, keep_first, keep_last, out.data_ptr(), stride,
+    rc = _so().smd_block_scores(*args, keep_first, keep_last, out.data_ptr(), stride,
                                 _stream(stream, q))
     if rc != SMD_OK:
         raise SmdError(rc, "smd_block_scores")
@@ -1093,7 +1098,7 @@ def paged_decode(q, cache: PagedCache, table, lengths, sm_scale: float, row_grou
         workspace = torch.zeros(paged_workspace_bytes(cache), dtype=torch.uint8, device=q.device)
     elif not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
-    rc = lib().smd_paged_decode(
+    rc = _so().smd_paged_decode(
         *args, sm_scale, _ptr(block_lists) if K or block_lists is None else workspace.data_ptr(),
         _ptr(block_counts), K, out.data_ptr(), lse.data_ptr(),
         _ptr(status), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
