@@ -62,8 +62,8 @@ constexpr int kMaxEntries = 1024;  // requests (or (row, kv head) lists) of one 
 constexpr int kNoPos = 0x3fffffff; // the position of tokens that no row sees
 constexpr float kPShift = 7.0f;    // weights are formed at 2^7 of the maximum kept
 constexpr float kSlack = 8.0f;     // which is moved when a logit exceeds it by 2^8
-constexpr int kUnitCost = 2;       // what a unit's begin and end cost a warp, in tiles
-constexpr int kMinTiles = 1;       // least tiles of a warp
+constexpr int kUnitCost = 3;       // what a unit's begin and end cost a warp, in tiles
+constexpr int kMinTiles = 2;       // least range of a warp, in tiles
 constexpr int kFan = 32;           // neighbouring CTAs of a first join
 
 struct PagedParams {
@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
     const auto find_entry = [&](int t) { return find(t, 0); };
     const int cost = total + kUnitCost * p.x_units * p.entries;
     const int worker = static_cast<int>(blockIdx.x) * kWarps + warp;
-    const int per = max((cost + p.workers - 1) / p.workers, kMinTiles + kUnitCost);
+    const int per = max((cost + p.workers - 1) / p.workers, kMinTiles);
     const auto tiles_before = [&](int64_t at) {  // tiles that lie before a cost position
         if (at >= cost) return total;
         const int c = static_cast<int>(at), e = find(c, kUnitCost);
@@ -464,20 +464,28 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
 #pragma unroll 1
     for (int s = 0; s < ST; ++s) issue(s);
 
+    // The unit of tile t: entry e, unit x of its x_units, each of nt tiles.
+    int nt = 1, x = 0;
+    if (t0 < t1) {
+        nt = (prefix[e + 1] - prefix[e]) / p.x_units;
+        x = (t0 - prefix[e]) / nt;
+    }
+    const auto unit_at = [&](int ue, int ux) {
+        Unit u;
+        const int rt = p.row_tiles == 1 ? 0 : ux % p.row_tiles;
+        u.b0 = lists ? ue / p.heads : ue * p.G;
+        u.head = lists ? ue - u.b0 * p.heads : p.row_tiles == 1 ? ux : ux / p.row_tiles;
+        u.m0 = rt * S::rows;
+        u.m_real = min(p.rows - u.m0, S::rows);
+        return u;
+    };
+    Unit u{};
+    if (t0 < t1) u = unit_at(e, x);
+
 #pragma unroll 1
     while (t < t1) {
-        while (prefix[e + 1] <= t) ++e;
-        const int nt = (prefix[e + 1] - prefix[e]) / p.x_units, x = (t - prefix[e]) / nt;
         const int u0 = prefix[e] + x * nt, u1 = u0 + nt, tend = min(u1, t1);
-        const int len = lens[e], b0 = lists ? e / p.heads : e * p.G;
-        Unit u;
-        {
-            const int rt = x % p.row_tiles;
-            u.b0 = b0;
-            u.head = lists ? e - b0 * p.heads : x / p.row_tiles;
-            u.m0 = rt * S::rows;
-            u.m_real = min(p.rows - u.m0, S::rows);
-        }
+        const int len = lens[e], b0 = u.b0;
         const int m_real = u.m_real;
         // The tokens that row m of the tile sees.
         const auto row_limit = [&](int m) {
@@ -528,6 +536,23 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
                 } else {
                     sts64(q_at + (n * NC + c) * 256, f0, f1);  // read by this lane only
                 }
+            }
+        }
+        // The unit after it, if this warp has some of that: its queries come into L1 meanwhile.
+        int e_next = e, x_next = x + 1;
+        Unit u_next{};
+        if (tend < t1) {
+            if (x_next == p.x_units) {
+                ++e_next;  // every entry has a tile
+                x_next = 0;
+            }
+            u_next = unit_at(e_next, x_next);
+            constexpr int kLines = D / 64;  // 128-byte lines of a row
+            for (int i = lane; i < u_next.m_real * kLines; i += 32) {
+                const int row = i / kLines;
+                asm volatile("prefetch.global.L1 [%0];" ::"l"(
+                    p.q + u_next.b(p, row) * p.q_stride +
+                    static_cast<int64_t>(u_next.a(p, row)) * D + i % kLines * 64));
             }
         }
         float m[RT][2], l[RT][2], o[RT][NC][4], vref = 0.0f;
@@ -605,27 +630,31 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
                             for (int z = 0; z < 2; ++z)
                                 if (pos[h] + qr + 8 * z >= lim) s[h][n][2 * z + y] = -INFINITY;
                     }
-                // V of tokens that no row sees becomes 0 (0 times a NaN would not be).
-#pragma unroll 1
-                for (int z = lane; z < KT * NC; z += 32) {
-                    const int j = z / NC;
-                    if ((j < 16 ? pos[0] : pos[1]) + (j & 15) >= max_lim)
-                        sts_zero16(vs_at + piece<D, KT>(j, z % NC));
-                }
-                // V of tokens that some rows see and others do not: a NaN goes to the rows
-                // that see it here, and 0 stands in its place for the products.
-                if (min_lim < max_lim) {
-#pragma unroll 1
-                    for (int j = 0; j < KT; ++j) {
-                        const int at = (j < 16 ? pos[0] : pos[1]) + (j & 15);
-                        if (at < min_lim || at >= max_lim) continue;
-                        bool nan = false;
-#pragma unroll 1
-                        for (int z = lane; z < 4 * NC; z += 32) {
-                            const uint32_t w = lds_u32(vs_at + piece<D, KT>(j, z >> 2) + 4 * (z & 3));
-                            nan = nan || (((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0;
+#pragma unroll
+                for (int h = 0; h < NH; ++h) {
+                    // V of tokens that no row sees becomes 0 (0 times a NaN would not be).
+                    if (pos[h] + 15 >= max_lim) {
+#pragma unroll
+                        for (int z = 0; z < 16 * NC; z += 32) {
+                            const int j = (z + lane) / NC;
+                            if (pos[h] + j >= max_lim)
+                                sts_zero16(vs_at + piece<D, KT>(16 * h + j, (z + lane) % NC));
                         }
-                        if (!__any_sync(0xffffffffu, nan)) continue;
+                    }
+                    // V of tokens that some rows see and others do not: a NaN goes to the rows
+                    // that see it here, and 0 stands in its place for the products.
+#pragma unroll 1
+                    for (int at = max(min_lim, pos[h]); at < min(max_lim, pos[h] + 16); ++at) {
+                        const int j = 16 * h + at - pos[h];
+                        uint32_t nan = 0;
+#pragma unroll
+                        for (int z = 0; z < 4 * NC; z += 32)
+                            if (z + lane < 4 * NC) {
+                                const uint32_t w = lds_u32(vs_at + piece<D, KT>(j, (z + lane) >> 2) +
+                                                           4 * (lane & 3));
+                                nan |= ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+                            }
+                        if (!__any_sync(0xffffffffu, nan != 0)) continue;
 #pragma unroll
                         for (int c = 0; c < NC; ++c) {
                             const uint32_t a = vs_at + piece<D, KT>(j, c) + 4 * (qr >> 1);
@@ -785,6 +814,12 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
                     if (qr == 0) p.head_ml[at] = make_float2(m[n][y], sum);
                 }
             }
+        if (tend < t1) {
+            if (e_next != e) nt = (prefix[e_next + 1] - prefix[e_next]) / p.x_units;
+            e = e_next;
+            x = x_next;
+            u = u_next;
+        }
     }
     // A wait that ran out left its copy in flight: none may outlive the warp.
     if (!ok)
