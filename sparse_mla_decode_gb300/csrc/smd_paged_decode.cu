@@ -324,16 +324,12 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
             return max((n + KT - 1) / KT, 1) * p.x_units;
         };
         constexpr int kPer = kMaxEntries / kThreads;
+        const int each = (p.entries + kThreads - 1) / kThreads;  // entries of a thread
         int v[kPer], sum = 0;
-        const int each = p.entries <= kThreads ? 1 : kPer;  // entries of a thread
-        if (each == 1) {
-            v[0] = sum = tiles_of(tid);
-        } else {
 #pragma unroll
-            for (int j = 0; j < kPer; ++j) {
-                v[j] = tiles_of(tid * kPer + j);
-                sum += v[j];
-            }
+        for (int j = 0; j < kPer; ++j) {
+            v[j] = j < each ? tiles_of(tid * each + j) : 0;
+            sum += v[j];
         }
         int inc = sum;
 #pragma unroll
@@ -351,15 +347,10 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
             if (w < warp) before += scan[w];
             total += scan[w];
         }
-        if (each == 1) {
-            if (tid < p.entries) prefix[tid] = before;
-        } else {
 #pragma unroll
-            for (int j = 0; j < kPer; ++j) {
-                const int e = tid * kPer + j;
-                if (e < p.entries) prefix[e] = before;
-                before += v[j];
-            }
+        for (int j = 0; j < kPer; ++j) {
+            if (j < each && tid * each + j < p.entries) prefix[tid * each + j] = before;
+            before += v[j];
         }
         if (tid == 0) prefix[p.entries] = total;
     }
@@ -942,33 +933,51 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
             return static_cast<int64_t>(4 * c + (c == u.first_cta ? 2 : 0) + stage) * S::rows;
         };
 #pragma unroll 1
-        for (int idx = me; idx < u.m_real * (D / 4); idx += threads) {
+        for (int i0 = me; i0 < u.m_real * (D / 4); i0 += 2 * threads) {
+            // Two pieces of 4 columns, 8 partials of each: one round trip.
             constexpr int kMany = 8;
-            const int row = idx / (D / 4), col = idx % (D / 4);
-            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            float top = -INFINITY, sum = 0.0f;
+            int row[2], col[2];
+            float4 acc[2];
+            float top[2], sum[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                row[i] = min((i0 + i * threads) / (D / 4), u.m_real - 1);
+                col[i] = (i0 + i * threads) % (D / 4);
+                acc[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                top[i] = -INFINITY;
+                sum[i] = 0.0f;
+            }
 #pragma unroll 1
             for (int j0 = 0; j0 < n; j0 += kMany) {
-                float4 v[kMany];
-                float2 ml[kMany];
+                float4 v[2][kMany];
+                float2 ml[2][kMany];
 #pragma unroll
                 for (int z = 0; z < kMany; ++z) {
-                    v[z] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    ml[z] = make_float2(-INFINITY, 0.0f);
-                    if (j0 + z >= n) continue;
                     const int c = level == 0 ? from + j0 + z : max(u.first_cta, (from + j0 + z) * kFan);
-                    const int64_t at = slot(c, level) + row;
-                    v[z] = __ldcg(reinterpret_cast<const float4*>(p.part + at * D) + col);
-                    ml[z] = __ldcg(p.part_ml + at);
+                    const int64_t at = slot(c, level);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        v[i][z] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        ml[i][z] = make_float2(-INFINITY, 0.0f);
+                        if (j0 + z < n) {
+                            v[i][z] = __ldcg(reinterpret_cast<const float4*>(p.part + (at + row[i]) * D) + col[i]);
+                            ml[i][z] = __ldcg(p.part_ml + at + row[i]);
+                        }
+                    }
                 }
-                add_partials<kMany>(acc, top, sum, v, ml);
+                add_partials<kMany>(acc[0], top[0], sum[0], v[0], ml[0]);
+                add_partials<kMany>(acc[1], top[1], sum[1], v[1], ml[1]);
             }
-            if (q == 0 ? done[0] : done[1]) {
-                write_row(p, u, D, row, 4 * col, acc, top, sum);
-            } else {
-                const int64_t to = slot(from, 1) + row;
-                reinterpret_cast<float4*>(p.part + to * D)[col] = acc;
-                if (col == 0) p.part_ml[to] = make_float2(top, sum);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (i0 + i * threads >= u.m_real * (D / 4)) break;
+                if (q == 0 ? done[0] : done[1]) {
+                    write_row(p, u, D, row[i], 4 * col[i], acc[i], top[i], sum[i]);
+                } else {
+                    const int64_t to = slot(from, 1) + row[i];
+                    reinterpret_cast<float4*>(p.part + to * D)[col[i]] = acc[i];
+                    if (col[i] == 0) p.part_ml[to] = make_float2(top[i], sum[i]);
+                }
             }
         }
         goes[0] = goes[0] && !done[0];
