@@ -884,14 +884,15 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
     }
     if (!goes[0] && !goes[1]) return;
 
-    // The units that cuts between CTAs divide, level 0: among up to kFan neighbours, level
-    // 1: among their groups. The CTA that arrives last at a join makes it.
+    // The units that cuts between CTAs divide, level 0: among kFan neighbours from the unit's
+    // first CTA on, level 1: among these groups. The CTA that arrives last at a join
+    // makes it.
     __shared__ int s_joins[2];
-    const int ctas = static_cast<int>(gridDim.x), group = cta / kFan * kFan;
-    const auto span = [&](int q, int level, int& from, int& n) {  // the partials of a join
+    const int ctas = static_cast<int>(gridDim.x);
+    const auto span = [&](int q, int level, int& from, int& n) {  // the first CTA of a join, its partials
         const int c0 = unit[q].first_cta, c1 = unit[q].last_cta;
-        from = level == 0 ? max(c0, group) : c0 / kFan;
-        n = (level == 0 ? min(c1, group + kFan - 1) : c1 / kFan) - from + 1;
+        from = level == 0 ? c0 + (cta - c0) / kFan * kFan : c0;
+        n = level == 0 ? min(c1, from + kFan - 1) - from + 1 : (c1 - c0) / kFan + 1;
     };
 #pragma unroll 1
     for (int level = 0; level < 2; ++level) {
@@ -905,9 +906,7 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
                 span(q, level, from, n);
                 if (n > 1) {
                     int* const count = p.arrived + level * 2 * ctas +
-                                       (level == 1             ? 2 * unit[q].first_cta
-                                        : unit[q].first_cta == from ? 2 * from + 1
-                                                                    : 2 * from);
+                                       2 * from + (unit[q].first_cta == from ? 1 : 0);
                     joins = atomicAdd(count, 1) == n - 1;
                     if (joins) *count = 0;  // for the next call
                 }
@@ -927,8 +926,8 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
         int from, n;
         span(q, level, from, n);
         const bool done[2] = {
-            level == 1 || (unit[0].first_cta >= group && unit[0].last_cta < group + kFan),
-            level == 1 || (unit[1].first_cta >= group && unit[1].last_cta < group + kFan)};
+            level == 1 || unit[0].last_cta - unit[0].first_cta < kFan,
+            level == 1 || unit[1].last_cta - unit[1].first_cta < kFan};
         const auto slot = [&](int c, int stage) {
             return static_cast<int64_t>(4 * c + (c == u.first_cta ? 2 : 0) + stage) * S::rows;
         };
@@ -953,7 +952,7 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
                 float2 ml[2][kMany];
 #pragma unroll
                 for (int z = 0; z < kMany; ++z) {
-                    const int c = level == 0 ? from + j0 + z : max(u.first_cta, (from + j0 + z) * kFan);
+                    const int c = from + (j0 + z) * (level == 0 ? 1 : kFan);
                     const int64_t at = slot(c, level);
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
