@@ -12,15 +12,18 @@
 // dependent loads slot -> x -> scale -> (kept codes) for a decode step.
 //
 // D / 8 lanes hold a token, 8 columns (16 bytes of bf16) each. Few tokens: one such
-// group of lanes takes a run of one head and side. Many: a block looks up the
-// runs that start in its chunk of tokens and deals (run, head, side) to its
-// warps; a warp keeps a run's values in registers between the maximum and the
-// encoding (32 tokens of 256 columns, 64 of 128, 128 of 64; what is longer is
-// read again, from L2), so that 16 KB a warp are on their way at a time.
+// group of lanes takes a run of one head and side. Many: a block of four warps
+// looks up the runs that start in its chunk of tokens and writes them for one head:
+// long ones together (two warps the keys, two the values), shorter ones by a warp
+// or a group of lanes each. A warp keeps its values in registers between the
+// maximum and the encoding (of a run, 32 tokens of 256 columns, 64 of 128, 128
+// of 64; what is longer is read again, from L2), so that 8 KB a warp and 160
+// KB an SM are on their way at a time.
 //
 // Measured (GB300): 96 tokens of as many requests, 8 heads of 128 columns, 2.9 us; 28
-// thousand tokens of 23 requests 41 us (62% of the copy rate for the 173 MB: a
-// warp's loads, maximum and stores follow one another, 12 warps an SM).
+// thousand tokens of 23 requests 38 us (68% of the copy rate for the 173 MB: the
+// slots, a run's loads, its maximum and its stores follow one another, and 20 warps
+// an SM do not quite cover that), 16 thousand of one 37 us (79%).
 #include "smd_internal.h"
 #include "smd_paged.h"
 #include "smd_ptx.cuh"
@@ -68,13 +71,6 @@ __device__ __forceinline__ float power_of(float a) {
     int e = static_cast<int>(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
     e = max(e, kMinExponent);
     return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-}
-
-// x / scale. A product where the scale is a power of two (kExact: the quotient has no
-// rounding either way); the branch between the two is taken once for a run.
-template <bool kExact>
-__device__ __forceinline__ float quotient(float x, float scale, float inv) {
-    return kExact ? x * inv : __fdiv_rn(x, scale);
 }
 
 __device__ __forceinline__ bool is_power(float scale) { return (__float_as_uint(scale) & 0x7fffffu) == 0; }
@@ -125,27 +121,47 @@ __device__ __forceinline__ void write_bounds(uint16_t* bounds, int D, int col, i
     b[D / 8] = make_uint4(finite2(lo[0]), finite2(lo[1]), finite2(lo[2]), finite2(lo[3]));
 }
 
-// Takes 8 values into the extremes and the largest size.
-__device__ __forceinline__ void take(const uint4& v, uint32_t (&hi)[4], uint32_t (&lo)[4], uint32_t& big) {
+// Takes 8 values into the extremes.
+__device__ __forceinline__ void take(const uint4& v, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         hi[j] = bmax2(hi[j], w[j]);
         lo[j] = bmin2(lo[j], w[j]);
-        big = bmax2(big, w[j] & 0x7fff7fffu);
     }
 }
 
+// The largest size: the largest of hi and -lo, or 0 where nothing but NaN was met
+// (hi is then -infinity, lo infinity).
+__device__ __forceinline__ float largest(const uint32_t (&hi)[4], const uint32_t (&lo)[4]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m = bmax2(m, finite2(bmax2(hi[j], lo[j] ^ 0x80008000u)));
+    return fmaxf(lo_f(m), hi_f(m));
+}
+
+// Eight values over the scale. A product where the scale is a power of two (kExact: the
+// quotient has no rounding either way); the branch between the two is taken once for
+// a run.
 template <bool kExact>
 __device__ __forceinline__ uint2 encode8(const uint4& v, float scale, float inv) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    float f[8];
+    uint32_t c[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        f[2 * j] = quotient<kExact>(lo_f(w[j]), scale, inv);
-        f[2 * j + 1] = quotient<kExact>(hi_f(w[j]), scale, inv);
+        float x = lo_f(w[j]), y = hi_f(w[j]);
+        if (kExact) {  // both products at once
+            asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %2};\n\t"
+                "mul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+                : "+f"(x), "+f"(y)
+                : "f"(inv));
+        } else {
+            x = __fdiv_rn(x, scale);
+            y = __fdiv_rn(y, scale);
+        }
+        c[j] = e4m3x2(x, y);
     }
-    return make_uint2(encode4(f[0], f[1], f[2], f[3]), encode4(f[4], f[5], f[6], f[7]));
+    return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
 }
 
 // Writes the first o tokens of a page again at a larger scale: lane i of N.
@@ -189,7 +205,7 @@ __device__ __forceinline__ void write_run(const AppendParams& p, const Run& r, i
         v[k] = make_uint4(0, 0, 0, 0);
         if (m < r.n) v[k] = __ldcs(reinterpret_cast<const uint4*>(x + m * xs));
     }
-    uint32_t hi[4], lo[4], big = 0;
+    uint32_t hi[4], lo[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         hi[j] = 0xff80ff80u;  // -infinity
@@ -197,11 +213,11 @@ __device__ __forceinline__ void write_run(const AppendParams& p, const Run& r, i
     }
 #pragma unroll
     for (int k = 0; k < kKept; ++k)
-        if (t_in + k * kStep < r.n) take(v[k], hi, lo, big);
+        if (t_in + k * kStep < r.n) take(v[k], hi, lo);
 #pragma unroll 8
     for (int m = t_in + kKept * kStep; m < r.n; m += kStep)
-        take(*reinterpret_cast<const uint4*>(x + m * xs), hi, lo, big);
-    float a = fmaxf(lo_f(finite2(big)), hi_f(finite2(big)));
+        take(*reinterpret_cast<const uint4*>(x + m * xs), hi, lo);
+    float a = largest(hi, lo);
 #pragma unroll
     for (int s = 1; s < N; s <<= 1) a = fmaxf(a, __shfl_xor_sync(mask, a, s));
     if (side == 0 && p.bounds != nullptr) {
@@ -235,6 +251,97 @@ __device__ __forceinline__ void write_run(const AppendParams& p, const Run& r, i
     } else {  // a kept scale that the caller has set: larger than the run's own, nothing is re-encoded
 #pragma unroll 1
         for (int m = t_in; m < r.n; m += kStep)
+            *reinterpret_cast<uint2*>(pool + (o + m) * ts + col) =
+                encode8<false>(*reinterpret_cast<const uint4*>(x + m * xs), now, inv);
+    }
+}
+
+// What the warps of a block tell one another of a run.
+template <int D>
+struct RunShared {
+    float a[4];
+    uint4 hi[D / 8], lo[D / 8];
+};
+
+// One run of one head by a block of four warps: two for the keys and two for the
+// values, each every second step of tokens. The first kKept values of a lane
+// stay in registers.
+template <int kKept, int D>
+__device__ __forceinline__ void write_run_block(const AppendParams& p, const Run& r, int head, int warp,
+                                                int lane, RunShared<D>& shared) {
+    constexpr int kCols = D / 8, kStep = 32 / kCols;
+    const int side = warp >> 1, half = warp & 1;
+    const int col = (lane % kCols) * 8, t_in = lane / kCols + half * kStep;
+    const int page = r.slot / p.P, o = r.slot - page * p.P;
+    const int64_t xs = p.x_stride[side], at = static_cast<int64_t>(page) * p.heads + head;
+    const uint16_t* const x = p.x[side] + r.t * xs + head * D + col;
+    float* const scale = p.scale[side] + at;
+    uint4 v[kKept];
+#pragma unroll
+    for (int k = 0; k < kKept; ++k) {
+        const int m = t_in + 2 * k * kStep;
+        v[k] = make_uint4(0, 0, 0, 0);
+        if (m < r.n) v[k] = __ldcs(reinterpret_cast<const uint4*>(x + m * xs));
+    }
+    const float old = o > 0 ? *scale : __uint_as_float(static_cast<uint32_t>(kMinExponent + 127) << 23);
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        hi[j] = 0xff80ff80u;  // -infinity
+        lo[j] = 0x7f807f80u;
+    }
+#pragma unroll
+    for (int k = 0; k < kKept; ++k)
+        if (t_in + 2 * k * kStep < r.n) take(v[k], hi, lo);
+#pragma unroll 4
+    for (int m = t_in + 2 * kKept * kStep; m < r.n; m += 2 * kStep)
+        take(*reinterpret_cast<const uint4*>(x + m * xs), hi, lo);
+    const float a = warp_max(largest(hi, lo));
+    const bool bounds = side == 0 && p.bounds != nullptr;
+    if (bounds) {
+#pragma unroll
+        for (int s = kCols; s < 32; s <<= 1)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                hi[j] = bmax2(hi[j], __shfl_xor_sync(0xffffffffu, hi[j], s));
+                lo[j] = bmin2(lo[j], __shfl_xor_sync(0xffffffffu, lo[j], s));
+            }
+        if (half == 1 && lane < kCols) {
+            shared.hi[lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            shared.lo[lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+    }
+    if (lane == 0) shared.a[warp] = a;
+    __syncthreads();
+    const float now = fmaxf(power_of(fmaxf(a, shared.a[warp ^ 1])), old);
+    if (bounds && half == 0 && lane < kCols) {
+        const uint4 h = shared.hi[lane], l = shared.lo[lane];
+        hi[0] = bmax2(hi[0], h.x), hi[1] = bmax2(hi[1], h.y);
+        hi[2] = bmax2(hi[2], h.z), hi[3] = bmax2(hi[3], h.w);
+        lo[0] = bmin2(lo[0], l.x), lo[1] = bmin2(lo[1], l.y);
+        lo[2] = bmin2(lo[2], l.z), lo[3] = bmin2(lo[3], l.w);
+        write_bounds(p.bounds + at * 2 * D, D, col, o, hi, lo);
+    }
+    __syncthreads();  // shared is free again, and every thread has read the old scale
+    if (half == 0 && lane == 0) *scale = now;
+    const float inv = 1.0f / now;
+    uint8_t* const pool = p.pool[side] + page * p.stride[side][0] + head * p.stride[side][1];
+    const int64_t ts = p.stride[side][2];
+    if (is_power(now)) {
+        if (o > 0 && now > old) reencode_kept<64, D>(pool, ts, o, old, inv, half * 32 + lane);
+#pragma unroll
+        for (int k = 0; k < kKept; ++k) {
+            const int m = t_in + 2 * k * kStep;
+            if (m < r.n)
+                *reinterpret_cast<uint2*>(pool + (o + m) * ts + col) = encode8<true>(v[k], now, inv);
+        }
+#pragma unroll 4
+        for (int m = t_in + 2 * kKept * kStep; m < r.n; m += 2 * kStep)
+            *reinterpret_cast<uint2*>(pool + (o + m) * ts + col) =
+                encode8<true>(*reinterpret_cast<const uint4*>(x + m * xs), now, inv);
+    } else {  // a kept scale that the caller has set: larger than the run's own, nothing is re-encoded
+#pragma unroll 1
+        for (int m = t_in; m < r.n; m += 2 * kStep)
             *reinterpret_cast<uint2*>(pool + (o + m) * ts + col) =
                 encode8<false>(*reinterpret_cast<const uint4*>(x + m * xs), now, inv);
     }
@@ -275,20 +382,21 @@ __global__ void __launch_bounds__(kThreads) append_few_kernel(const AppendParams
 
 constexpr int kChunk = 64;      // tokens of a block
 constexpr int kMostPage = 256;  // tokens of a page
-constexpr int kHeads = 2;       // heads of a block
+
 constexpr int kShort = 4;       // runs up to this length go to D / 8 lanes each
 
-// A block for each chunk of tokens and kHeads heads: it takes the runs that start
-// in its chunk.
+// A block for each chunk of tokens and head: it takes the runs that start in its
+// chunk.
 template <int D>
-__global__ void __launch_bounds__(kThreads, 3) append_many_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kThreads, 5) append_many_kernel(const AppendParams p) {
     constexpr int N = D / 8, kWarps = kThreads / 32;
+    constexpr int kMedium = 8 * (32 / N);  // runs up to this length go to a warp each
     __shared__ int s_slot[kChunk];
     __shared__ int2 s_runs[kChunk];  // first token and length: short runs from the front, long from the back
     __shared__ uint32_t s_goes[(kChunk + kMostPage) / 32], s_lead[kChunk / 32];
     __shared__ int s_short, s_long;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int head0 = blockIdx.y * kHeads, heads = min(kHeads, p.heads - head0);
+    const int head = blockIdx.y;
     if (tid == 0) s_short = s_long = 0;
     pdl_entry();
     const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kChunk;
@@ -329,20 +437,23 @@ __global__ void __launch_bounds__(kThreads, 3) append_many_kernel(const AppendPa
         s_runs[at] = make_int2(tid, n);
     }
     __syncthreads();
-    for (int u = warp; u < s_long * heads * 2; u += kWarps) {
-        const int run = u / (heads * 2), hs = u - run * heads * 2;
-        const int2 r = s_runs[kChunk - 1 - run];
-        const Run one{t0 + r.x, r.y, s_slot[r.x]};
-        if (r.y <= 8 * (32 / N))
-            write_run<32, 8, D>(p, one, head0 + (hs >> 1), hs & 1, lane, 0xffffffffu);
-        else
-            write_run<32, 32, D>(p, one, head0 + (hs >> 1), hs & 1, lane, 0xffffffffu);
+    __shared__ RunShared<D> s_run;
+#pragma unroll 1
+    for (int u = 0; u < s_long; ++u) {
+        const int2 r = s_runs[kChunk - 1 - u];
+        if (r.y > kMedium) write_run_block<16, D>(p, Run{t0 + r.x, r.y, s_slot[r.x]}, head, warp, lane, s_run);
+    }
+#pragma unroll 1
+    for (int u = warp; u < 2 * s_long; u += kWarps) {
+        const int2 r = s_runs[kChunk - 1 - (u >> 1)];
+        if (r.y <= kMedium)
+            write_run<32, 8, D>(p, Run{t0 + r.x, r.y, s_slot[r.x]}, head, u & 1, lane, 0xffffffffu);
     }
     const unsigned mask = group_mask<N>(lane);
-    for (int u = tid / N; u < s_short * heads * 2; u += kThreads / N) {
-        const int run = u / (heads * 2), hs = u - run * heads * 2;
-        const int2 r = s_runs[run];
-        write_run<N, 1, D>(p, Run{t0 + r.x, r.y, s_slot[r.x]}, head0 + (hs >> 1), hs & 1, tid % N, mask);
+#pragma unroll 1
+    for (int u = tid / N; u < 2 * s_short; u += kThreads / N) {
+        const int2 r = s_runs[u >> 1];
+        write_run<N, 1, D>(p, Run{t0 + r.x, r.y, s_slot[r.x]}, head, u & 1, tid % N, mask);
     }
 }
 
@@ -350,7 +461,7 @@ template <int D>
 int launch_append(const AppendParams& p, int sms, smd_stream_t stream) {
     // Few tokens: lanes for each token. Many: blocks by chunks of tokens. 8 heads of 128
     // columns, few / many: 1000 tokens of as many requests 5.8 / 44 us, 900 tokens of 30
-    // requests 15 / 18 us, 4000 tokens of one request 52 / 16 us.
+    // requests 15 / 18 us, 4000 tokens of one request 52 / 15 us.
     const int64_t units = static_cast<int64_t>(p.T) * p.heads * 2;
     if (units <= static_cast<int64_t>(sms) * 256)
         return launch_pdl(append_few_kernel<D>,
@@ -358,7 +469,7 @@ int launch_append(const AppendParams& p, int sms, smd_stream_t stream) {
                           kThreads, 0, stream, p);
     return launch_pdl(append_many_kernel<D>,
                       dim3(static_cast<unsigned>((p.T + kChunk - 1) / kChunk),
-                           static_cast<unsigned>((p.heads + kHeads - 1) / kHeads)),
+                           static_cast<unsigned>(p.heads)),
                       kThreads, 0, stream, p);
 }
 
