@@ -46,8 +46,6 @@
 // never sees its range.
 #include <atomic>
 #include <cstring>
-#include <cstdlib>
-#include <cstdlib>
 
 #include "smd_internal.h"
 #include "smd_paged.h"
@@ -704,21 +702,22 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
                     }
             }
 
-            // weights and the second product
+            // weights and the second product, relative to the largest scale of V so far
+            const float vtop = fmaxf(vs[0], vs[NH - 1]);
+            if (vtop > vref) {
+                const float down = vref / vtop;
+                vref = vtop;
+#pragma unroll
+                for (int n = 0; n < RT; ++n)
+#pragma unroll
+                    for (int c = 0; c < NC; ++c)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) o[n][c][j] *= down;
+            }
+            uint32_t pb[NH][RT][2];
 #pragma unroll
             for (int h = 0; h < NH; ++h) {
-                if (vs[h] > vref) {
-                    const float down = vref / vs[h];
-                    vref = vs[h];
-#pragma unroll
-                    for (int n = 0; n < RT; ++n)
-#pragma unroll
-                        for (int c = 0; c < NC; ++c)
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) o[n][c][j] *= down;
-                }
                 const float ratio = vref > 0.0f ? vs[h] / vref : 0.0f;
-                uint32_t pb[RT][2];
 #pragma unroll
                 for (int n = 0; n < RT; ++n) {
                     float w[4];
@@ -732,9 +731,12 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
                             w[2 * z + y] = pv * ratio;
                         }
                     }
-                    pb[n][0] = transpose8x8(f16x2(w[0], w[1]));
-                    pb[n][1] = transpose8x8(f16x2(w[2], w[3]));
+                    pb[h][n][0] = transpose8x8(f16x2(w[0], w[1]));
+                    pb[h][n][1] = transpose8x8(f16x2(w[2], w[3]));
                 }
+            }
+#pragma unroll
+            for (int h = 0; h < NH; ++h) {
 #pragma unroll
                 for (int c = 0; c < NC; c += 2) {
                     uint32_t vr[4];
@@ -746,7 +748,7 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
                         e4m3_to_f16(__byte_perm(vr[2 * z + 1], 0, 0x3120), a[2], a[3]);
 #pragma unroll
                         for (int n = 0; n < RT; ++n)
-                            mma_f16(o[n][c + z], a[0], a[1], a[2], a[3], pb[n][0], pb[n][1]);
+                            mma_f16(o[n][c + z], a[0], a[1], a[2], a[3], pb[h][n][0], pb[h][n][1]);
                     }
                 }
             }
@@ -1096,7 +1098,7 @@ extern "C" int smd_paged_decode(const uint16_t* q, int64_t q_stride, const smd_p
     std::memcpy(maps, &cache->map[1], sizeof maps);
 
     // Requests of one launch: their entries fit the prefix table, their tiles an int.
-    const int64_t per_entry = (static_cast<int64_t>(lists ? K : width) * P + KT - 1) / KT + 1;
+    const int64_t per_entry = (static_cast<int64_t>(lists ? K : width) * P + KT - 1) / KT + 1 + kUnitCost;
     const int64_t per_request =
         static_cast<int64_t>(lists ? row_group * cache->heads : 1) * p.x_units * per_entry;
     const int entries_of = lists ? row_group * cache->heads : 1;
