@@ -94,7 +94,6 @@ struct PagedParams {
                         // what its group of CTAs has of it; the same of the unit that it begins
     float2* head_ml;    // the same without columns: maximum, sum
     float2* part_ml;
-    int32_t box;        // tokens of a copy box
 };
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -185,10 +184,11 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
 }
 
 // The sizes of one instantiation: D columns, RT tiles of 8 query rows, KT
-// tokens a tile, ST slots of a warp's ring, CTAs an SM holds.
-template <int D_, int RT_, int KT_, int ST_, int CTAS_>
+// tokens a tile, from one page or (NP = 2) a page for each half, ST slots of a
+// warp's ring, CTAs an SM holds.
+template <int D_, int RT_, int KT_, int NP_, int ST_, int CTAS_>
 struct Shape {
-    static constexpr int D = D_, RT = RT_, KT = KT_, ST = ST_, CTAS = CTAS_;
+    static constexpr int D = D_, RT = RT_, KT = KT_, NP = NP_, ST = ST_, CTAS = CTAS_;
     static constexpr int rows = 8 * RT;
     static constexpr int row_bytes = D < 128 ? D : 128;  // of a copy box
     static constexpr int side = KT * D;                  // bytes of a tile's K, and of its V
@@ -213,12 +213,12 @@ __device__ __forceinline__ uint32_t piece(int row, int c) {
     return (c >> 3) * (KT * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
 }
 
-// One tile's tokens: for each 16 of them the page, the offset in it, the first
-// token's position in its request and the scales.
-template <int NH>
+// One tile's tokens: for each page the offset in it, the first token's position
+// in its request and the scales.
+template <int NP>
 struct Tile {
-    int page[NH], off[NH], pos[NH], head;
-    float ks[NH], vs[NH];
+    int page[NP], off[NP], pos[NP], head;
+    float ks[NP], vs[NP];
 };
 
 // A unit's row tile: its query rows as rows of the batch and query heads, and the
@@ -284,6 +284,7 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
                         const __grid_constant__ CUtensorMap vmap) {
     constexpr int D = S::D, RT = S::RT, KT = S::KT, ST = S::ST;
     constexpr int NH = KT / 16;   // 16-token halves of a tile
+    constexpr int NP = S::NP;     // its pages
     constexpr int NC = D / 16;    // 16-column chunks
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
@@ -380,11 +381,11 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
     const int t0 = __shfl_sync(0xffffffffu, cut, 0), t1 = __shfl_sync(0xffffffffu, cut, 1);
 
     // Lane l resolves tile t0 + 32 * (k / 32) + l.
-    Tile<NH> td;
+    Tile<NP> td;
     const auto resolve = [&](int kk) {
         const int t = t0 + kk;
 #pragma unroll
-        for (int h = 0; h < NH; ++h) {
+        for (int h = 0; h < NP; ++h) {
             td.page[h] = -1;
             td.off[h] = 0;
             td.pos[h] = kNoPos;
@@ -400,9 +401,9 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
         td.head = lists ? e - b * p.heads : x / p.row_tiles;
         const int32_t* const row = p.table + static_cast<int64_t>(r) * p.table_stride;
 #pragma unroll
-        for (int h = 0; h < NH; ++h) {
-            int blk = (first + 16 * h) / p.page_size;
-            const int off = first + 16 * h - blk * p.page_size;
+        for (int h = 0; h < NP; ++h) {
+            int blk = (first + KT / NP * h) / p.page_size;
+            const int off = first + KT / NP * h - blk * p.page_size;
             if (lists) {
                 const int c = p.counts != nullptr ? max(min(p.counts[e], p.K), 0) : p.K;
                 blk = blk < c ? p.lists[static_cast<int64_t>(e) * p.K + blk] : -1;
@@ -429,18 +430,17 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
             const uint32_t bar = bars + 8 * s, dst = ring + s * S::slot;
             mbar_arrive_expect_tx(bar, S::slot);
 #pragma unroll
-            for (int h = 0; h < NH; ++h) {
-                if (h > 0 && p.box != 16) break;
+            for (int h = 0; h < NP; ++h) {
 #pragma unroll
                 for (int sub = 0; sub < (D > 128 ? 2 : 1); ++sub) {
-                    const uint32_t at = dst + sub * KT * 128 + h * 16 * S::row_bytes;
+                    const uint32_t at = dst + sub * KT * 128 + h * (KT / NP) * S::row_bytes;
                     tma_load_4d(at, &kmap, sub * 128, td.off[h], td.head, td.page[h], bar);
                     tma_load_4d(at + S::side, &vmap, sub * 128, td.off[h], td.head, td.page[h],
                                 bar);
                 }
             }
-            sts_v4(meta + 32 * s, make_float4(td.ks[0], td.ks[NH - 1], td.vs[0], td.vs[NH - 1]));
-            sts64(meta + 32 * s + 16, td.pos[0], td.pos[NH - 1]);
+            sts_v4(meta + 32 * s, make_float4(td.ks[0], td.ks[NP - 1], td.vs[0], td.vs[NP - 1]));
+            sts64(meta + 32 * s + 16, td.pos[0], td.pos[NP - 1] + (NP == 1 ? 16 : 0));
         }
         __syncwarp();
     };
@@ -544,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
                     static_cast<int64_t>(u_next.a(p, row)) * D + i % kLines * 64));
             }
         }
-        float m[RT][2], l[RT][2], o[RT][NC][4], vref = 0.0f;
+        float m[RT][2], l[RT][2], o[RT][NC][4], vref = 0.0f, vinv = 0.0f;
 #pragma unroll
         for (int n = 0; n < RT; ++n)
 #pragma unroll
@@ -668,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
             }
 
             // The maximum stays while no logit exceeds it by more than kSlack.
-            float f[NH][RT][2], v[RT][2];
+            float f[NP][RT][2], v[RT][2];
             bool moved = false;
 #pragma unroll
             for (int n = 0; n < RT; ++n)
@@ -676,9 +676,11 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
                 for (int y = 0; y < 2; ++y) {
                     v[n][y] = -INFINITY;
 #pragma unroll
-                    for (int h = 0; h < NH; ++h) {
+                    for (int h = 0; h < NP; ++h) {
                         f[h][n][y] = fmaxf(fac[n][y] * ks[h], 1.17549435e-38f);
-                        v[n][y] = fmaxf(v[n][y], fmaxf(s[h][n][y], s[h][n][2 + y]) * f[h][n][y]);
+                        float w = fmaxf(s[h][n][y], s[h][n][2 + y]);
+                        if (NP < NH) w = fmaxf(w, fmaxf(s[NH - 1][n][y], s[NH - 1][n][2 + y]));
+                        v[n][y] = fmaxf(v[n][y], w * f[h][n][y]);
                     }
                     moved = moved || v[n][y] > m[n][y] + kSlack;
                 }
@@ -703,10 +705,11 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
             }
 
             // weights and the second product, relative to the largest scale of V so far
-            const float vtop = fmaxf(vs[0], vs[NH - 1]);
+            const float vtop = fmaxf(fmaxf(vs[0], vs[NP - 1]), 1.17549435e-38f);
             if (vtop > vref) {
                 const float down = vref / vtop;
                 vref = vtop;
+                vinv = 1.0f / vref;
 #pragma unroll
                 for (int n = 0; n < RT; ++n)
 #pragma unroll
@@ -717,7 +720,7 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
             uint32_t pb[NH][RT][2];
 #pragma unroll
             for (int h = 0; h < NH; ++h) {
-                const float ratio = vref > 0.0f ? vs[h] / vref : 0.0f;
+                const float ratio = vs[NP == NH ? h : 0] * vinv;
 #pragma unroll
                 for (int n = 0; n < RT; ++n) {
                     float w[4];
@@ -726,7 +729,7 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
                         const float top = m[n][y] == -INFINITY ? 0.0f : m[n][y] - kPShift;
 #pragma unroll
                         for (int z = 0; z < 2; ++z) {
-                            const float pv = ex2_approx(fmaf(s[h][n][2 * z + y], f[h][n][y], -top));
+                            const float pv = ex2_approx(fmaf(s[h][n][2 * z + y], f[NP == NH ? h : 0][n][y], -top));
                             l[n][y] += pv;
                             w[2 * z + y] = pv * ratio;
                         }
@@ -1093,7 +1096,7 @@ extern "C" int smd_paged_decode(const uint16_t* q, int64_t q_stride, const smd_p
     p.K = K;
     p.status = status;
     p.arrived = static_cast<int32_t*>(workspace);
-    p.box = page_box_tokens(*cache);
+    const bool halves = page_box_tokens(*cache) < KT;  // a tile spans two pages
     CUtensorMap maps[2];
     std::memcpy(maps, &cache->map[1], sizeof maps);
 
@@ -1121,15 +1124,21 @@ extern "C" int smd_paged_decode(const uint16_t* q, int64_t q_stride, const smd_p
             return launch_decode<decltype(shape)>(p, maps[0], maps[1], sms, tiles, stream);
         };
         if (D == 64)
-            rc = RT == 1   ? launch(Shape<64, 1, 32, 4, 3>{})
-                 : RT == 2 ? launch(Shape<64, 2, 32, 4, 3>{})
-                           : launch(Shape<64, 4, 32, 4, 2>{});
+            rc = halves    ? (RT == 1   ? launch(Shape<64, 1, 32, 2, 4, 3>{})
+                              : RT == 2 ? launch(Shape<64, 2, 32, 2, 4, 3>{})
+                                        : launch(Shape<64, 4, 32, 2, 4, 2>{}))
+                 : RT == 1 ? launch(Shape<64, 1, 32, 1, 4, 3>{})
+                 : RT == 2 ? launch(Shape<64, 2, 32, 1, 4, 3>{})
+                           : launch(Shape<64, 4, 32, 1, 4, 2>{});
         else if (D == 128)
-            rc = RT == 1   ? launch(Shape<128, 1, 32, 2, 3>{})
-                 : RT == 2 ? launch(Shape<128, 2, 32, 2, 3>{})
-                           : launch(Shape<128, 4, 32, 2, 2>{});
+            rc = halves    ? (RT == 1   ? launch(Shape<128, 1, 32, 2, 2, 3>{})
+                              : RT == 2 ? launch(Shape<128, 2, 32, 2, 2, 3>{})
+                                        : launch(Shape<128, 4, 32, 2, 2, 2>{}))
+                 : RT == 1 ? launch(Shape<128, 1, 32, 1, 2, 3>{})
+                 : RT == 2 ? launch(Shape<128, 2, 32, 1, 2, 3>{})
+                           : launch(Shape<128, 4, 32, 1, 2, 2>{});
         else
-            rc = RT == 1 ? launch(Shape<256, 1, 16, 2, 3>{}) : launch(Shape<256, 2, 16, 2, 2>{});
+            rc = RT == 1 ? launch(Shape<256, 1, 16, 1, 2, 3>{}) : launch(Shape<256, 2, 16, 1, 2, 2>{});
         if (rc != SMD_OK) return rc;
     }
     return SMD_OK;
