@@ -58,8 +58,9 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxEntries = 1024;  // requests (or (row, kv head) lists) of one launch
 constexpr int kNoPos = 0x3fffffff; // the position of tokens that no row sees
-constexpr float kPShift = 7.0f;    // weights are formed at 2^7 of the maximum kept
+constexpr float kPShift = 7.0f;    // weights are 2^7 at the maximum kept
 constexpr float kSlack = 8.0f;     // which is moved when a logit exceeds it by 2^8
+constexpr float kNone = -3.402823466e38f;  // no logit met
 constexpr int kUnitCost = 3;       // what a unit's begin and end cost a warp, in tiles
 constexpr int kMinTiles = 2;       // least range of a warp, in tiles
 constexpr int kFan = 32;           // neighbouring CTAs of a first join
@@ -170,9 +171,9 @@ __device__ __forceinline__ float4 lds_f4(uint32_t addr) {
 __device__ __forceinline__ float bf_lo(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
-// ln of the sum of e^logits, from a maximum (base 2) and the sum of the weights at it.
-__device__ __forceinline__ float natural_lse(float top, float sum) {
-    return sum == 0.0f ? -INFINITY : 0.69314718055994531f * (top - kPShift + log2f(sum));
+// ln of the sum of e^logits, from the base-2 logit whose weight is 1 and the sum of the weights.
+__device__ __forceinline__ float natural_lse(float base, float sum) {
+    return sum == 0.0f ? -INFINITY : 0.69314718055994531f * (base + log2f(sum));
 }
 
 // Transposes the 8 x 8 block of 16-bit elements whose row g holds its elements
@@ -549,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
         for (int n = 0; n < RT; ++n)
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
-                m[n][y] = -INFINITY;
+                m[n][y] = kNone;
                 l[n][y] = 0.0f;
             }
 #pragma unroll
@@ -667,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
                 __syncwarp();
             }
 
-            // The maximum stays while no logit exceeds it by more than kSlack.
+            // The maximum (m + kPShift) stays while no logit exceeds it by more than kSlack.
             float f[NP][RT][2], v[RT][2];
             bool moved = false;
 #pragma unroll
@@ -682,14 +683,14 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
                         if (NP < NH) w = fmaxf(w, fmaxf(s[NH - 1][n][y], s[NH - 1][n][2 + y]));
                         v[n][y] = fmaxf(v[n][y], w * f[h][n][y]);
                     }
-                    moved = moved || v[n][y] > m[n][y] + kSlack;
+                    moved = moved || v[n][y] > m[n][y] + (kSlack + kPShift);
                 }
             if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
                 for (int n = 0; n < RT; ++n)
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
-                        float top = fmaxf(m[n][y], v[n][y]);
+                        float top = fmaxf(m[n][y], v[n][y] - kPShift);
                         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
                         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
                         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
@@ -726,10 +727,9 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
                     float w[4];
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
-                        const float top = m[n][y] == -INFINITY ? 0.0f : m[n][y] - kPShift;
 #pragma unroll
                         for (int z = 0; z < 2; ++z) {
-                            const float pv = ex2_approx(fmaf(s[h][n][2 * z + y], f[NP == NH ? h : 0][n][y], -top));
+                            const float pv = ex2_approx(fmaf(s[h][n][2 * z + y], f[NP == NH ? h : 0][n][y], -m[n][y]));
                             l[n][y] += pv;
                             w[2 * z + y] = pv * ratio;
                         }
@@ -800,14 +800,14 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
                         sts64(ring + row * D * 4 + (piece16 << 4) + 8 * (qr & 1),
                               __float_as_uint(o[n][c][y] * vref), __float_as_uint(o[n][c][2 + y] * vref));
                     }
-                    if (qr == 0) s_ml[warp * S::rows + row] = make_float2(m[n][y], sum);
+                    if (qr == 0) s_ml[warp * S::rows + row] = make_float2(m[n][y] == kNone ? -INFINITY : m[n][y], sum);
                 } else {
                     const int64_t at = static_cast<int64_t>(worker) * S::rows + row;
                     float2* const out = reinterpret_cast<float2*>(p.head + at * D) + qr;
 #pragma unroll
                     for (int c = 0; c < NC; ++c)
                         out[8 * c] = make_float2(o[n][c][y] * vref, o[n][c][2 + y] * vref);
-                    if (qr == 0) p.head_ml[at] = make_float2(m[n][y], sum);
+                    if (qr == 0) p.head_ml[at] = make_float2(m[n][y] == kNone ? -INFINITY : m[n][y], sum);
                 }
             }
         if (tend < t1) {
