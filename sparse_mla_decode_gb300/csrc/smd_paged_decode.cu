@@ -168,6 +168,31 @@ __device__ __forceinline__ float4 lds_f4(uint32_t addr) {
     return v;
 }
 
+// Two fp32 operations an instruction.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 __device__ __forceinline__ float bf_lo(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
@@ -669,28 +694,31 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
             }
 
             // The maximum (m + kPShift) stays while no logit exceeds it by more than kSlack.
-            float f[NP][RT][2], v[RT][2];
-            bool moved = false;
+            float f[NP][RT][2], over = kNone;
+            const auto largest = [&](int h, int n, int y) {  // product of the page's tokens
+                float w = fmaxf(s[h][n][y], s[h][n][2 + y]);
+                if (NP < NH) w = fmaxf(w, fmaxf(s[NH - 1][n][y], s[NH - 1][n][2 + y]));
+                return w;
+            };
 #pragma unroll
             for (int n = 0; n < RT; ++n)
 #pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    v[n][y] = -INFINITY;
+                for (int y = 0; y < 2; ++y)
 #pragma unroll
                     for (int h = 0; h < NP; ++h) {
                         f[h][n][y] = fmaxf(fac[n][y] * ks[h], 1.17549435e-38f);
-                        float w = fmaxf(s[h][n][y], s[h][n][2 + y]);
-                        if (NP < NH) w = fmaxf(w, fmaxf(s[NH - 1][n][y], s[NH - 1][n][2 + y]));
-                        v[n][y] = fmaxf(v[n][y], w * f[h][n][y]);
+                        over = fmaxf(over, fmaf(largest(h, n, y), f[h][n][y], -m[n][y]));
                     }
-                    moved = moved || v[n][y] > m[n][y] + (kSlack + kPShift);
-                }
+            const bool moved = over > kSlack + kPShift;
             if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
                 for (int n = 0; n < RT; ++n)
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
-                        float top = fmaxf(m[n][y], v[n][y] - kPShift);
+                        float top = m[n][y];
+#pragma unroll
+                        for (int h = 0; h < NP; ++h)
+                            top = fmaxf(top, fmaf(largest(h, n, y), f[h][n][y], -kPShift));
                         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
                         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
                         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
@@ -725,15 +753,18 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
 #pragma unroll
                 for (int n = 0; n < RT; ++n) {
                     float w[4];
+                    const float* const fh = f[NP == NH ? h : 0][n];
+                    uint64_t sum = pack2(l[n][0], l[n][1]);
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-#pragma unroll
-                        for (int z = 0; z < 2; ++z) {
-                            const float pv = ex2_approx(fmaf(s[h][n][2 * z + y], f[NP == NH ? h : 0][n][y], -m[n][y]));
-                            l[n][y] += pv;
-                            w[2 * z + y] = pv * ratio;
-                        }
+                    for (int z = 0; z < 2; ++z) {
+                        float x0, x1;
+                        unpack2(fma2(pack2(s[h][n][2 * z], s[h][n][2 * z + 1]), pack2(fh[0], fh[1]),
+                                     pack2(-m[n][0], -m[n][1])), x0, x1);
+                        const uint64_t pv = pack2(ex2_approx(x0), ex2_approx(x1));
+                        sum = add2(sum, pv);
+                        unpack2(mul2(pv, pack2(ratio, ratio)), w[2 * z], w[2 * z + 1]);
                     }
+                    unpack2(sum, l[n][0], l[n][1]);
                     pb[h][n][0] = transpose8x8(f16x2(w[0], w[1]));
                     pb[h][n][1] = transpose8x8(f16x2(w[2], w[3]));
                 }
