@@ -43,7 +43,6 @@
 
 #include "smd.h"
 #include "smd_internal.h"
-#include "smd_paged.h"
 #include "smd_ptx.cuh"
 #include "smd_tc_common.cuh"
 #include "smd_trace.cuh"
@@ -840,31 +839,6 @@ int tc_resident_clusters(int split) {
 bool encode_row_map(CUtensorMap* out, const void* ptr, uint64_t rows, uint32_t box_cols,
                     uint32_t box_rows) {
     return encode_map(out, ptr, rows, box_cols, box_rows);
-}
-
-bool encode_page_map(CUtensorMap* out, const void* ptr, const int64_t (&stride)[3],
-                     const smd_paged_cache_t& c) {
-    EncodeTiledFn encode = encode_fn();
-    if (encode == nullptr) return false;
-    const cuuint64_t dims[4] = {
-        static_cast<cuuint64_t>(c.head_dim), static_cast<cuuint64_t>(c.page_size),
-        static_cast<cuuint64_t>(c.heads), static_cast<cuuint64_t>(c.pages)};
-    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(stride[2]),
-                                   static_cast<cuuint64_t>(stride[1]),
-                                   static_cast<cuuint64_t>(stride[0])};
-    const cuuint32_t box[4] = {static_cast<cuuint32_t>(c.head_dim < 128 ? c.head_dim : 128),
-                               static_cast<cuuint32_t>(page_box_tokens(c)), 1, 1};
-    const cuuint32_t estr[4] = {1, 1, 1, 1};
-    // L2 fetches no more than a row where rows of 64 bytes lie apart (310 requests of up to
-    // 5001 tokens: 158 us against 247 us at 128 bytes, whose other half is another head's).
-    const CUtensorMapL2promotion fetch = c.head_dim < 128 && stride[2] != c.head_dim
-                                             ? CU_TENSOR_MAP_L2_PROMOTION_L2_64B
-                                             : CU_TENSOR_MAP_L2_PROMOTION_L2_128B;
-    return encode(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(ptr), dims, strides, box,
-                  estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  c.head_dim < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
-                  fetch,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // ---- the exchange scratch of smd_sparse_mla_decode_noalloc --------------------------
