@@ -792,15 +792,17 @@ int64_t smd_paged_workspace_bytes(const smd_paged_cache_t* cache);
  *   lse  = ln sum_t e^(s_t);  out[c] = BF16(sum_t e^(s_t - lse) v[t,h,c])
  * with k, v the values the codes stand for; a row that sees nothing gets
  * zeros and -inf. Sums and statistics are fp32; the weights enter the second
- * product as f16 at 2^14 of the running maximum, the queries the first as f16
- * at a power of two of each (row, head)'s maximum (exact but for elements
- * below 2^-30 of it).
+ * product as f16, at 2^7 for the running maximum that they are taken from (and up
+ * to 2^15, for it moves in steps) times the page's scale over the largest so
+ * far, the queries the first as f16 at a power of two of each (row, head)'s
+ * maximum (exact but for elements below 2^-30 of it).
  *   block_lists   NULL: a row sees its first n = length - G + 1 + i tokens.
  *            Else [B, heads, K] int32 (row b, kv head h): page numbers within
  *            the request (0 = its first page), the first
  *            clamp(block_counts[b, h], 0, K) of them; the row sees those
  *            pages' tokens below n, once for each time a page is listed.
  *            Numbers outside the row's pages are passed over (such as -1).
+ *            With lists row_group * heads <= 1024 (SMD_ERR_SHAPE).
  *   block_counts  [B, heads] int32; NULL: all K.
  *   out      [B, Hq, head_dim] bfloat16, contiguous, 16-byte aligned.
  *   lse      [B, Hq] float32; may be NULL.

@@ -21,7 +21,7 @@
 // KB an SM are on their way at a time.
 //
 // Measured (GB300): 96 tokens of as many requests, 8 heads of 128 columns, 2.9 us; 28
-// thousand tokens of 23 requests 38 us (68% of the copy rate for the 173 MB: the
+// thousand tokens of 23 requests 37 us (69% of the copy rate for the 173 MB: the
 // slots, a run's loads, its maximum and its stores follow one another, and 20 warps
 // an SM do not quite cover that), 16 thousand of one 37 us (79%).
 #include "smd_internal.h"
@@ -460,8 +460,8 @@ __global__ void __launch_bounds__(kThreads, 5) append_many_kernel(const AppendPa
 template <int D>
 int launch_append(const AppendParams& p, int sms, smd_stream_t stream) {
     // Few tokens: lanes for each token. Many: blocks by chunks of tokens. 8 heads of 128
-    // columns, few / many: 1000 tokens of as many requests 5.8 / 44 us, 900 tokens of 30
-    // requests 15 / 18 us, 4000 tokens of one request 52 / 15 us.
+    // columns, few / many: 1000 tokens of as many requests 5.8 / 23.6 us, 2400 11.3 / 25.4,
+    // 900 tokens of 30 requests 13 / 10.4, 4000 tokens of one request 45 / 14.7.
     const int64_t units = static_cast<int64_t>(p.T) * p.heads * 2;
     if (units <= static_cast<int64_t>(sms) * 256)
         return launch_pdl(append_few_kernel<D>,

@@ -44,6 +44,20 @@
 // accumulators, maxima and sums are fp32. V's scale multiplies the weights
 // relative to the largest scale met so far (exact for powers of two), so f16
 // never sees its range.
+//
+// Measured (GB300, device time; of the rate at which the GPU copies):
+//   64 requests of 1024 .. 8192 tokens, 8 query rows of 128 columns   109 us   82%
+//   64 listed pages of 64 tokens in each of 64 requests               104 us   77%
+//   16 requests up to 131072 tokens, 32 query rows                    430 us   75%
+//   31 requests up to 5001 tokens, 12 query rows of 64 columns         34 us   36%
+//   one request of 777 tokens                                          10 us
+// What bounds it now. The start costs 4 us before a copy is on its way (lengths,
+// table entry, copy: three round trips and the launch), the joins 5 to 10 us after
+// the last tile: all of the time of one short request, half of that of a small batch. At
+// 8 rows the rest is HBM, and its unevenness: some neighbourhoods of SMs stream 7%
+// slower than the others, the same ones every time. At 32 rows the 255 registers a
+// lane leave 8 warps an SM, and the products' and softmax's latencies show
+// (mma.sync takes 8 cycles a sub-partition, 52% of the time in all; issue 38%).
 #include <atomic>
 #include <cstring>
 
@@ -61,9 +75,12 @@ constexpr int kNoPos = 0x3fffffff; // the position of tokens that no row sees
 constexpr float kPShift = 7.0f;    // weights are 2^7 at the maximum kept
 constexpr float kSlack = 8.0f;     // which is moved when a logit exceeds it by 2^8
 constexpr float kNone = -3.402823466e38f;  // no logit met
-constexpr int kUnitCost = 3;       // what a unit's begin and end cost a warp, in tiles
-constexpr int kMinTiles = 2;       // least range of a warp, in tiles
-constexpr int kFan = 32;           // neighbouring CTAs of a first join
+// What a unit's begin and end cost a warp, in tiles. 0 / 1 / 3 / 6: 31 requests up to 5001
+// tokens of 64 columns 44 / 39 / 34 / 33 us, 1000 up to 300 tokens of 128 columns 93 / 81 /
+// 78 / 78, 64 up to 8192 tokens 111 / 110 / 109 / 109; twice as much at 64 columns: no gain.
+constexpr int kUnitCost = 3;
+constexpr int kMinTiles = 2;       // least range of a warp, in tiles (1 to 8: the same times)
+constexpr int kFan = 32;           // neighbouring CTAs of a first join (8 to 64: the same times)
 
 struct PagedParams {
     const uint16_t* q;
@@ -1105,7 +1122,10 @@ extern "C" int smd_paged_decode(const uint16_t* q, int64_t q_stride, const smd_p
 
     const bool lists = block_lists != nullptr;
     const int g = Hq / cache->heads, rows = lists ? g : row_group * g;
-    const int most_tiles = D == 256 ? 2 : 4;  // of 8 rows: what the registers hold
+    // Tiles of 8 query rows that a warp holds: as many as there are rows for, up to what its
+    // registers take. 16 requests up to 65536 tokens, 4 / 2 at 32 rows 226 / 340 us, at 16
+    // rows 213 / 189; 2 / 1 at 8 rows 113 / 109 (64 requests up to 8192 tokens).
+    const int most_tiles = D == 256 ? 2 : 4;
     const int RT = rows <= 8 ? 1 : rows <= 16 ? 2 : most_tiles, KT = D == 256 ? 16 : 32;
     PagedParams p{};
     p.q_stride = q_stride;
