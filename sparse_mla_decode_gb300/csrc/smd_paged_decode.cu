@@ -1107,7 +1107,7 @@ extern "C" int smd_paged_decode(const uint16_t* q, int64_t q_stride, const smd_p
     const int D = cache->head_dim, P = cache->page_size;
     if (cache->k == nullptr) return SMD_ERR_NULL;
     if (block_lists != nullptr &&
-        (K < 0 || static_cast<int64_t>(K) * P >= (1ll << 31) ||
+        (K < 0 || static_cast<int64_t>(K) * P >= (1ll << 31) || row_group * cache->heads > kMaxEntries ||
          static_cast<int64_t>(R) * row_group * cache->heads >= (1ll << 31)))
         return SMD_ERR_SHAPE;
     if (skip) return SMD_OK;
@@ -1156,7 +1156,7 @@ extern "C" int smd_paged_decode(const uint16_t* q, int64_t q_stride, const smd_p
     const int64_t per_request =
         static_cast<int64_t>(lists ? row_group * cache->heads : 1) * p.x_units * per_entry;
     const int entries_of = lists ? row_group * cache->heads : 1;
-    if (entries_of > kMaxEntries || per_request >= (1ll << 30)) return SMD_ERR_SHAPE;
+    if (per_request >= (1ll << 30)) return SMD_ERR_SHAPE;
     int64_t step = kMaxEntries / entries_of;
     if (step > (1ll << 30) / per_request) step = (1ll << 30) / per_request;
     for (int64_t r = 0; r < R; r += step) {

@@ -324,3 +324,49 @@ def test_nothing_to_do_and_refusals(cuda):
         binding.paged_decode(q.float(), c, t, n, 0.1)
     with pytest.raises(ValueError):
         binding.paged_decode(q, c, t, n, 0.1, block_counts=n)
+
+
+@pytest.mark.parametrize("D,P,g,G", [(64, 16, 8, 1), (64, 112, 5, 1), (64, 16, 20, 1), (64, 256, 24, 1),
+                                     (128, 16, 6, 3), (128, 16, 20, 1), (256, 48, 9, 1)])
+def test_tiles_of_one_page_and_of_two_with_and_without_lists(cuda, D, P, g, G):
+    rng = np.random.default_rng(7 * D + P + g)
+    lengths = [1, 40, 333, 1500]
+    pages = sum(-(-n // P) for n in lengths) + 2
+    cache = Cache(3, pages, 2, P, D)
+    table = table_for(rng, lengths, P, pages, extra=1)
+    q = queries(rng, len(lengths) * G, 2 * g, D, 2.0)
+    check_decode(*run(cuda, cache, q, table, lengths, G), oracle(cache, q, table, lengths, G))
+    K = 5
+    lists = rng.integers(-1, max(-(-1500 // P), 2), (len(lengths) * G, 2, K))
+    check_decode(*run(cuda, cache, q, table, lengths, G, lists),
+                 oracle(cache, q, table, lengths, G, lists))
+
+
+def test_scales_that_are_no_powers_of_two_and_far_apart(cuda):
+    rng = np.random.default_rng(23)
+    cache = Cache(4, 40, 2, 32, 128)
+    cache.scales = [s * np.float32(2.0) ** rng.integers(-12, 13, s.shape) * rng.uniform(1, 2, s.shape)
+                    for s in cache.scales]
+    cache.scales = [s.astype(np.float32) for s in cache.scales]
+    table = table_for(rng, [700, 90], 32, 40)
+    q = queries(rng, 2, 8, 128, 2.0 ** -9)
+    check_decode(*run(cuda, cache, q, table, [700, 90]), oracle(cache, q, table, [700, 90]))
+
+
+def test_lists_for_more_heads_than_a_launch_takes_are_refused(cuda):
+    import torch
+    from sparse_mla_decode_gb300 import binding
+    c = binding.PagedCache.empty(1, 130, 16, 64, bounds=False, device=cuda)
+    t, n = i32([[0]], cuda), i32([16], cuda)
+    ws = torch.zeros(binding.paged_workspace_bytes(c), dtype=torch.uint8, device=cuda)
+    for G, fits in ((7, True), (8, False)):
+        q = torch.zeros((G, 130, 64), dtype=torch.bfloat16, device=cuda)
+        lists = torch.zeros((G, 130, 1), dtype=torch.int32, device=cuda)
+        if fits:
+            binding.paged_decode(q, c, t, n, 0.1, row_group=G, block_lists=lists, workspace=ws)
+            continue
+        with pytest.raises(binding.SmdError) as e:
+            binding.paged_decode(q, c, t, n, 0.1, row_group=G, block_lists=lists, workspace=ws)
+        assert e.value.status == binding.SMD_ERR_SHAPE
+        binding.paged_decode(q, c, t, n, 0.1, row_group=G, workspace=ws)
+    torch.cuda.synchronize()
