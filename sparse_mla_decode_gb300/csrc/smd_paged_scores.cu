@@ -16,9 +16,9 @@
 // match. The query rows pass over these registers 8 at a time.
 //
 // Measured (GB300): 48 requests of 8192 .. 131072 tokens in pages of 64, 8 heads of
-// 128 columns: 35 us for 8 query rows a head (84% of the copy rate for the 201
-// MB), 40 us for 16 rows, 95 us for 64 rows, where each 8 more rows cost 8 us of
-// MMAs and of shared-memory reads.
+// 128 columns: 33 us for 8 query rows a head (89% of the copy rate for the 201
+// MB), 37 us for 16 rows, 76 us for 64 rows, where each 8 more rows cost 6 us: 3 of
+// MMAs, 3 of reads of the query fragments from shared memory.
 #include "smd_internal.h"
 #include "smd_paged.h"
 #include "smd_ptx.cuh"
@@ -30,7 +30,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kGroup = 16 * kWarps;  // pages that a block's warps take at once
 // Such turns of a block: the waits for length, page and query are paid once a block. The
-// 201 MB above take 42 us at one turn, 36 at two, 35 at four, 38 at eight (too few blocks).
+// 201 MB above take 34.3 us at two turns, 33.4 at four, 35.4 at eight (too few blocks).
 constexpr int kMostSteps = 4;
 
 struct ScoreParams {
@@ -46,7 +46,7 @@ struct ScoreParams {
     int32_t keep_first, keep_last;
     uint16_t* scores;
     int64_t score_stride;
-    int32_t cols;       // columns of the MMA that one verify row takes: a power of two up to 8
+    int32_t cols, cols_log2;  // columns of the MMA that one verify row takes: a power of two up to 8
     int32_t parts;      // MMAs that one verify row takes (more than 8 query heads)
     int32_t tiles;      // MMAs over all rows
     int32_t steps;      // turns of a block
@@ -94,6 +94,8 @@ __global__ void __launch_bounds__(kThreads) block_scores_kernel(const ScoreParam
             row[c] = 0x7fffu;
     }
     if (block0 >= have) return;
+    uint16_t* const scores = p.scores + (b0 * p.heads + head) * p.score_stride;
+    const int64_t row_step = p.heads * p.score_stride;
 
     // The pages of a turn, one turn ahead of the bounds; those are on their way while the
     // products of the turn before (at first, while the queries) are dealt with.
@@ -137,8 +139,8 @@ __global__ void __launch_bounds__(kThreads) block_scores_kernel(const ScoreParam
             i = tile / p.parts;
             a = (tile % p.parts) * 8 + (l >> 2);
         } else {
-            i = (tile * 8 + (l >> 2)) / p.cols;
-            a = (l >> 2) % p.cols;
+            i = (tile * 8 + (l >> 2)) >> p.cols_log2;
+            a = (l >> 2) & (p.cols - 1);
         }
         i = min(p.i0 + i, p.i_end - 1);
         a = min(a, p.g - 1);
@@ -182,7 +184,7 @@ __global__ void __launch_bounds__(kThreads) block_scores_kernel(const ScoreParam
                 d[0] = fmaxf(d[0], __shfl_xor_sync(0xffffffffu, d[0], 2));
                 d[2] = fmaxf(d[2], __shfl_xor_sync(0xffffffffu, d[2], 2));
             }
-            int i = (tile * 8 + 2 * gi) / p.cols;
+            int i = (tile * 8 + 2 * gi) >> p.cols_log2;
             if (p.parts > 1) {
                 i = tile / p.parts;
                 const int part = tile - i * p.parts;
@@ -196,7 +198,7 @@ __global__ void __launch_bounds__(kThreads) block_scores_kernel(const ScoreParam
             for (int y = 0; y < (p.cols == 1 ? 2 : 1); ++y, ++i) {
                 if (p.i0 + i >= p.i_end) break;
                 const int sees = s_sees[i];
-                uint16_t* const out = p.scores + ((b0 + p.i0 + i) * p.heads + head) * p.score_stride;
+                uint16_t* const out = scores + (p.i0 + i) * row_step;
 #pragma unroll
                 for (int z = 0; z < 2; ++z) {
                     const int c = c0 + 8 * z + gr;
@@ -282,7 +284,7 @@ extern "C" int smd_block_scores(const uint16_t* q, int64_t q_stride, const smd_p
     p.scores = scores;
     p.score_stride = score_stride;
     p.cols = 1;
-    while (p.cols < p.g && p.cols < 8) p.cols *= 2;
+    while (p.cols < p.g && p.cols < 8) p.cols *= 2, ++p.cols_log2;
     p.parts = (p.g + 7) / 8;
     p.tiles = p.parts > 1 ? p.G * p.parts : (p.G * p.cols + 7) / 8;
     return cache->head_dim == 64    ? launch_scores<64>(p, R, sms, stream)
