@@ -390,7 +390,10 @@ constexpr int kShort = 4;       // runs up to this length go to D / 8 lanes each
 template <int D>
 __global__ void __launch_bounds__(kThreads, 5) append_many_kernel(const AppendParams p) {
     constexpr int N = D / 8, kWarps = kThreads / 32;
-    constexpr int kMedium = 8 * (32 / N);  // runs up to this length go to a warp each
+    // Runs up to kHalf tokens go to half a warp each, up to kMedium to a warp: 8 values a lane.
+    // (30 thousand tokens in pages of 16 of 64 columns: 33 us, by whole warps 41; in pages of 32,
+    // whose runs take a warp each, 33 and 32.)
+    constexpr int kHalf = D == 64 ? 16 : 0, kMedium = 8 * (32 / N);
     __shared__ int s_slot[kChunk];
     __shared__ int2 s_runs[kChunk];  // first token and length: short runs from the front, long from the back
     __shared__ uint32_t s_goes[(kChunk + kMostPage) / 32], s_lead[kChunk / 32];
@@ -446,8 +449,17 @@ __global__ void __launch_bounds__(kThreads, 5) append_many_kernel(const AppendPa
 #pragma unroll 1
     for (int u = warp; u < 2 * s_long; u += kWarps) {
         const int2 r = s_runs[kChunk - 1 - (u >> 1)];
-        if (r.y <= kMedium)
+        if ((kHalf == 0 || r.y > kHalf) && r.y <= kMedium)
             write_run<32, 8, D>(p, Run{t0 + r.x, r.y, s_slot[r.x]}, head, u & 1, lane, 0xffffffffu);
+    }
+    if constexpr (kHalf > 0) {
+#pragma unroll 1
+        for (int u = tid / 16; u < 2 * s_long; u += kThreads / 16) {
+            const int2 r = s_runs[kChunk - 1 - (u >> 1)];
+            if (r.y <= kHalf)
+                write_run<16, 8, D>(p, Run{t0 + r.x, r.y, s_slot[r.x]}, head, u & 1, tid % 16,
+                                                   group_mask<16>(lane));
+        }
     }
     const unsigned mask = group_mask<N>(lane);
 #pragma unroll 1
