@@ -904,29 +904,27 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
             else unit[0] = u, goes[0] = true;
         }
         const int64_t slot = static_cast<int64_t>(4 * cta + (begins ? 2 : 0)) * S::rows;
-#pragma unroll 2
+#pragma unroll 1
         for (int idx = tid; idx < u.m_real * (D / 4); idx += kThreads) {
             const int row = idx / (D / 4), col = idx % (D / 4);
-            // The partials of up to kWarps - 1 open warps and one end, or kWarps open ones.
-            float4 v[kWarps];
-            float2 ml[kWarps];
-#pragma unroll
-            for (int j = 0; j < kWarps; ++j) {
-                v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                ml[j] = make_float2(-INFINITY, 0.0f);
-                if (j < opens) {
-                    v[j] = lds_f4(base + (first + j) * ST * S::slot + row * D * 4 +
-                                  ((col ^ (((row >> 1) & 3) << 1)) << 4));
-                    ml[j] = s_ml[(first + j) * S::rows + row];
-                } else if (j == opens && end_at >= 0) {
-                    const int64_t at = (static_cast<int64_t>(cta) * kWarps + end_at) * S::rows + row;
-                    v[j] = __ldcg(reinterpret_cast<const float4*>(p.head + at * D) + col);
-                    ml[j] = __ldcg(p.head_ml + at);
-                }
+            // The open warps' partials in order, then the end.
+            float4 end_v[1] = {make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
+            float2 end_ml[1] = {make_float2(-INFINITY, 0.0f)};
+            if (end_at >= 0) {
+                const int64_t at = (static_cast<int64_t>(cta) * kWarps + end_at) * S::rows + row;
+                end_v[0] = __ldcg(reinterpret_cast<const float4*>(p.head + at * D) + col);
+                end_ml[0] = __ldcg(p.head_ml + at);
             }
             float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             float top = -INFINITY, sum = 0.0f;
-            add_partials<kWarps>(acc, top, sum, v, ml);
+#pragma unroll 1
+            for (int j = 0; j < opens; ++j) {
+                const float4 v[1] = {lds_f4(base + (first + j) * ST * S::slot + row * D * 4 +
+                                            ((col ^ (((row >> 1) & 3) << 1)) << 4))};
+                const float2 ml[1] = {s_ml[(first + j) * S::rows + row]};
+                add_partials<1>(acc, top, sum, v, ml);
+            }
+            if (end_at >= 0) add_partials<1>(acc, top, sum, end_v, end_ml);
             if (whole) {
                 write_row(p, u, D, row, 4 * col, acc, top, sum);
             } else {
@@ -987,7 +985,7 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
 #pragma unroll 1
         for (int i0 = me; i0 < u.m_real * (D / 4); i0 += 2 * threads) {
             // Two pieces of 4 columns, 8 partials of each: one round trip.
-            constexpr int kMany = 8;
+            constexpr int kMany = 4;
             int row[2], col[2];
             float4 acc[2];
             float top[2], sum[2];
