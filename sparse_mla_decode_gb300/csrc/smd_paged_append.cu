@@ -21,7 +21,7 @@
 // KB an SM are on their way at a time.
 //
 // Measured (GB300): 96 tokens of as many requests, 8 heads of 128 columns, 2.9 us; 28
-// thousand tokens of 23 requests 37 us (69% of the copy rate for the 173 MB: the
+// thousand tokens of 23 requests 37 us (68% of the copy rate for the 173 MB: the
 // slots, a run's loads, its maximum and its stores follow one another, and 20 warps
 // an SM do not quite cover that), 16 thousand of one 37 us (79%).
 #include "smd_internal.h"

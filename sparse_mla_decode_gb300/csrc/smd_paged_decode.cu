@@ -46,18 +46,20 @@
 // never sees its range.
 //
 // Measured (GB300, device time; of the rate at which the GPU copies):
-//   64 requests of 1024 .. 8192 tokens, 8 query rows of 128 columns   109 us   82%
-//   64 listed pages of 64 tokens in each of 64 requests               104 us   77%
-//   16 requests up to 131072 tokens, 32 query rows                    430 us   75%
-//   31 requests up to 5001 tokens, 12 query rows of 64 columns         34 us   36%
-//   one request of 777 tokens                                          10 us
+//   64 requests of 1024 .. 8192 tokens, 8 query rows of 128 columns   107 us   84%
+//   64 listed pages of 64 tokens in each of 64 requests               101 us   79%
+//   16 requests up to 131072 tokens, 32 query rows                    425 us   76%
+//   31 requests up to 5001 tokens, 12 query rows of 64 columns         32 us   37%
+//   one request of 777 tokens                                         9.6 us
 // What bounds it now. The start costs 4 us before a copy is on its way (lengths,
-// table entry, copy: three round trips and the launch), the joins 5 to 10 us after
-// the last tile: all of the time of one short request, half of that of a small batch. At
-// 8 rows the rest is HBM, and its unevenness: some neighbourhoods of SMs stream 7%
-// slower than the others, the same ones every time. At 32 rows the 255 registers a
-// lane leave 8 warps an SM, and the products' and softmax's latencies show
-// (mma.sync takes 8 cycles a sub-partition, 52% of the time in all; issue 38%).
+// table entry, copy: three round trips and the launch), the joins 5 to 9 us after
+// the last tile: all of the time of one short request, half of that of a small batch.
+// (The joins run once a CTA, from instructions that are not cached yet: they are
+// kept short, which took 1 to 2.5 us off each of these.) At 8 rows the rest is HBM,
+// and its unevenness: some neighbourhoods of SMs stream 7% slower than the others,
+// the same ones every time. At 32 rows the 255 registers a lane leave 8 warps an
+// SM, and the products' and softmax's latencies show (mma.sync takes 8 cycles a
+// sub-partition, 52% of the time in all; issue 38%).
 #include <atomic>
 #include <cstring>
 
