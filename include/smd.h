@@ -794,8 +794,10 @@ int64_t smd_paged_workspace_bytes(const smd_paged_cache_t* cache);
  * zeros and -inf. Sums and statistics are fp32; the weights enter the second
  * product as f16, at 2^7 for the running maximum that they are taken from (and up
  * to 2^15, for it moves in steps) times the page's scale over the largest so
- * far, the queries the first as f16 at a power of two of each (row, head)'s
- * maximum (exact but for elements below 2^-30 of it).
+ * far among the pages of the request's verify rows (11 bits while weight times
+ * scale is within 2^-21 of the largest weight times the largest scale, a bit
+ * less for each power of two below), the queries the first as f16 at a power of
+ * two of each (row, head)'s maximum (exact but for elements below 2^-30 of it).
  *   block_lists   NULL: a row sees its first n = length - G + 1 + i tokens.
  *            Else [B, heads, K] int32 (row b, kv head h): page numbers within
  *            the request (0 = its first page), the first

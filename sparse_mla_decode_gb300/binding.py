@@ -935,10 +935,22 @@ def _vector(t, name: str, dtype, n: int | None = None):
         raise ValueError(f"{name} must have at least {n} elements")
 
 
-def _output(t, name: str, dtype, n: int, like):
+def _new(make, stream, shape, dtype, device):
+    """A tensor made (torch.empty, torch.zeros) on the stream of the call that
+    uses it, so that the allocator reuses its memory in that stream's order."""
+    import torch
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=device)
+
+
+def _output(t, name: str, dtype, n: int, like, stream):
     if t is None:
         import torch
-        return torch.empty(n, dtype=dtype, device=like.device)
+        return _new(torch.empty, stream, n, dtype, like.device)
     _vector(t, name, dtype, n)
     return t
 
@@ -965,14 +977,14 @@ def block_tables(lengths, new_tokens, table, ring, state, page_size: int, max_to
     if slots is None:
         if max_tokens is None:
             raise ValueError("block_tables needs slots or max_tokens")
-        slots = torch.empty(int(max_tokens), dtype=torch.int32, device=lengths.device)
+        slots = _new(torch.empty, stream, int(max_tokens), torch.int32, lengths.device)
     T = slots.numel()
 
-    new_lengths = _output(new_lengths, "new_lengths", torch.int32, R, lengths)
-    new_state = _output(new_state, "new_state", torch.int64, 2, lengths)
-    starts = _output(starts, "starts", torch.int32, R + 1, lengths)
+    new_lengths = _output(new_lengths, "new_lengths", torch.int32, R, lengths, stream)
+    new_state = _output(new_state, "new_state", torch.int64, 2, lengths, stream)
+    starts = _output(starts, "starts", torch.int32, R + 1, lengths, stream)
     _vector(slots, "slots", torch.int32)
-    positions = _output(positions, "positions", torch.int32, T, lengths)
+    positions = _output(positions, "positions", torch.int32, T, lengths, stream)
     if new_lengths.data_ptr() == lengths.data_ptr() and R or new_state.data_ptr() == state.data_ptr():
         raise ValueError("new_lengths and new_state may not be lengths and state")
     rc = _so().smd_block_tables(
@@ -1039,8 +1051,8 @@ def block_scores(q, cache: PagedCache, table, lengths, row_group: int = 1, keep_
     args = _paged_rows(q, cache, table, lengths, row_group)
     B, width = q.shape[0], table.shape[1]
     if out is None:  # rows of a multiple of 8 scores: topk_select reads them in 16-byte pieces
-        out = torch.empty((B, cache.heads, (width + 7) // 8 * 8), dtype=torch.bfloat16,
-                          device=q.device)[:, :, :width]
+        out = _new(torch.empty, stream, (B, cache.heads, (width + 7) // 8 * 8), torch.bfloat16,
+                   q.device)[:, :, :width]
     if not out.is_cuda or out.dtype != torch.bfloat16 or tuple(out.shape) != (B, cache.heads, width) \
             or out.stride(2) != 1 or (B > 1 and out.stride(0) != cache.heads * out.stride(1)):
         raise ValueError(f"out must be a bfloat16 CUDA tensor [{B}, {cache.heads}, {width}] with "
@@ -1087,15 +1099,15 @@ def paged_decode(q, cache: PagedCache, table, lengths, sm_scale: float, row_grou
     elif block_counts is not None:
         raise ValueError("block_counts without block_lists")
     if out is None:
-        out = torch.empty((B, Hq, cache.head_dim), dtype=torch.bfloat16, device=q.device)
+        out = _new(torch.empty, stream, (B, Hq, cache.head_dim), torch.bfloat16, q.device)
     elif tuple(out.shape) != (B, Hq, cache.head_dim):
         raise ValueError(f"out must be [{B}, {Hq}, {cache.head_dim}]")
     _vector(out, "out", torch.bfloat16)
     if lse is None:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+        lse = _new(torch.empty, stream, (B, Hq), torch.float32, q.device)
     _vector(lse, "lse", torch.float32, B * Hq)
     if workspace is None:
-        workspace = torch.zeros(paged_workspace_bytes(cache), dtype=torch.uint8, device=q.device)
+        workspace = _new(torch.zeros, stream, paged_workspace_bytes(cache), torch.uint8, q.device)
     elif not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
     rc = _so().smd_paged_decode(

@@ -370,3 +370,27 @@ def test_lists_for_more_heads_than_a_launch_takes_are_refused(cuda):
         assert e.value.status == binding.SMD_ERR_SHAPE
         binding.paged_decode(q, c, t, n, 0.1, row_group=G, workspace=ws)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_what_a_call_allocates_is_made_on_its_stream(cuda, raw):
+    """The workspace is zeroed in the order of the call's stream, not behind what
+    the current stream still has to do, and in memory that held something else."""
+    import torch
+    from sparse_mla_decode_gb300 import binding
+    rng = np.random.default_rng(31)
+    cache = Cache(5, 70, 2, 64, 128)
+    c = cache.to(cuda)
+    table = table_for(rng, [4000], 64, 70)
+    q = queries(rng, 1, 16, 128)
+    tq, tt, tl = bf16(q, cuda), i32(table, cuda), i32([4000], cuda)
+    s = torch.cuda.Stream()
+    used = torch.full((binding.paged_workspace_bytes(c),), 7, dtype=torch.uint8, device=cuda)
+    torch.cuda.synchronize()
+    del used
+    torch.cuda._sleep(20_000_000)
+    out, lse = binding.paged_decode(tq, c, tt, tl, 128 ** -0.5, stream=s.cuda_stream if raw else s)
+    s.synchronize()
+    got = out.cpu(), lse.cpu()
+    torch.cuda.synchronize()
+    check_decode(*got, oracle(cache, q, table, [4000]))
