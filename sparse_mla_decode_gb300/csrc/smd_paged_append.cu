@@ -20,7 +20,7 @@
 // of 64; what is longer is read again, from L2), so that 8 KB a warp and 160
 // KB an SM are on their way at a time.
 //
-// Measured (GB300): 96 tokens of as many requests, 8 heads of 128 columns, 2.9 us; 28
+// Measured (GB300): 96 tokens of as many requests, 8 heads of 128 columns, 2.5 us; 28
 // thousand tokens of 23 requests 37 us (68% of the copy rate for the 173 MB: the
 // slots, a run's loads, its maximum and its stores follow one another, and 20 warps
 // an SM do not quite cover that), 16 thousand of one 37 us (79%).
@@ -105,20 +105,37 @@ __device__ __forceinline__ bool starts_run(const AppendParams& p, int t, int slo
     return t == 0 || slot % p.P == 0 || p.slots[t - 1] != slot - 1;
 }
 
-// The largest and smallest of a run's keys, joined with the bounds before (o > 0)
-// and written: 8 columns from `col` on.
-__device__ __forceinline__ void write_bounds(uint16_t* bounds, int D, int col, int o, uint32_t (&hi)[4],
-                                             uint32_t (&lo)[4]) {
-    uint4* const b = reinterpret_cast<uint4*>(bounds + col);
-    if (o > 0) {
-        const uint4 h = b[0], l = b[D / 8];
-        hi[0] = bmax2(hi[0], h.x), hi[1] = bmax2(hi[1], h.y);
-        hi[2] = bmax2(hi[2], h.z), hi[3] = bmax2(hi[3], h.w);
-        lo[0] = bmin2(lo[0], l.x), lo[1] = bmin2(lo[1], l.y);
-        lo[2] = bmin2(lo[2], l.z), lo[3] = bmin2(lo[3], l.w);
+// What a page holds before a run: its scale and, of 8 columns from `col` on, its bounds
+// (loaded ahead of the run's values, so that nothing waits for them afterwards).
+struct Before {
+    float scale;
+    uint4 hi, lo;
+};
+
+template <int D>
+__device__ __forceinline__ Before before(const AppendParams& p, int64_t at, int side, int o, int col) {
+    Before b;
+    b.scale = o > 0 ? p.scale[side][at] : __uint_as_float(static_cast<uint32_t>(kMinExponent + 127) << 23);
+    b.hi = make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);  // -infinity
+    b.lo = make_uint4(0x7f807f80u, 0x7f807f80u, 0x7f807f80u, 0x7f807f80u);
+    if (side == 0 && o > 0 && p.bounds != nullptr) {
+        const uint4* const w = reinterpret_cast<const uint4*>(p.bounds + at * 2 * D + col);
+        b.hi = w[0];
+        b.lo = w[D / 8];
     }
-    b[0] = make_uint4(finite2(hi[0]), finite2(hi[1]), finite2(hi[2]), finite2(hi[3]));
-    b[D / 8] = make_uint4(finite2(lo[0]), finite2(lo[1]), finite2(lo[2]), finite2(lo[3]));
+    return b;
+}
+
+// The largest and smallest of a run's keys, joined with the bounds before and
+// written: 8 columns from `col` on.
+__device__ __forceinline__ void write_bounds(uint16_t* bounds, int D, int col, const Before& was,
+                                             uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+    uint4* const b = reinterpret_cast<uint4*>(bounds + col);
+    const uint4 h = was.hi, l = was.lo;
+    b[0] = make_uint4(finite2(bmax2(hi[0], h.x)), finite2(bmax2(hi[1], h.y)), finite2(bmax2(hi[2], h.z)),
+                      finite2(bmax2(hi[3], h.w)));
+    b[D / 8] = make_uint4(finite2(bmin2(lo[0], l.x)), finite2(bmin2(lo[1], l.y)), finite2(bmin2(lo[2], l.z)),
+                          finite2(bmin2(lo[3], l.w)));
 }
 
 // Takes 8 values into the extremes.
@@ -190,20 +207,23 @@ struct Run {
 // lanes that run together). The first kKept values of a lane stay in registers.
 template <int N, int kKept, int D>
 __device__ __forceinline__ void write_run(const AppendParams& p, const Run& r, int head, int side,
-                                          int i, unsigned mask) {
+                                          int i, unsigned mask, const Before* given = nullptr,
+                                          const uint4* first = nullptr) {
     constexpr int kCols = D / 8, kStep = N / kCols;  // lanes of a token; tokens at once
     const int col = (i % kCols) * 8, t_in = i / kCols;
     const int page = r.slot / p.P, o = r.slot - page * p.P;
     const int64_t xs = p.x_stride[side], at = static_cast<int64_t>(page) * p.heads + head;
     const uint16_t* const x = p.x[side] + r.t * xs + head * D + col;
     float* const scale = p.scale[side] + at;
-    const float old = o > 0 ? *scale : __uint_as_float(static_cast<uint32_t>(kMinExponent + 127) << 23);
+    const Before was = given != nullptr ? *given : before<D>(p, at, side, o, col);
+    const float old = was.scale;
     uint4 v[kKept];
 #pragma unroll
     for (int k = 0; k < kKept; ++k) {
         const int m = t_in + k * kStep;
         v[k] = make_uint4(0, 0, 0, 0);
-        if (m < r.n) v[k] = __ldcs(reinterpret_cast<const uint4*>(x + m * xs));
+        if (k == 0 && first != nullptr) v[k] = *first;
+        else if (m < r.n) v[k] = __ldcs(reinterpret_cast<const uint4*>(x + m * xs));
     }
     uint32_t hi[4], lo[4];
 #pragma unroll
@@ -228,7 +248,7 @@ __device__ __forceinline__ void write_run(const AppendParams& p, const Run& r, i
                 hi[j] = bmax2(hi[j], __shfl_xor_sync(mask, hi[j], s));
                 lo[j] = bmin2(lo[j], __shfl_xor_sync(mask, lo[j], s));
             }
-        if (i < kCols) write_bounds(p.bounds + at * 2 * D, D, col, o, hi, lo);
+        if (i < kCols) write_bounds(p.bounds + at * 2 * D, D, col, was, hi, lo);
     }
     const float now = fmaxf(power_of(a), old);
     __syncwarp(mask);  // every lane has read the old scale
@@ -286,7 +306,7 @@ __device__ __forceinline__ void write_run_block(const AppendParams& p, const Run
             if (m < r.n) v[k] = __ldcg(reinterpret_cast<const uint4*>(x + m * xs));
         }
     };
-    const float old = o > 0 ? *scale : __uint_as_float(static_cast<uint32_t>(kMinExponent + 127) << 23);
+    const float old = before<D>(p, at, side, o, col).scale;  // the bounds later: registers
     uint32_t hi[4], lo[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -326,7 +346,7 @@ __device__ __forceinline__ void write_run_block(const AppendParams& p, const Run
         hi[2] = bmax2(hi[2], h.z), hi[3] = bmax2(hi[3], h.w);
         lo[0] = bmin2(lo[0], l.x), lo[1] = bmin2(lo[1], l.y);
         lo[2] = bmin2(lo[2], l.z), lo[3] = bmin2(lo[3], l.w);
-        write_bounds(p.bounds + at * 2 * D, D, col, o, hi, lo);
+        write_bounds(p.bounds + at * 2 * D, D, col, before<D>(p, at, 0, o, col), hi, lo);
     }
     __syncthreads();  // shared is free again, and every thread has read the old scale
     if (half == 0 && lane == 0) *scale = now;
@@ -373,6 +393,10 @@ __global__ void __launch_bounds__(kThreads) append_few_kernel(const AppendParams
     if (t >= p.T) return;
     const int slot = p.slots[t];
     if (!starts_run(p, t, slot)) return;
+    // The first token's values and the page's state are on their way meanwhile.
+    const int side = hs & 1, head = hs >> 1, page = slot / p.P, o = slot - page * p.P;
+    const uint4 first = __ldcs(reinterpret_cast<const uint4*>(p.x[side] + t * p.x_stride[side] + head * D + 8 * i));
+    const Before was = before<D>(p, static_cast<int64_t>(page) * p.heads + head, side, o, 8 * i);
     // Tokens that continue it, up to the page's end.
     const int most = min(p.P - slot % p.P, p.T - t);
     int n = 1;
@@ -383,7 +407,7 @@ __global__ void __launch_bounds__(kThreads) append_few_kernel(const AppendParams
         n += c;
         if (c < N) break;
     }
-    write_run<N, 1, D>(p, Run{t, n, slot}, hs >> 1, hs & 1, i, mask);
+    write_run<N, 1, D>(p, Run{t, n, slot}, head, side, i, mask, &was, &first);
 }
 
 constexpr int kChunk = 64;      // tokens of a block
@@ -478,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, 5) append_many_kernel(const AppendPa
 template <int D>
 int launch_append(const AppendParams& p, int sms, smd_stream_t stream) {
     // Few tokens: lanes for each token. Many: blocks by chunks of tokens. 8 heads of 128
-    // columns, few / many: 1000 tokens of as many requests 5.8 / 23.6 us, 2400 11.3 / 25.4,
+    // columns, few / many: 1000 tokens of as many requests 5.5 / 23.6 us, 2400 11.3 / 25.4,
     // 900 tokens of 30 requests 13 / 10.4, 4000 tokens of one request 45 / 14.7.
     const int64_t units = static_cast<int64_t>(p.T) * p.heads * 2;
     if (units <= static_cast<int64_t>(sms) * 256)
