@@ -2,6 +2,7 @@
 // smd_paged_append, smd_block_scores, smd_paged_decode).
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 
 #include <cuda.h>
@@ -43,6 +44,32 @@ int check_paged_rows(const uint16_t* q, int64_t q_stride, const smd_paged_cache_
 
 // SMs of the current device; 0 on failure.
 int device_sms();
+
+constexpr int kMaxDevices = 64;
+
+// A kernel's limit of dynamic shared memory, raised once on each device, whatever the
+// first call asks for: below the raised limit the static bytes count with the dynamic
+// ones, so whether one call fits must not rest on its own dynamic bytes alone.
+struct SharedLimit {
+    std::atomic<bool> ready[kMaxDevices];
+
+    template <typename... Params>
+    int raise(void (*kernel)(Params...), int bytes) {
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
+            (void)cudaGetLastError();
+            return SMD_ERR_DEVICE;
+        }
+        if (ready[dev]) return SMD_OK;
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
+            cudaSuccess) {
+            (void)cudaGetLastError();
+            return SMD_ERR_DEVICE;
+        }
+        ready[dev] = true;
+        return SMD_OK;
+    }
+};
 
 // Launches `kernel` with programmatic stream serialization, as every kernel of
 // the library; an smd_status.

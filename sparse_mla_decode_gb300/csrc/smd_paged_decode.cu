@@ -60,7 +60,6 @@
 // the same ones every time. At 32 rows the 255 registers a lane leave 8 warps an
 // SM, and the products' and softmax's latencies show (mma.sync takes 8 cycles a
 // sub-partition, 52% of the time in all; issue 38%).
-#include <atomic>
 #include <cstring>
 
 #include "smd_internal.h"
@@ -1038,7 +1037,6 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
     }
 }
 
-constexpr int kMaxDevices = 64;
 constexpr int kWorkersPerSm = 12;  // most warps on an SM (the workspace has room for them)
 
 template <typename S>
@@ -1046,18 +1044,10 @@ int launch_decode(PagedParams p, const CUtensorMap& kmap, const CUtensorMap& vma
                   int64_t tiles, smd_stream_t stream) {
     static_assert(S::CTAS * kWarps <= kWorkersPerSm, "the workspace's workers");
     static_assert(S::CTAS * (S::smem(kMaxEntries) + 64 + 1024) <= 228 * 1024, "CTAs of an SM");
-    static std::atomic<bool> ready[kMaxDevices];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return SMD_ERR_DEVICE;
+    static SharedLimit limit;
     auto kernel = paged_decode_kernel<S>;
-    if (!ready[dev]) {
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 S::smem(kMaxEntries)) != cudaSuccess) {
-            (void)cudaGetLastError();
-            return SMD_ERR_DEVICE;
-        }
-        ready[dev] = true;
-    }
+    const int rc = limit.raise(kernel, S::smem(kMaxEntries));
+    if (rc != SMD_OK) return rc;
     const int64_t most = static_cast<int64_t>(sms) * kWorkersPerSm;
     const int64_t want = (tiles + kWarps - 1) / kWarps;  // a tile for each warp
     int64_t grid = static_cast<int64_t>(sms) * S::CTAS;

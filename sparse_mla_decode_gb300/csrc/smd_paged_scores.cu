@@ -218,12 +218,9 @@ template <int D>
 int launch_scores(ScoreParams p, int R, int sms, smd_stream_t stream) {
     constexpr int kTile = 32 * D, kMost = 176 * 1024;  // shared bytes of an MMA's columns
     static_assert(kMost / kTile >= kPagedMaxHeads / 8, "a verify row's query heads fit");
-    if (p.tiles * kTile > 48 * 1024 &&
-        cudaFuncSetAttribute(block_scores_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kMost) != cudaSuccess) {
-        (void)cudaGetLastError();
-        return SMD_ERR_DEVICE;
-    }
+    static SharedLimit limit;
+    int rc = limit.raise(block_scores_kernel<D>, kMost);
+    if (rc != SMD_OK) return rc;
     // Turns of a block: few where there are few pages, so that the blocks still fill the device.
     const int64_t groups = (static_cast<int64_t>(p.width) + kGroup - 1) / kGroup;
     p.steps = kMostSteps;
@@ -237,7 +234,7 @@ int launch_scores(ScoreParams p, int R, int sms, smd_stream_t stream) {
         p.tiles = p.parts > 1 ? n * p.parts : (n * p.cols + 7) / 8;
         for (p.r0 = 0; p.r0 < R; p.r0 += 65535) {
             const int z = R - p.r0 < 65535 ? R - p.r0 : 65535;
-            const int rc = launch_pdl(
+            rc = launch_pdl(
                 block_scores_kernel<D>, dim3(gx, static_cast<unsigned>(p.heads), static_cast<unsigned>(z)),
                 kThreads, static_cast<size_t>(p.tiles) * kTile, stream, p);
             if (rc != SMD_OK) return rc;

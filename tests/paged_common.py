@@ -1,9 +1,15 @@
 """Inputs and comparisons shared by the paged-cache tests."""
 from __future__ import annotations
 
+import os
+import subprocess
+import sys
+
 import numpy as np
 
 from oracle import paged as opaged
+
+TESTS = os.path.dirname(os.path.abspath(__file__))
 
 
 class Cache:
@@ -91,3 +97,11 @@ def check_decode(got_out, got_lse, want, what=""):
     fin = np.isfinite(lse)
     assert np.array_equal(np.isfinite(glse), fin)
     assert (np.abs(glse[fin] - lse[fin]) <= t_lse[fin]).all(), f"{what}: lse"
+
+
+def in_a_fresh_process(code):
+    """Runs `code` where nothing has called the library yet."""
+    path = os.pathsep.join([os.path.dirname(TESTS), TESTS])
+    r = subprocess.run([sys.executable, "-c", code], cwd=TESTS, env={**os.environ, "PYTHONPATH": path},
+                       capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0, r.stdout[-2000:] + r.stderr[-2000:]

@@ -7,7 +7,7 @@ import numpy as np
 import pytest
 
 from oracle import paged as opaged
-from paged_common import Cache, bf16, i32, table_for
+from paged_common import Cache, bf16, i32, in_a_fresh_process, table_for
 
 pytestmark = pytest.mark.gpu
 
@@ -118,3 +118,24 @@ def test_refusals(cuda):
         assert e.value.status == code
     with pytest.raises(ValueError):
         binding.block_scores(q, c, t, n, out=torch.empty((2, 2, 3), dtype=torch.bfloat16, device=cuda))
+
+
+# Query rows whose fragments fill 48 KB of shared memory to the byte: 24, 12 and 6 MMAs.
+FULL = [(64, 1, 64, 3), (128, 2, 16, 6), (128, 1, 32, 3), (128, 1, 24, 4), (256, 1, 8, 6), (256, 1, 24, 2)]
+
+
+def fill_48_kb():
+    import torch
+    cuda = torch.device("cuda:0")
+    for D, heads, g, G in FULL:
+        rng = np.random.default_rng(D + g)
+        P, lengths = 32, [0, 70, 1000]
+        cache = Cache(5, 40, heads, P, D)
+        table = table_for(rng, lengths, P, 40)
+        q = opaged.bf16_round(rng.standard_normal((len(lengths) * G, heads * g, D)))
+        check(cuda, cache, q, table, lengths, G)
+
+
+def test_queries_that_fill_48_kb_are_a_process_first_call(cuda):
+    """The limit that a larger call raises is not there yet."""
+    in_a_fresh_process("import test_block_scores_gpu as t; t.fill_48_kb()")
