@@ -260,12 +260,9 @@ int launch_tables(const TableParams& p, int sms, smd_stream_t stream) {
     constexpr int kTokensPerBlock = 4 * kThreads;  // of one turn
     const size_t smem = (2 * static_cast<size_t>(p.R) + 1) * 4;  // at most 64 KB
     static_assert((2 * kMaxRequests + 1) * 4 <= 80 * 1024, "shared memory of the sums");
-    if (smem > 48 * 1024 &&
-        cudaFuncSetAttribute(block_tables_kernel<kThreads>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (2 * kMaxRequests + 1) * 4) != cudaSuccess) {
-        (void)cudaGetLastError();
-        return SMD_ERR_DEVICE;
-    }
+    static SharedLimit limit;
+    const int rc = limit.raise(block_tables_kernel<kThreads>, (2 * kMaxRequests + 1) * 4);
+    if (rc != SMD_OK) return rc;
     const int64_t want = (static_cast<int64_t>(p.T) + kTokensPerBlock - 1) / kTokensPerBlock;
     const int grid = static_cast<int>(want < 1 ? 1 : want < 2 * sms ? want : 2 * sms);
     return launch_pdl(block_tables_kernel<kThreads>, dim3(grid), kThreads, smem, stream, p);
@@ -305,5 +302,5 @@ extern "C" int smd_block_tables(const int32_t* lengths, const int32_t* new_token
     // Few requests take small blocks, whose sums are over fewer warps. 128 / 512 threads: 96
     // requests with a token each 5.1 / 5.9 us, 100 with 16 tokens 5.1 / 6.2, with 400 4.4 / 5.5.
     return R <= kSmall ? launch_tables<kSmall>(p, sms, stream)
-                                          : launch_tables<kThreadsMost>(p, sms, stream);
+                       : launch_tables<kThreadsMost>(p, sms, stream);
 }

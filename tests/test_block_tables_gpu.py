@@ -6,7 +6,7 @@ import numpy as np
 import pytest
 
 from oracle import paged as opaged
-from paged_common import i32
+from paged_common import i32, in_a_fresh_process
 
 pytestmark = pytest.mark.gpu
 
@@ -143,3 +143,17 @@ def test_streams_and_binding_refusals(cuda):
     with pytest.raises(binding.SmdError) as e:
         binding.block_tables(n, n, table, ring, state, 0, 4)
     assert e.value.status == binding.SMD_ERR_SHAPE
+
+
+def many_requests():
+    import torch
+    rng = np.random.default_rng(30)
+    for R in (6063, 6064, 6100, 6143, 6144):
+        lengths, table, ring, state = make(rng, R, 16, 3, 7000)
+        n = rng.integers(-1, 4, R).astype(np.int32)
+        check(torch.device("cuda:0"), lengths, n, table, ring, state, 16, 3 * R)
+
+
+def test_requests_whose_sums_fill_48_kb_are_a_process_first_call(cuda):
+    """The limit that a larger call raises is not there yet."""
+    in_a_fresh_process("import test_block_tables_gpu as t; t.many_requests()")
