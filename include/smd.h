@@ -819,14 +819,26 @@ int64_t smd_paged_workspace_bytes(const smd_paged_cache_t* cache);
  * lengths of the whole batch and the device's SM count, in a fixed order, so
  * equal calls give equal bits, but a request's bits may change with the
  * others in its batch. Returns SMD_OK, SMD_ERR_NULL, SMD_ERR_SHAPE,
- * SMD_ERR_ALIGN, SMD_ERR_WORKSPACE, SMD_ERR_DEVICE, SMD_ERR_LAUNCH;
- * SMD_ERR_TIMEOUT in `status` (optional) if a bounded wait runs out. */
+ * SMD_ERR_ALIGN, SMD_ERR_WORKSPACE, SMD_ERR_DEVICE, SMD_ERR_LAUNCH. If a
+ * bounded wait for a copy runs out, the rows it was for (out and lse) are NaN
+ * and `status` (optional) gets SMD_ERR_TIMEOUT. */
 int smd_paged_decode(const uint16_t* q, int64_t q_stride, const smd_paged_cache_t* cache,
                      const int32_t* table, int64_t table_stride, int32_t width,
                      const int32_t* lengths, int32_t R, int32_t row_group, int32_t Hq,
                      float sm_scale, const int32_t* block_lists, const int32_t* block_counts,
                      int32_t K, uint16_t* out, float* lse, int32_t* status, void* workspace,
                      int64_t workspace_bytes, smd_stream_t stream);
+
+/* As smd_paged_decode, with the testing hooks of `force` (may be NULL; its other
+ * fields are not read): wait_budget_us, and inject_stall = n > 0, by which the
+ * copy of every warp's n-th tile expects 16 bytes that nothing delivers, so that
+ * its wait runs out. For the tests. */
+int smd_paged_decode_ex(const uint16_t* q, int64_t q_stride, const smd_paged_cache_t* cache,
+                        const int32_t* table, int64_t table_stride, int32_t width,
+                        const int32_t* lengths, int32_t R, int32_t row_group, int32_t Hq,
+                        float sm_scale, const int32_t* block_lists, const int32_t* block_counts,
+                        int32_t K, uint16_t* out, float* lse, int32_t* status, void* workspace,
+                        int64_t workspace_bytes, smd_stream_t stream, const smd_plan_t* force);
 
 /* Static text for a status code. */
 const char* smd_status_str(int status);

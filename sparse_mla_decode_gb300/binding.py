@@ -210,6 +210,8 @@ def lib() -> ctypes.CDLL:
             so.smd_paged_decode.argtypes = rows + [ctypes.c_float, ptr, ptr, i32, ptr, ptr, ptr,
                                                    ptr, i64, ptr]
             so.smd_paged_decode.restype = ctypes.c_int
+            so.smd_paged_decode_ex.argtypes = so.smd_paged_decode.argtypes + [ctypes.POINTER(SmdPlan)]
+            so.smd_paged_decode_ex.restype = ctypes.c_int
             so.smd_status_str.argtypes = [ctypes.c_int]
             so.smd_version.restype = ctypes.c_int
             so.smd_version.argtypes = []
@@ -1075,15 +1077,17 @@ def paged_workspace_bytes(cache: PagedCache) -> int:
 
 def paged_decode(q, cache: PagedCache, table, lengths, sm_scale: float, row_group: int = 1,
                  block_lists=None, block_counts=None, out=None, lse=None, status=None,
-                 workspace=None, stream=None):
+                 workspace=None, stream=None, plan: SmdPlan | dict | None = None):
     """Attention over the cache (smd_paged_decode). q [R * row_group, Hq,
     head_dim] bfloat16 (rows may lie apart), table [R, width] and lengths [R]
     int32; block_lists [R * row_group, heads, K] int32: the pages of its request
     that each row and kv head attends (topk_select's output on block_scores),
     the first block_counts [R * row_group, heads] of them; None: all of its
     tokens. ``workspace``: a CUDA tensor of paged_workspace_bytes(cache) bytes,
-    zeroed once before its first use (allocated here if None). Returns (out [R * row_group, Hq, head_dim]
-    bfloat16, lse [R * row_group, Hq] float32)."""
+    zeroed once before its first use (allocated here if None). ``status`` is an optional int32
+    CUDA tensor: without one, a wait that runs out shows in NaN rows only. ``plan`` sets the
+    testing hooks (smd_paged_decode_ex). Returns (out [R * row_group, Hq, head_dim] bfloat16,
+    lse [R * row_group, Hq] float32)."""
     import torch
 
     args = _paged_rows(q, cache, table, lengths, row_group)
@@ -1110,11 +1114,13 @@ def paged_decode(q, cache: PagedCache, table, lengths, sm_scale: float, row_grou
         workspace = _new(torch.zeros, stream, paged_workspace_bytes(cache), torch.uint8, q.device)
     elif not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
-    rc = _so().smd_paged_decode(
-        *args, sm_scale, _ptr(block_lists) if K or block_lists is None else workspace.data_ptr(),
-        _ptr(block_counts), K, out.data_ptr(), lse.data_ptr(),
-        _ptr(status), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-        _stream(stream, q))
+    args += (sm_scale, _ptr(block_lists) if K or block_lists is None else workspace.data_ptr(),
+             _ptr(block_counts), K, out.data_ptr(), lse.data_ptr(), _ptr(status),
+             workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream, q))
+    if plan is None:
+        rc = _so().smd_paged_decode(*args)
+    else:
+        rc = _so().smd_paged_decode_ex(*args, ctypes.byref(_as_plan(plan)))
     if rc != SMD_OK:
         raise SmdError(rc, "smd_paged_decode")
     return out, lse

@@ -106,6 +106,8 @@ struct PagedParams {
     uint16_t* out;
     float* lse;
     int32_t* status;
+    uint64_t budget_ns; // bound of every wait
+    int32_t stall;      // n > 0: the copy of each warp's n-th tile never completes (tests)
     int32_t workers;    // warps of the grid
     int32_t* arrived;   // [2][2 CTAs]: arrivals at the joins of CTAs, 0 between calls
     float* head;        // [workers][rows of a tile][D]: the end of a unit begun by a warp before
@@ -472,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
         if (lane == (kk & 31)) {
             const int s = kk % ST;
             const uint32_t bar = bars + 8 * s, dst = ring + s * S::slot;
-            mbar_arrive_expect_tx(bar, S::slot);
+            mbar_arrive_expect_tx(bar, S::slot + (kk + 1 == p.stall ? 16 : 0));
 #pragma unroll
             for (int h = 0; h < NP; ++h) {
 #pragma unroll
@@ -492,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
     float2* const s_ml = reinterpret_cast<float2*>(gbase + S::off_ml);
     Left* const s_left = reinterpret_cast<Left*>(gbase + S::off_left);
     if (lane == 0) s_left[warp].ended = s_left[warp].open = -1;
-    bool ok = true;
+    bool ok = true;  // until a wait runs out; the same in every lane outside the tile loop
     int k = 0, t = t0, e = t0 < t1 ? find(t0, 0) : 0;
 #pragma unroll 1
     for (int s = 0; s < ST; ++s) issue(s);
@@ -604,10 +606,12 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
                 for (int j = 0; j < 4; ++j) o[n][c][j] = 0.0f;
 
 #pragma unroll 1
-        for (; t < tend; ++t, ++k) {
+        for (; t < tend && ok; ++t, ++k) {
             if (k > 0) issue(k + ST - 1);
             const int slot = k % ST;
-            mbar_wait(bars + 8 * slot, (k / ST) & 1, ok, p.status, kWaitBudgetNs);
+            mbar_wait(bars + 8 * slot, (k / ST) & 1, ok, p.status, p.budget_ns);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
             const uint32_t ks_at = ring + slot * S::slot, vs_at = ks_at + S::side;
 
             // logits: token 16 h + g (+ 8 for j >= 2), query row 8 n + 2 i + (j & 1)
@@ -807,6 +811,14 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
             __syncwarp();
         }
 
+        if (!ok) {
+            // A wait ran out: this unit and the warp's later ones are NaN (a NaN sum stays one
+            // through every join), and nothing more is issued.
+            t = tend;
+#pragma unroll
+            for (int n = 0; n < RT; ++n) l[n][0] = l[n][1] = NAN;
+        }
+
         // The unit's rows, or this warp's part of them.
         const bool whole = u0 >= t0 && u1 <= t1, open = u1 > t1;
         if (!whole) {
@@ -842,9 +854,11 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
                         out[8 * c] = bf16x2(o[n][c][y] * w, o[n][c][2 + y] * w);
                     if (qr == 0 && p.lse != nullptr) p.lse[at] = natural_lse(m[n][y], sum);
                 } else if (open) {
-                    // every tile of the ring has been consumed
+                    // every tile of the ring has been consumed (or, after a wait that ran out, the
+                    // ring is left to the copies in flight)
 #pragma unroll
                     for (int c = 0; c < NC; ++c) {
+                        if (!ok) break;
                         const uint32_t piece16 = (4 * c + (qr >> 1)) ^ (qi << 1);
                         sts64(ring + row * D * 4 + (piece16 << 4) + 8 * (qr & 1),
                               __float_as_uint(o[n][c][y] * vref), __float_as_uint(o[n][c][2 + y] * vref));
@@ -866,11 +880,12 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
             u = u_next;
         }
     }
-    // A wait that ran out left its copy in flight: none may outlive the warp.
+    // After a wait that ran out the copies of tiles k to k + ST - 1 are in flight: none may
+    // outlive the warp.
     if (!ok)
-        for (int j = max(k - ST, 0); j < k; ++j) {
+        for (int j = k; j < min(k + ST, t1 - t0); ++j) {
             bool done = true;
-            mbar_wait(bars + 8 * (j % ST), (j / ST) & 1, done, p.status, kWaitBudgetNs, true);
+            mbar_wait(bars + 8 * (j % ST), (j / ST) & 1, done, p.status, p.budget_ns, true);
         }
 
     // The CTA's warps: the units that cuts between them divide. Open partials of
@@ -1089,6 +1104,19 @@ extern "C" int smd_paged_decode(const uint16_t* q, int64_t q_stride, const smd_p
                                 const int32_t* block_counts, int32_t K, uint16_t* out, float* lse,
                                 int32_t* status, void* workspace, int64_t workspace_bytes,
                                 smd_stream_t stream) {
+    return smd_paged_decode_ex(q, q_stride, cache, table, table_stride, width, lengths, R, row_group, Hq,
+                               sm_scale, block_lists, block_counts, K, out, lse, status, workspace,
+                               workspace_bytes, stream, nullptr);
+}
+
+extern "C" int smd_paged_decode_ex(const uint16_t* q, int64_t q_stride,
+                                   const smd_paged_cache_t* cache, const int32_t* table,
+                                   int64_t table_stride, int32_t width, const int32_t* lengths,
+                                   int32_t R, int32_t row_group, int32_t Hq, float sm_scale,
+                                   const int32_t* block_lists, const int32_t* block_counts, int32_t K,
+                                   uint16_t* out, float* lse, int32_t* status, void* workspace,
+                                   int64_t workspace_bytes, smd_stream_t stream,
+                                   const smd_plan_t* force) {
     using namespace smd;
     bool skip;
     int rc = check_paged_rows(q, q_stride, cache, table, table_stride, width, lengths, R, row_group,
@@ -1136,6 +1164,10 @@ extern "C" int smd_paged_decode(const uint16_t* q, int64_t q_stride, const smd_p
     p.scale_log2 = sm_scale * 1.4426950408889634f;
     p.K = K;
     p.status = status;
+    p.budget_ns = force != nullptr && force->wait_budget_us > 0
+                      ? static_cast<uint64_t>(force->wait_budget_us) * 1000ull
+                      : kWaitBudgetNs;
+    p.stall = force != nullptr ? force->inject_stall : 0;
     p.arrived = static_cast<int32_t*>(workspace);
     const bool halves = page_box_tokens(*cache) < KT;  // a tile spans two pages
     CUtensorMap maps[2];

@@ -394,3 +394,37 @@ def test_what_a_call_allocates_is_made_on_its_stream(cuda, raw):
     got = out.cpu(), lse.cpu()
     torch.cuda.synchronize()
     check_decode(*got, oracle(cache, q, table, [4000]))
+
+
+@pytest.mark.parametrize("D,P,g,G,stall", [
+    (128, 64, 8, 1, 1), (128, 64, 8, 1, 4), (128, 16, 12, 2, 3), (128, 32, 32, 1, 2), (128, 48, 7, 4, 6),
+    (64, 16, 3, 4, 6), (64, 64, 30, 1, 5), (256, 32, 4, 1, 3), (256, 64, 16, 1, 2)])
+def test_a_wait_that_runs_out_gives_nan_rows_and_the_context_survives(cuda, D, P, g, G, stall):
+    """The copy of every warp's tile number `stall` never completes. Each row is right or NaN
+    throughout, the status says so, and the next call is right."""
+    import torch
+    from sparse_mla_decode_gb300 import binding
+    rng = np.random.default_rng(D + P + stall)
+    lengths = [200000, 0, 1, 40, 3000] + [int(n) for n in rng.integers(0, 700, 120)]
+    cache = Cache(6, 80, 2, P, D)
+    table = rng.integers(0, 80, (len(lengths), -(-200000 // P)))  # a range of 9 tiles or more for a warp
+    q = queries(rng, len(lengths) * G, 2 * g, D, 2.0)
+    ref = oracle(cache, q, table, lengths, G)
+    c = cache.to(cuda)
+    args = (bf16(q, cuda), c, i32(table, cuda), i32(lengths, cuda), D ** -0.5)
+    status = torch.zeros(1, dtype=torch.int32, device=cuda)
+    ws = torch.zeros(binding.paged_workspace_bytes(c), dtype=torch.uint8, device=cuda)
+    for with_status in (status, None):
+        out, lse = binding.paged_decode(*args, row_group=G, status=with_status, workspace=ws,
+                                        plan=dict(wait_budget_us=2000, inject_stall=stall))
+        torch.cuda.synchronize()
+        bad = np.isnan(lse.cpu().numpy())
+        assert np.array_equal(np.isnan(out.float().cpu().numpy()), np.broadcast_to(bad[..., None], out.shape))
+        assert bad.any() and (stall == 1) == bool(bad.all())
+        good = torch.from_numpy(~bad)
+        if not bad.all():
+            check_decode(out.cpu()[good], lse.cpu()[good], tuple(x[~bad] for x in ref), "rows not stalled")
+        ws.zero_()
+    assert int(status.item()) == binding.SMD_ERR_TIMEOUT
+    out, lse = binding.paged_decode(*args, row_group=G, workspace=ws)
+    check_decode(out, lse, ref, "after a wait that ran out")
