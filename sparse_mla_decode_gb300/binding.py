@@ -854,8 +854,9 @@ class PagedCache:
     k, v: [pages, heads, page_size, head_dim] E4M3 (uint8 or float8_e4m3fn), any
     strides in 16-byte steps with contiguous columns (a token-major pool is
     passed as ``pool.transpose(1, 2)``); k_scale, v_scale: [pages, heads]
-    float32; bounds: [pages, heads, 2, head_dim] bfloat16 or None. A cache that
-    only block_scores reads may leave k, v and the scales out (then
+    float32; bounds: [pages, heads, 2, head_dim] bfloat16 or None. All on one GPU,
+    where the calls on the cache run and every other tensor of theirs must be. A cache
+    that only block_scores reads may leave k, v and the scales out (then
     ``page_size`` says how many tokens a page holds)."""
 
     def __init__(self, k=None, v=None, k_scale=None, v_scale=None, bounds=None, page_size=None):
@@ -890,10 +891,11 @@ class PagedCache:
             if tuple(t.shape) != tuple(want) or t.dtype != dtype or not t.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {want}")
             setattr(c, name, _ptr(t))
+        self.device = _gpu(k if k is not None else v if v is not None else bounds, "the cache")
         for name, t in (("k", k), ("v", v), ("k_scale", k_scale), ("v_scale", v_scale),
                         ("bounds", bounds)):
-            if t is not None and not t.is_cuda:
-                raise ValueError(f"{name} must be a CUDA tensor")
+            if t is not None and t.get_device() != self.device:
+                raise ValueError(f"{name} must be on cuda:{self.device}")
         c.pages, c.heads, c.page_size, c.head_dim = (int(x) for x in shape)
         rc = lib().smd_paged_cache_init(ctypes.byref(c))
         if rc != SMD_OK:
@@ -923,16 +925,50 @@ def _so() -> ctypes.CDLL:
     return _lib if _lib is not None else lib()  # no lock once it is loaded
 
 
-def _stream(stream, t) -> int:
+_raw_stream = _cuda_device = None  # torch's, looked up once: an import costs a call 0.2 us
+
+
+def _stream(stream, dev: int) -> int:
     if stream is None:
-        import torch
-        return torch._C._cuda_getCurrentRawStream(t.device.index)
+        global _raw_stream
+        if _raw_stream is None:
+            import torch
+            _raw_stream = torch._C._cuda_getCurrentRawStream
+        return _raw_stream(dev)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _vector(t, name: str, dtype, n: int | None = None):
-    if not t.is_cuda or t.dtype != dtype or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor")
+def _gpu(t, name: str) -> int:
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return dev
+
+
+def _current_device() -> int:
+    global _cuda_device
+    if _cuda_device is None:
+        import torch
+        _cuda_device = torch._C._cuda_getDevice
+    return _cuda_device()
+
+
+def _entry(name: str, dev: int):
+    """The library's call ``name``, made on GPU ``dev``: it launches on the current one."""
+    call = getattr(_so(), name)
+    if _current_device() == dev:
+        return call
+    import torch
+
+    def there(*args):
+        with torch.cuda.device(dev):
+            return call(*args)
+    return there
+
+
+def _vector(t, name: str, dtype, dev: int, n: int | None = None):
+    if t.get_device() != dev or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor on cuda:{dev}")
     if n is not None and t.numel() < n:
         raise ValueError(f"{name} must have at least {n} elements")
 
@@ -953,8 +989,18 @@ def _output(t, name: str, dtype, n: int, like, stream):
     if t is None:
         import torch
         return _new(torch.empty, stream, n, dtype, like.device)
-    _vector(t, name, dtype, n)
+    _vector(t, name, dtype, like.get_device(), n)
     return t
+
+
+def _table(table, R: int, dev: int):
+    """Entries of a row that may be used, and from one row to the next."""
+    import torch
+    if table.get_device() == dev and table.dtype == torch.int32:
+        shape, steps = table.shape, table.stride()
+        if len(shape) == 2 and shape[0] >= R and steps[1] == 1:
+            return shape[1], steps[0] if shape[0] > 1 else shape[1]
+    raise ValueError(f"table must be an int32 tensor [>= {R}, width] on cuda:{dev} with contiguous rows")
 
 
 def block_tables(lengths, new_tokens, table, ring, state, page_size: int, max_tokens: int | None = None,
@@ -968,14 +1014,12 @@ def block_tables(lengths, new_tokens, table, ring, state, page_size: int, max_to
     positions [T]); the outputs may be given, and may not be the inputs."""
     import torch
 
-    R = lengths.numel()
-    _vector(lengths, "lengths", torch.int32)
-    _vector(new_tokens, "new_tokens", torch.int32, R)
-    _vector(ring, "ring", torch.int32)
-    _vector(state, "state", torch.int64, 2)
-    if not table.is_cuda or table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] < R \
-            or table.stride(1) != 1:
-        raise ValueError("table must be an int32 CUDA tensor [>= R, width] with contiguous rows")
+    R, dev = lengths.numel(), _gpu(lengths, "lengths")
+    _vector(lengths, "lengths", torch.int32, dev)
+    _vector(new_tokens, "new_tokens", torch.int32, dev, R)
+    _vector(ring, "ring", torch.int32, dev)
+    _vector(state, "state", torch.int64, dev, 2)
+    width, step = _table(table, R, dev)
     if slots is None:
         if max_tokens is None:
             raise ValueError("block_tables needs slots or max_tokens")
@@ -985,15 +1029,17 @@ def block_tables(lengths, new_tokens, table, ring, state, page_size: int, max_to
     new_lengths = _output(new_lengths, "new_lengths", torch.int32, R, lengths, stream)
     new_state = _output(new_state, "new_state", torch.int64, 2, lengths, stream)
     starts = _output(starts, "starts", torch.int32, R + 1, lengths, stream)
-    _vector(slots, "slots", torch.int32)
+    _vector(slots, "slots", torch.int32, dev)
     positions = _output(positions, "positions", torch.int32, T, lengths, stream)
     if new_lengths.data_ptr() == lengths.data_ptr() and R or new_state.data_ptr() == state.data_ptr():
         raise ValueError("new_lengths and new_state may not be lengths and state")
-    rc = _so().smd_block_tables(
-        lengths.data_ptr(), new_tokens.data_ptr(), R, table.data_ptr(), table.stride(0),
-        table.shape[1], ring.data_ptr(), ring.numel(), state.data_ptr(), page_size, T,
+    if status is not None:
+        _vector(status, "status", torch.int32, dev, 1)
+    rc = _entry("smd_block_tables", dev)(
+        lengths.data_ptr(), new_tokens.data_ptr(), R, table.data_ptr(), step, width,
+        ring.data_ptr(), ring.numel(), state.data_ptr(), page_size, T,
         new_lengths.data_ptr(), new_state.data_ptr(), starts.data_ptr(), slots.data_ptr(),
-        positions.data_ptr(), _ptr(status), _stream(stream, lengths))
+        positions.data_ptr(), _ptr(status), _stream(stream, dev))
     if rc != SMD_OK:
         raise SmdError(rc, "smd_block_tables")
     return new_lengths, new_state, starts, slots, positions
@@ -1005,19 +1051,19 @@ def paged_append(cache: PagedCache, k, v, slots, stream=None) -> None:
     (slices of a fused projection); slots [T] int32."""
     import torch
 
-    _vector(slots, "slots", torch.int32)
-    T = slots.numel()
+    dev = cache.device
+    _vector(slots, "slots", torch.int32, dev)
+    T, args = slots.numel(), (cache.ref,)
     for name, t in (("k", k), ("v", v)):
-        if not t.is_cuda or t.dtype != torch.bfloat16 or tuple(t.shape) != (
+        if t.get_device() != dev or t.dtype != torch.bfloat16 or t.shape != (
                 T, cache.heads, cache.head_dim):
-            raise ValueError(f"{name} must be a bfloat16 CUDA tensor "
-                             f"[{T}, {cache.heads}, {cache.head_dim}]")
-        if t.stride(2) != 1 or (cache.heads > 1 and t.stride(1) != cache.head_dim):
+            raise ValueError(f"{name} must be a bfloat16 tensor [{T}, {cache.heads}, "
+                             f"{cache.head_dim}] on cuda:{dev}")
+        steps = t.stride()
+        if steps[2] != 1 or (cache.heads > 1 and steps[1] != cache.head_dim):
             raise ValueError(f"{name}: a token's heads must be contiguous")
-    row = cache.heads * cache.head_dim
-    rc = _so().smd_paged_append(cache.ref, k.data_ptr(), k.stride(0) if T > 1 else row, v.data_ptr(),
-                                v.stride(0) if T > 1 else row, slots.data_ptr(), T,
-                                _stream(stream, slots))
+        args += (t.data_ptr(), steps[0] if T > 1 else cache.heads * cache.head_dim)
+    rc = _entry("smd_paged_append", dev)(*args, slots.data_ptr(), T, _stream(stream, dev))
     if rc != SMD_OK:
         raise SmdError(rc, "smd_paged_append")
 
@@ -1025,20 +1071,21 @@ def paged_append(cache: PagedCache, k, v, slots, stream=None) -> None:
 def _paged_rows(q, cache, table, lengths, row_group):
     import torch
 
-    R = lengths.numel()
-    _vector(lengths, "lengths", torch.int32)
-    if not q.is_cuda or q.dtype != torch.bfloat16 or q.dim() != 3 or q.shape[0] != R * row_group \
-            or q.shape[2] != cache.head_dim:
-        raise ValueError(f"q must be a bfloat16 CUDA tensor [{R} * {row_group}, Hq, {cache.head_dim}]")
-    if q.stride(2) != 1 or (q.shape[1] > 1 and q.stride(1) != cache.head_dim):
+    R, dev = lengths.numel(), cache.device
+    _vector(lengths, "lengths", torch.int32, dev)
+    shape = q.shape
+    if q.get_device() != dev or q.dtype != torch.bfloat16 or len(shape) != 3 \
+            or shape[0] != R * row_group or shape[2] != cache.head_dim:
+        raise ValueError(f"q must be a bfloat16 tensor [{R} * {row_group}, Hq, {cache.head_dim}] on "
+                         f"cuda:{dev}")
+    B, Hq, D = shape
+    steps = q.stride()
+    if steps[2] != 1 or (Hq > 1 and steps[1] != D):
         raise ValueError("q: a row's heads must be contiguous")
-    if not table.is_cuda or table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] < R \
-            or table.stride(1) != 1:
-        raise ValueError("table must be an int32 CUDA tensor [>= R, width] with contiguous rows")
-    width = table.shape[1]
-    return (q.data_ptr(), q.stride(0) if q.shape[0] > 1 else q.shape[1] * q.shape[2], cache.ref,
-            table.data_ptr(), table.stride(0) if table.shape[0] > 1 else width, width,
-            lengths.data_ptr(), R, row_group, q.shape[1])
+    q_stride = steps[0] if B > 1 else Hq * D
+    width, step = _table(table, R, dev)
+    return (q.data_ptr(), q_stride, cache.ref, table.data_ptr(), step, width, lengths.data_ptr(), R,
+            row_group, Hq)
 
 
 def block_scores(q, cache: PagedCache, table, lengths, row_group: int = 1, keep_first: int = 0,
@@ -1050,18 +1097,19 @@ def block_scores(q, cache: PagedCache, table, lengths, row_group: int = 1, keep_
     the pages a row sees; ``scores.flatten(0, 1)`` goes to topk_select."""
     import torch
 
-    args = _paged_rows(q, cache, table, lengths, row_group)
-    B, width = q.shape[0], table.shape[1]
+    args, dev = _paged_rows(q, cache, table, lengths, row_group), cache.device
+    B, heads, width = q.shape[0], cache.heads, table.shape[1]
     if out is None:  # rows of a multiple of 8 scores: topk_select reads them in 16-byte pieces
-        out = _new(torch.empty, stream, (B, cache.heads, (width + 7) // 8 * 8), torch.bfloat16,
-                   q.device)[:, :, :width]
-    if not out.is_cuda or out.dtype != torch.bfloat16 or tuple(out.shape) != (B, cache.heads, width) \
-            or out.stride(2) != 1 or (B > 1 and out.stride(0) != cache.heads * out.stride(1)):
-        raise ValueError(f"out must be a bfloat16 CUDA tensor [{B}, {cache.heads}, {width}] with "
-                         "evenly spaced rows")
-    stride = out.stride(1) if cache.heads > 1 else out.stride(0) if B > 1 else width
-    rc = _so().smd_block_scores(*args, keep_first, keep_last, out.data_ptr(), stride,
-                                _stream(stream, q))
+        stride = (width + 7) // 8 * 8
+        out = _new(torch.empty, stream, (B, heads, stride), torch.bfloat16, q.device)[:, :, :width]
+    else:
+        if out.get_device() != dev or out.dtype != torch.bfloat16 or out.shape != (B, heads, width) \
+                or out.stride(2) != 1 or (B > 1 and out.stride(0) != heads * out.stride(1)):
+            raise ValueError(f"out must be a bfloat16 tensor [{B}, {heads}, {width}] on cuda:{dev} "
+                             "with evenly spaced rows")
+        stride = out.stride(1) if heads > 1 else out.stride(0) if B > 1 else width
+    rc = _entry("smd_block_scores", dev)(*args, keep_first, keep_last, out.data_ptr(), stride,
+                                         _stream(stream, dev))
     if rc != SMD_OK:
         raise SmdError(rc, "smd_block_scores")
     return out
@@ -1069,7 +1117,7 @@ def block_scores(q, cache: PagedCache, table, lengths, row_group: int = 1, keep_
 
 def paged_workspace_bytes(cache: PagedCache) -> int:
     """Bytes of workspace paged_decode needs for this cache, whatever the batch."""
-    n = int(lib().smd_paged_workspace_bytes(cache.ref))
+    n = int(_entry("smd_paged_workspace_bytes", cache.device)(cache.ref))
     if n < 0:
         raise SmdError(n, "smd_paged_workspace_bytes")
     return n
@@ -1090,37 +1138,42 @@ def paged_decode(q, cache: PagedCache, table, lengths, sm_scale: float, row_grou
     lse [R * row_group, Hq] float32)."""
     import torch
 
-    args = _paged_rows(q, cache, table, lengths, row_group)
+    args, dev = _paged_rows(q, cache, table, lengths, row_group), cache.device
     B, Hq = q.shape[0], q.shape[1]
     K = 0
     if block_lists is not None:
-        _vector(block_lists, "block_lists", torch.int32)
+        _vector(block_lists, "block_lists", torch.int32, dev)
         if block_lists.dim() != 3 or tuple(block_lists.shape[:2]) != (B, cache.heads):
             raise ValueError(f"block_lists must be [{B}, {cache.heads}, K]")
         K = block_lists.shape[2]
         if block_counts is not None:
-            _vector(block_counts, "block_counts", torch.int32, B * cache.heads)
+            _vector(block_counts, "block_counts", torch.int32, dev, B * cache.heads)
     elif block_counts is not None:
         raise ValueError("block_counts without block_lists")
     if out is None:
         out = _new(torch.empty, stream, (B, Hq, cache.head_dim), torch.bfloat16, q.device)
-    elif tuple(out.shape) != (B, Hq, cache.head_dim):
-        raise ValueError(f"out must be [{B}, {Hq}, {cache.head_dim}]")
-    _vector(out, "out", torch.bfloat16)
+    else:
+        if out.shape != (B, Hq, cache.head_dim):
+            raise ValueError(f"out must be [{B}, {Hq}, {cache.head_dim}]")
+        _vector(out, "out", torch.bfloat16, dev)
     if lse is None:
         lse = _new(torch.empty, stream, (B, Hq), torch.float32, q.device)
-    _vector(lse, "lse", torch.float32, B * Hq)
+    else:
+        _vector(lse, "lse", torch.float32, dev, B * Hq)
     if workspace is None:
         workspace = _new(torch.zeros, stream, paged_workspace_bytes(cache), torch.uint8, q.device)
-    elif not workspace.is_cuda or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous CUDA tensor")
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
+    if status is not None:
+        _vector(status, "status", torch.int32, dev, 1)
     args += (sm_scale, _ptr(block_lists) if K or block_lists is None else workspace.data_ptr(),
-             _ptr(block_counts), K, out.data_ptr(), lse.data_ptr(), _ptr(status),
-             workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream, q))
+             _ptr(block_counts), K, out.data_ptr(), lse.data_ptr(),
+             _ptr(status), workspace.data_ptr(),
+             workspace.numel() * workspace.element_size(), _stream(stream, dev))
     if plan is None:
-        rc = _so().smd_paged_decode(*args)
+        rc = _entry("smd_paged_decode", dev)(*args)
     else:
-        rc = _so().smd_paged_decode_ex(*args, ctypes.byref(_as_plan(plan)))
+        rc = _entry("smd_paged_decode_ex", dev)(*args, ctypes.byref(_as_plan(plan)))
     if rc != SMD_OK:
         raise SmdError(rc, "smd_paged_decode")
     return out, lse

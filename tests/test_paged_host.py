@@ -154,3 +154,115 @@ def test_tables(kw, code):
 
 def test_the_new_status_has_a_text():
     assert smd.smd_status_str(smd.SMD_ERR_PAGES) != "unknown status"
+
+
+class OnGpu:
+    """A host tensor that says it is on a GPU."""
+
+    def __init__(self, t, index):
+        self.t, self.index, self.device, self.is_cuda = t, index, f"cuda:{index}", index >= 0
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+    def get_device(self):
+        return self.index
+
+
+@pytest.fixture
+def two_gpus(monkeypatch):
+    """The library's calls, recorded with the GPU that is current at each."""
+    import torch
+    now, calls = [0], []
+
+    class Library:
+        def __getattr__(self, name):
+            def call(*args):
+                calls.append((name, now[0]))
+                return 16 if name == "smd_paged_workspace_bytes" else smd.SMD_OK
+            return call
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.before, now[0] = now[0], self.index
+
+        def __exit__(self, *_):
+            now[0] = self.before
+
+    monkeypatch.setattr(smd, "lib", Library)
+    monkeypatch.setattr(smd, "_so", Library)
+    monkeypatch.setattr(smd, "_current_device", lambda: now[0])
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    return calls
+
+
+def paged_calls():
+    """Each call's tensors by name, and the call on them."""
+    import torch
+
+    def zeros(*shape, dtype=torch.int32):
+        return torch.zeros(shape, dtype=dtype)
+
+    bf, f32, u8 = torch.bfloat16, torch.float32, torch.uint8
+    cache = dict(k=zeros(4, 2, 16, 64, dtype=u8), v=zeros(4, 2, 16, 64, dtype=u8), k_scale=zeros(4, 2, dtype=f32),
+                 v_scale=zeros(4, 2, dtype=f32), bounds=zeros(4, 2, 2, 64, dtype=bf))
+    rows = dict(q=zeros(3, 4, 64, dtype=bf), table=zeros(3, 2), lengths=zeros(3))
+
+    def on_cache(call):
+        def with_cache(**t):
+            c = smd.PagedCache(**{n: t.pop(n) for n in cache})
+            call(c, t)
+        return with_cache
+
+    return {
+        "smd_block_tables": (dict(lengths=zeros(3), new_tokens=zeros(3), table=zeros(3, 2), ring=zeros(4),
+                                  state=zeros(2, dtype=torch.int64), new_lengths=zeros(3),
+                                  new_state=zeros(2, dtype=torch.int64), starts=zeros(4), slots=zeros(5),
+                                  positions=zeros(5), status=zeros(1)),
+                             lambda **t: smd.block_tables(page_size=16, stream=7, **t)),
+        "smd_paged_append": (dict(cache, k_new=zeros(5, 2, 64, dtype=bf), v_new=zeros(5, 2, 64, dtype=bf),
+                                  slots=zeros(5)),
+                             on_cache(lambda c, t: smd.paged_append(c, t["k_new"], t["v_new"], t["slots"], stream=7))),
+        "smd_block_scores": (dict(cache, **rows, out=zeros(3, 2, 2, dtype=bf)),
+                             on_cache(lambda c, t: smd.block_scores(cache=c, stream=7, **t))),
+        "smd_paged_decode": (dict(cache, **rows, block_lists=zeros(3, 2, 1), block_counts=zeros(3, 2),
+                                  out=zeros(3, 4, 64, dtype=bf), lse=zeros(3, 4, dtype=f32),
+                                  status=zeros(1), workspace=zeros(16, dtype=u8)),
+                             on_cache(lambda c, t: smd.paged_decode(cache=c, sm_scale=0.1, stream=7, **t)))}
+
+
+CALLS = ["smd_block_tables", "smd_paged_append", "smd_block_scores", "smd_paged_decode"]
+
+
+@pytest.mark.parametrize("name", CALLS)
+@pytest.mark.parametrize("index", [0, 1])
+def test_a_call_runs_on_the_gpu_of_its_tensors(two_gpus, name, index):
+    tensors, call = paged_calls()[name]
+    call(**{n: OnGpu(t, index) for n, t in tensors.items()})
+    assert (name, index) in two_gpus
+    if name == "smd_paged_decode":
+        cache = smd.PagedCache(bounds=OnGpu(tensors["bounds"], index), page_size=16)
+        assert smd.paged_workspace_bytes(cache) == 16
+        assert two_gpus[-1] == ("smd_paged_workspace_bytes", index)
+
+
+@pytest.mark.parametrize("name", CALLS)
+@pytest.mark.parametrize("elsewhere", [0, -1])
+def test_a_tensor_on_another_gpu_or_the_host_is_refused(two_gpus, name, elsewhere):
+    tensors, call = paged_calls()[name]
+    for odd in tensors:
+        with pytest.raises(ValueError):
+            call(**{n: OnGpu(t, elsewhere if n == odd else 1) for n, t in tensors.items()})
+    assert name not in [n for n, _ in two_gpus]
+
+
+@pytest.mark.parametrize("name", ["smd_block_tables", "smd_paged_decode"])
+def test_the_status_word_is_checked(two_gpus, name):
+    tensors, call = paged_calls()[name]
+    for status in (tensors["status"][:0], tensors["status"].long(), tensors["status"].float()):
+        with pytest.raises(ValueError):
+            call(**{n: OnGpu(t, 1) for n, t in dict(tensors, status=status).items()})
+    assert name not in [n for n, _ in two_gpus]
