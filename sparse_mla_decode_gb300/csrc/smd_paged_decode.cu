@@ -246,7 +246,7 @@ struct Shape {
     static constexpr int off_scan = off_bar + kWarps * ST * 8;    // [warps] words
     static constexpr int off_ml = off_scan + 32;                  // [warps][rows] maximum, sum
     static constexpr int off_left = off_ml + kWarps * rows * 8;   // [warps] what a warp leaves
-    static constexpr int off_prefix = off_left + kWarps * 64;     // [entries + 1], then [entries] lengths
+    static constexpr int off_prefix = off_left + kWarps * 64;     // [entries + 1], then [entries] lengths (of a list's row)
     static_assert(rows * D * 4 <= ST * slot, "a warp's accumulators fit its ring");
     static constexpr int smem(int entries) { return off_prefix + 4 * (2 * entries + 1) + 1024; }
 };
@@ -362,9 +362,14 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
     {
         const auto tiles_of = [&](int e) {
             if (e >= p.entries) return 0;
-            const int len = max(min(p.lengths[lists ? e / (p.heads * p.G) : e], p.width * p.page_size), 0);
-            int n = len;
-            if (lists) n = max(min(p.counts != nullptr ? p.counts[e] : p.K, p.K), 0) * p.page_size;
+            const int b = lists ? e / p.heads : e, r = lists ? b / p.G : e;  // row, or request
+            int len = max(min(p.lengths[r], p.width * p.page_size), 0), n = len;
+            if (lists) {
+                // The tokens that the list's row sees: a listed page past them is not read, so its
+                // scales reach nothing either.
+                len = max(len - p.G + 1 + b - r * p.G, 0);
+                n = max(min(p.counts != nullptr ? p.counts[e] : p.K, p.K), 0) * p.page_size;
+            }
             lens[e] = len;
             return max((n + KT - 1) / KT, 1) * p.x_units;
         };
@@ -520,11 +525,11 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
 #pragma unroll 1
     while (t < t1) {
         const int u0 = prefix[e] + x * nt, u1 = u0 + nt, tend = min(u1, t1);
-        const int len = lens[e], b0 = u.b0;
+        const int len = lens[e];
         const int m_real = u.m_real;
         // The tokens that row m of the tile sees.
         const auto row_limit = [&](int m) {
-            return max(len - p.G + 1 + (lists ? b0 % p.G : u.verify_row(p, m)), 0);
+            return lists ? len : max(len - p.G + 1 + u.verify_row(p, m), 0);
         };
         const int min_lim = row_limit(0), max_lim = row_limit(m_real - 1);
 

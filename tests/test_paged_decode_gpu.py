@@ -428,3 +428,18 @@ def test_a_wait_that_runs_out_gives_nan_rows_and_the_context_survives(cuda, D, P
     assert int(status.item()) == binding.SMD_ERR_TIMEOUT
     out, lse = binding.paged_decode(*args, row_group=G, workspace=ws)
     check_decode(out, lse, ref, "after a wait that ran out")
+
+
+@pytest.mark.parametrize("D,P,g", [(64, 16, 3), (64, 32, 8), (128, 64, 8), (128, 48, 20), (256, 32, 4)])
+def test_a_listed_page_that_only_a_later_verify_row_sees_does_not_matter(cuda, D, P, g):
+    """Its values' scale is far above the others', it comes first in every row's list."""
+    rng = np.random.default_rng(D + P)
+    G, lengths = 2, [4 * P + 1, 5 * P + 1]
+    cache = Cache(7, 20, 2, P, D)
+    table = table_for(rng, lengths, P, 20)
+    for r, n in enumerate(lengths):
+        cache.scales[1][table[r, (n - 1) // P]] = 2.0 ** 60  # of the last token alone, which row 1 sees
+    q = queries(rng, len(lengths) * G, 2 * g, D, 2.0)
+    lists = np.tile(np.array([[4, 0, 2, 1], [5, 0, 3, 1]]).repeat(G, 0)[:, None], (1, 2, 1))
+    ref = oracle(cache, q, table, lengths, G, lists)
+    check_decode(*run(cuda, cache, q, table, lengths, G, lists), ref)
