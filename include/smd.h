@@ -793,10 +793,10 @@ int64_t smd_paged_workspace_bytes(const smd_paged_cache_t* cache);
  * with k, v the values the codes stand for; a row that sees nothing gets
  * zeros and -inf. Sums and statistics are fp32; the weights enter the second
  * product as f16, at 2^7 for the running maximum that they are taken from (and up
- * to 2^15, for it moves in steps) times the page's scale over the largest so
- * far among the pages of the request's verify rows (11 bits while weight times
- * scale is within 2^-21 of the largest weight times the largest scale, a bit
- * less for each power of two below), the queries the first as f16 at a power of
+ * to 2^15, for it moves in steps) times the page's scale over the largest among
+ * it and the row's pages before it (11 bits while weight times scale is within
+ * 2^-21 of the largest weight times the largest scale, a bit less for each power
+ * of two below), the queries the first as f16 at a power of
  * two of each (row, head)'s maximum (exact but for elements below 2^-30 of it).
  *   block_lists   NULL: a row sees its first n = length - G + 1 + i tokens.
  *            Else [B, heads, K] int32 (row b, kv head h): page numbers within
@@ -814,7 +814,9 @@ int64_t smd_paged_workspace_bytes(const smd_paged_cache_t* cache);
  *            one. A call that reported an error in `status` may leave counts
  *            behind: zero it again.
  * The other arguments are smd_block_scores'. Codes of tokens that a row does
- * not see never reach its result, whatever they are. Table entries outside the
+ * not see never reach its result, whatever they are, nor do scales of pages that
+ * it sees nothing of (a finite one that a later verify row sees, and up to 2^100
+ * times the row's own). Table entries outside the
  * pool read nothing (their tokens count as zeros). The keys are cut by the
  * lengths of the whole batch and the device's SM count, in a fixed order, so
  * equal calls give equal bits, but a request's bits may change with the

@@ -760,12 +760,23 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
                     }
             }
 
-            // weights and the second product, relative to the largest scale of V so far
+            // weights and the second product, relative to the largest scale of V so far. Of two pages
+            // the first's products are done before the second's scale comes in: a verify row may
+            // not see the second at all, and its weights must keep their bits.
             const float vtop = fmaxf(fmaxf(vs[0], vs[NP - 1]), 1.17549435e-38f);
+            float ratio[NP], later = 1.0f;  // what the accumulators come down by between the pages
+#pragma unroll
+            for (int h = 0; h < NP; ++h) ratio[h] = vs[h] * vinv;
             if (vtop > vref) {
-                const float down = vref / vtop;
+                const float first = NP == 1 ? vtop : fmaxf(fmaxf(vs[0], vref), 1.17549435e-38f);
+                const float down = vref / first;
                 vref = vtop;
                 vinv = 1.0f / vref;
+                ratio[NP - 1] = vs[NP - 1] * vinv;
+                if (NP == 2) {
+                    ratio[0] = vs[0] / first;
+                    later = first / vtop;
+                }
 #pragma unroll
                 for (int n = 0; n < RT; ++n)
 #pragma unroll
@@ -776,7 +787,7 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
             uint32_t pb[NH][RT][2];
 #pragma unroll
             for (int h = 0; h < NH; ++h) {
-                const float ratio = vs[NP == NH ? h : 0] * vinv;
+                const float by = ratio[NP == NH ? h : 0];
 #pragma unroll
                 for (int n = 0; n < RT; ++n) {
                     float w[4];
@@ -789,7 +800,7 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
                                      pack2(-m[n][0], -m[n][1])), x0, x1);
                         const uint64_t pv = pack2(ex2_approx(x0), ex2_approx(x1));
                         sum = add2(sum, pv);
-                        unpack2(mul2(pv, pack2(ratio, ratio)), w[2 * z], w[2 * z + 1]);
+                        unpack2(mul2(pv, pack2(by, by)), w[2 * z], w[2 * z + 1]);
                     }
                     unpack2(sum, l[n][0], l[n][1]);
                     pb[h][n][0] = transpose8x8(f16x2(w[0], w[1]));
@@ -798,6 +809,14 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
             }
 #pragma unroll
             for (int h = 0; h < NH; ++h) {
+                if (NP == 2 && h == 1 && later != 1.0f) {
+#pragma unroll
+                    for (int n = 0; n < RT; ++n)
+#pragma unroll
+                        for (int c = 0; c < NC; ++c)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) o[n][c][j] *= later;
+                }
 #pragma unroll
                 for (int c = 0; c < NC; c += 2) {
                     uint32_t vr[4];

@@ -443,3 +443,27 @@ def test_a_listed_page_that_only_a_later_verify_row_sees_does_not_matter(cuda, D
     lists = np.tile(np.array([[4, 0, 2, 1], [5, 0, 3, 1]]).repeat(G, 0)[:, None], (1, 2, 1))
     ref = oracle(cache, q, table, lengths, G, lists)
     check_decode(*run(cuda, cache, q, table, lengths, G, lists), ref)
+
+
+@pytest.mark.parametrize("D,P,g,G,n", [(64, 16, 3, 2, 49), (64, 48, 8, 3, 146), (128, 16, 8, 4, 18),
+                                       (128, 80, 16, 2, 81), (128, 48, 12, 2, 241), (128, 64, 8, 2, 65),
+                                       (256, 16, 4, 2, 33)])
+def test_a_page_that_only_a_later_verify_row_sees_does_not_matter(cuda, D, P, g, G, n):
+    """The values of a draft token that begins a page are far above the others' (or infinite: 2^120 is
+    the scale that they are written with): the rows before it are as without it."""
+    for scale in (2.0 ** 60, 2.0 ** 120):
+        rng = np.random.default_rng(D + P)
+        lengths = [n, 3 * n]
+        cache = Cache(7, 60, 2, P, D)
+        table = table_for(rng, lengths, P, 60)
+        last = (n - 1) // P
+        cache.scales[1][table[0, last]] = scale
+        q = queries(rng, 2 * G, 2 * g, D, 2.0)
+        ref = oracle(cache, q, table, lengths, G)
+        seen = n - G + 1 + np.arange(G) > last * P
+        assert seen.any() and not seen.all()
+        out, lse = run(cuda, cache, q, table, lengths, G)
+        rows = np.concatenate([~seen, np.ones(G, dtype=bool)])
+        if scale == 2.0 ** 60:  # the rows that see it, too
+            rows[:] = True
+        check_decode(out.cpu()[rows], lse.cpu()[rows], tuple(x[rows] for x in ref), f"scale {scale}")
