@@ -72,7 +72,6 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxEntries = 1024;  // requests (or (row, kv head) lists) of one launch
-constexpr int kNoPos = 0x3fffffff; // the position of tokens that no row sees
 constexpr float kPShift = 7.0f;    // weights are 2^7 at the maximum kept
 constexpr float kSlack = 8.0f;     // which is moved when a logit exceeds it by 2^8
 constexpr float kNone = -3.402823466e38f;  // no logit met
@@ -332,6 +331,10 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
     constexpr int NH = KT / 16;   // 16-token halves of a tile
     constexpr int NP = S::NP;     // its pages
     constexpr int NC = D / 16;    // 16-column chunks
+    // The position of tokens that no row sees: past every row's end (lengths are whole pages below
+    // 2^31 at most, of 32 tokens where a tile has one position for 32) and, with the 31 or 15
+    // that are added to it, still an int.
+    constexpr int kNoPos = NH > NP ? 0x7fffffe0 : 0x7ffffff0;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
     uint8_t* const gbase = smem_raw + (base - smem_addr(smem_raw));
@@ -371,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
                 n = max(min(p.counts != nullptr ? p.counts[e] : p.K, p.K), 0) * p.page_size;
             }
             lens[e] = len;
-            return max((n + KT - 1) / KT, 1) * p.x_units;
+            return max(n / KT + (n % KT != 0 ? 1 : 0), 1) * p.x_units;
         };
         constexpr int kPer = kMaxEntries / kThreads;
         const int each = (p.entries + kThreads - 1) / kThreads;  // entries of a thread
@@ -491,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
                 }
             }
             sts_v4(meta + 32 * s, make_float4(td.ks[0], td.ks[NP - 1], td.vs[0], td.vs[NP - 1]));
-            sts64(meta + 32 * s + 16, td.pos[0], td.pos[NP - 1] + (NP == 1 ? 16 : 0));
+            sts64(meta + 32 * s + 16, td.pos[0], td.pos[NP - 1] + (NH > NP ? 16 : 0));
         }
         __syncwarp();
     };
@@ -686,7 +689,7 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
                     // V of tokens that some rows see and others do not: a NaN goes to the rows
                     // that see it here, and 0 stands in its place for the products.
 #pragma unroll 1
-                    for (int at = max(min_lim, pos[h]); at < min(max_lim, pos[h] + 16); ++at) {
+                    for (int at = max(min_lim, pos[h]); at < pos[h] + min(max_lim - pos[h], 16); ++at) {
                         const int j = 16 * h + at - pos[h];
                         uint32_t nan = 0;
 #pragma unroll

@@ -467,3 +467,56 @@ def test_a_page_that_only_a_later_verify_row_sees_does_not_matter(cuda, D, P, g,
         if scale == 2.0 ** 60:  # the rows that see it, too
             rows[:] = True
         check_decode(out.cpu()[rows], lse.cpu()[rows], tuple(x[rows] for x in ref), f"scale {scale}")
+
+
+@pytest.mark.parametrize("D,P,G", [(64, 16, 1), (64, 32, 2), (128, 64, 1), (256, 16, 1)])
+def test_requests_of_nearly_2_to_the_31_tokens(cuda, D, P, G):
+    """As long as the table allows. All pages but a few lie outside the pool, so their tokens count as
+    zeros: logits of 0 and no values."""
+    import torch
+    from sparse_mla_decode_gb300 import binding
+    rng = np.random.default_rng(D + P)
+    width = 2 ** 31 // P - 1
+    cache = Cache(8, 6, 1, P, D)
+    at = [0, 5, 2 ** 30 // P, width // 2, width - 2, width - 1]
+    table = torch.full((1, width), -1, dtype=torch.int32, device=cuda)
+    table[0, at] = torch.arange(6, dtype=torch.int32, device=cuda)
+    q = queries(rng, G, 1, D)
+    k, v = cache.values(0)[:, 0], cache.values(1)[:, 0]  # [6, P, D]
+    for row in range(6):  # a token of each page at a logit of about 24, where 2^31 zeros weigh 8 %
+        o = 3 * row % P if row < 5 else P - 1
+        code = q[G - 1, 0] * (24 * D ** 0.5 / (q[G - 1, 0] ** 2).sum())
+        cache.scales[0][row] = 2.0 ** -6
+        cache.codes[0][row, 0, o] = opaged.e4m3_encode(code * 64)
+        k[row] = opaged.VALUES[cache.codes[0][row, 0]] * 2.0 ** -6
+    c = cache.to(cuda)
+    for n in (width * P, width * P - 1, width * P - P + 1):
+        out, lse = binding.paged_decode(bf16(q, cuda), c, table, i32([n], cuda), D ** -0.5, row_group=G)
+        for i in range(G):
+            lim = n - G + 1 + i
+            seen = [min(max(lim - j * P, 0), P) for j in at]
+            ks = np.concatenate([k[r, :m] for r, m in enumerate(seen)])
+            vs = np.concatenate([v[r, :m] for r, m in enumerate(seen)])
+            s = ks @ q[i, 0] * D ** -0.5
+            total = np.exp(s).sum() + (lim - len(s))
+            ref = (np.exp(s) @ vs / total)[None, None]
+            reach = np.array([[D ** -0.5 * (np.abs(ks) @ np.abs(q[i, 0])).max()]])
+            check_decode(out[i:i + 1], lse[i:i + 1], (ref, np.array([[np.log(total)]]), reach,
+                                                      np.abs(vs).max(0)[None, None]), f"{n} {i}")
+
+
+@pytest.mark.parametrize("D,P", [(64, 16), (128, 32), (256, 48)])
+def test_lists_of_a_request_past_2_to_the_30_tokens(cuda, D, P):
+    """Listed pages that the row does not have are passed over there, too."""
+    rng = np.random.default_rng(D)
+    n = 2 ** 30 + 5 * P + 3
+    width = n // P + 3
+    cache = Cache(9, 6, 2, P, D)
+    table = np.full((1, width), -1, dtype=np.int32)
+    last = (n - 1) // P
+    at = [0, 1, last - 1, last]
+    table[0, at] = [3, 0, 5, 1]
+    lists = np.array([[[last, -1, width + 5, 0, last + 1, last + 2, -7], [-1, last - 1, -1, 1, -1, last + 1, 0]]])
+    q = queries(rng, 1, 6, D)
+    ref = oracle(cache, q, table, [n], 1, lists)
+    check_decode(*run(cuda, cache, q, table, [n], 1, lists), ref)
