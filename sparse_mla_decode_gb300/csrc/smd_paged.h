@@ -24,6 +24,12 @@ inline bool paged_ready(const smd_paged_cache_t* c) { return c->map[0] == kPaged
 
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
+// Pages that hold a number of tokens (0 to 2^31 - 1).
+__device__ __forceinline__ int pages_of(int tokens, int P) {
+    return static_cast<int>((static_cast<uint32_t>(tokens) + static_cast<uint32_t>(P) - 1) /
+                            static_cast<uint32_t>(P));
+}
+
 // Tokens of one copy box: the largest of 32 and 16 that divides a page (16 at
 // 256 columns, where the decode's tile holds 16 tokens).
 inline int page_box_tokens(const smd_paged_cache_t& c) {

@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(kThreads) block_scores_kernel(const ScoreParam
     const int block0 = blockIdx.x * kGroup * p.steps, block1 = block0 + kGroup * p.steps;
     pdl_entry();
     const int len = max(min(p.lengths[r], p.width * p.P), 0);
-    const int have = (len + p.P - 1) / p.P;  // pages that the last verify row sees
+    const int have = pages_of(len, p.P);  // pages that the last verify row sees
     const int64_t b0 = static_cast<int64_t>(r) * p.G;
 
     // Pages that no row sees: NaN.
@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(kThreads) block_scores_kernel(const ScoreParam
     load();
     look_up(block0 + 16 * warp + kGroup);
     if (tid < p.i_end - p.i0)
-        s_sees[tid] = (max(len - p.G + 1 + p.i0 + tid, 0) + p.P - 1) / p.P;
+        s_sees[tid] = pages_of(max(len - p.G + 1 + p.i0 + tid, 0), p.P);
     for (int idx = tid; idx < p.tiles * kJ * 32; idx += kThreads) {
         // Column l / 4 of a tile, the pieces of lane l. Columns beyond the heads repeat the
         // last one, which leaves the maximum as it is.

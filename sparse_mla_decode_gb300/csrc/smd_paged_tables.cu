@@ -51,11 +51,6 @@ struct Request {
     bool ended, narrow;
 };
 
-__device__ __forceinline__ int pages_of(int tokens, int P) {
-    return static_cast<int>((static_cast<uint32_t>(tokens) + static_cast<uint32_t>(P) - 1) /
-                            static_cast<uint32_t>(P));
-}
-
 __device__ __forceinline__ Request request(const TableParams& p, int r) {
     Request q;
     const int room = p.width * p.P;

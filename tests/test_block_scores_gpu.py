@@ -139,3 +139,26 @@ def fill_48_kb():
 def test_queries_that_fill_48_kb_are_a_process_first_call(cuda):
     """The limit that a larger call raises is not there yet."""
     in_a_fresh_process("import test_block_scores_gpu as t; t.fill_48_kb()")
+
+
+def test_a_request_of_nearly_2_to_the_31_tokens(cuda):
+    """As long as the table allows: every page is scored, up to the last one."""
+    import torch
+    from sparse_mla_decode_gb300 import binding
+    rng = np.random.default_rng(5)
+    P, D, width = 48, 64, 2 ** 31 // 48
+    cache = Cache(4, 5, 1, P, D)
+    table = torch.full((1, width), -1, dtype=torch.int32, device=cuda)
+    at = [0, 1, width // 2, width - 2, width - 1]
+    table[0, at] = i32([3, 1, 4, 0, 2], cuda)
+    q = opaged.bf16_round(rng.standard_normal((1, 3, D)))
+    c = binding.PagedCache(bounds=bf16(cache.bounds, cuda), page_size=P)
+    want = opaged.block_scores(q, cache.bounds, np.array([[3, 1, 4, 0, 2]]), [5 * P], P, 1)[0, 0]
+    for n in (width * P, width * P - P + 1, width * P - P):  # the last page is seen whole, a token, not
+        s = binding.block_scores(bf16(q, cuda), c, table, i32([n], cuda))[0, 0]
+        sees = -(-n // P)
+        assert bool(torch.isnan(s[sees:]).all()) and not bool(torch.isnan(s[:sees]).any())
+        assert int((s[:sees] != 0).sum()) == 5 - (width - sees)
+        got = s[at].float().cpu().numpy()[:5 - (width - sees)]
+        size = np.abs(q).max() * np.abs(cache.bounds).max() * D
+        assert (np.abs(got - want[:len(got)]) <= 2.0 ** -8 * np.abs(want[:len(got)]) + 2.0 ** -17 * size).all()
