@@ -86,6 +86,12 @@ def main(argv=None) -> int:
     ap.add_argument("--steps", type=int, default=8)
     ap.add_argument("--pages", type=int, default=64)
     args = ap.parse_args(argv)
+    for name in ("requests", "context", "steps", "pages"):
+        if getattr(args, name) < 1:
+            ap.error(f"--{name} must be at least 1")
+    if args.requests > 8192:
+        ap.error("--requests must be at most 8192")
+    replays = (args.steps + 1) // 2  # of two steps each
 
     import torch
 
@@ -128,11 +134,11 @@ def main(argv=None) -> int:
         graph.replay()
         start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
         start.record()
-        for _ in range(args.steps // 2):
+        for _ in range(replays):
             graph.replay()
         end.record()
         torch.cuda.synchronize()
-        times[name] = start.elapsed_time(end) * 1e3 / (args.steps // 2 * 2)
+        times[name] = start.elapsed_time(end) * 1e3 / (2 * replays)
         assert int(s.status) == 0, "device status"
         if pages is not None:
             _, lse = s.attend(q)

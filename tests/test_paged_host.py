@@ -266,3 +266,12 @@ def test_the_status_word_is_checked(two_gpus, name):
         with pytest.raises(ValueError):
             call(**{n: OnGpu(t, 1) for n, t in dict(tensors, status=status).items()})
     assert name not in [n for n, _ in two_gpus]
+
+
+@pytest.mark.parametrize("option,value", [("--requests", 0), ("--requests", 8193), ("--context", 0), ("--steps", 0),
+                                          ("--steps", -2), ("--pages", 0)])
+def test_the_step_command_refuses_sizes_that_it_cannot_run(option, value, capsys):
+    from sparse_mla_decode_gb300 import paged_step
+    with pytest.raises(SystemExit) as e:
+        paged_step.main([option, str(value)])
+    assert e.value.code == 2 and option in capsys.readouterr().err

@@ -59,3 +59,11 @@ def test_the_command_runs(cuda, capsys):
     from sparse_mla_decode_gb300 import paged_step
     assert paged_step.main(["--requests", "3", "--context", "700", "--steps", "4", "--pages", "4"]) == 0
     assert "step over all tokens" in capsys.readouterr().out
+
+
+@pytest.mark.parametrize("steps", [1, 3])
+def test_the_command_runs_an_odd_number_of_steps(cuda, capsys, steps):
+    """The table has room for them all: the status is checked by the command."""
+    from sparse_mla_decode_gb300 import paged_step
+    assert paged_step.main(["--requests", "2", "--context", "64", "--steps", str(steps), "--pages", "2"]) == 0
+    assert "step over all tokens" in capsys.readouterr().out
