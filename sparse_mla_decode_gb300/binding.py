@@ -1104,7 +1104,8 @@ def block_scores(q, cache: PagedCache, table, lengths, row_group: int = 1, keep_
         out = _new(torch.empty, stream, (B, heads, stride), torch.bfloat16, q.device)[:, :, :width]
     else:
         if out.get_device() != dev or out.dtype != torch.bfloat16 or out.shape != (B, heads, width) \
-                or out.stride(2) != 1 or (B > 1 and out.stride(0) != heads * out.stride(1)):
+                or out.stride(2) != 1 \
+                or (B > 1 and heads > 1 and out.stride(0) != heads * out.stride(1)):
             raise ValueError(f"out must be a bfloat16 tensor [{B}, {heads}, {width}] on cuda:{dev} "
                              "with evenly spaced rows")
         stride = out.stride(1) if heads > 1 else out.stride(0) if B > 1 else width

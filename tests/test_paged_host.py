@@ -275,3 +275,18 @@ def test_the_step_command_refuses_sizes_that_it_cannot_run(option, value, capsys
     with pytest.raises(SystemExit) as e:
         paged_step.main([option, str(value)])
     assert e.value.code == 2 and option in capsys.readouterr().err
+
+
+def test_scores_of_one_head_go_to_rows_of_any_spacing(two_gpus):
+    """A dimension of one head has whatever stride the caller's view gave it."""
+    import torch
+    tensors, call = paged_calls()["smd_block_scores"]
+    one = {n: t[:, :1].contiguous() if n in ("k", "v", "k_scale", "v_scale", "bounds") else t
+           for n, t in tensors.items()}
+    wide = torch.zeros((3, 9), dtype=torch.bfloat16)
+    for out in (wide[:, None, :2], wide[:, :2][:, None], wide.as_strided((3, 1, 2), (9, 100, 1))):
+        call(**{n: OnGpu(t, 0) for n, t in dict(one, out=out).items()})
+    assert [n for n, _ in two_gpus].count("smd_block_scores") == 3
+    two = dict(tensors, out=torch.zeros((3, 5, 2), dtype=torch.bfloat16)[:, :2])
+    with pytest.raises(ValueError):
+        call(**{n: OnGpu(t, 0) for n, t in two.items()})
