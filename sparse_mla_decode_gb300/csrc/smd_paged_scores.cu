@@ -157,6 +157,7 @@ __global__ void __launch_bounds__(kThreads) block_scores_kernel(const ScoreParam
         float run[2] = {0.0f, 0.0f};
 #pragma unroll 1
         for (int tile = 0; tile < p.tiles; ++tile) {
+            __syncwarp();  // some lanes wrote the scores of the tile before; the MMAs are the warp's
             // page g: columns 2 i, 2 i + 1; page g + 8. Four sums, so that the MMAs do not wait
             // for one another.
             float d[4] = {}, d1[4] = {}, d2[4] = {}, d3[4] = {};
