@@ -744,10 +744,13 @@ int smd_block_tables(const int32_t* lengths, const int32_t* new_tokens, int32_t 
  * A power of two as scale makes both quotients exact, so a kept token loses
  * nothing but what falls off at the small end; the codes have the same
  * relative precision with any scale. Tokens of the page after the run are not
- * kept (a shorter run later writes over rejected tokens). bounds (unless
- * NULL) becomes the largest and smallest key of each channel, of the run and,
- * if o > 0, of the bounds before; NaN are passed over, infinities count as
- * the largest finite values.
+ * kept (a shorter run later writes over rejected tokens), but what they did to
+ * the page stays until a run begins it anew: a scale does not come down, so what
+ * the small end of kept codes lost to a rejected token's large value is lost (an
+ * infinite one takes all of them to zero), and bounds stay as wide.
+ * bounds (unless NULL) becomes the largest and smallest key of each channel, of
+ * the run and, if o > 0, of the bounds before; NaN are passed over, infinities
+ * count as the largest finite values.
  * T >= 0 (0: no-op). Returns SMD_OK, SMD_ERR_NULL, SMD_ERR_SHAPE,
  * SMD_ERR_ALIGN, SMD_ERR_DEVICE, SMD_ERR_LAUNCH. */
 int smd_paged_append(const smd_paged_cache_t* cache, const uint16_t* k, int64_t k_stride,
@@ -757,9 +760,12 @@ int smd_paged_append(const smd_paged_cache_t* cache, const uint16_t* k, int64_t 
 /* An upper bound, up to its rounding, of the products of a row's queries with
  * the keys of each page: for row b, kv head h and page j of its request,
  *   score[b, h, j] = BF16(max over the query heads i of h of
- *                         sum_c max(q[b,i,c] * hi[c], q[b,i,c] * lo[c]))
- * with hi, lo the bounds of the page; query heads h * Hq / heads and the
- * Hq / heads - 1 after it are those of kv head h (at most 128 of them).
+ *                    sum_c max(q[b,i,c], 0) * hi[c] + min(q[b,i,c], 0) * lo[c])
+ * with hi, lo the bounds of the page: the larger of q * hi and q * lo in each
+ * channel. (A channel whose keys were all NaN has hi < lo, the extremes of
+ * bfloat16, and takes the smaller: such a page scores lowest.) Query heads
+ * h * Hq / heads and the Hq / heads - 1 after it are those of kv head h (at most
+ * 128 of them).
  *   q        [B, Hq, head_dim] bfloat16, row b at q + b * q_stride (elements; a
  *            multiple of 8; rows of heads are head_dim apart), 16-byte aligned,
  *            finite. B = R * row_group.
@@ -773,6 +779,8 @@ int smd_paged_append(const smd_paged_cache_t* cache, const uint16_t* k, int64_t 
  *   scores   [B, heads, score_stride] bfloat16, written up to width; the pages
  *            past those a row sees get NaN, which smd_topk_select passes over.
  * Table entries outside the pool read nothing and score as zero bounds would.
+ * Bounds (SMD_ERR_SHAPE): Hq <= 65535, R * row_group * Hq < 2^31, width *
+ * page_size < 2^31.
  * Returns SMD_OK, SMD_ERR_NULL (also: a cache without bounds), SMD_ERR_SHAPE,
  * SMD_ERR_ALIGN, SMD_ERR_DEVICE, SMD_ERR_LAUNCH. */
 int smd_block_scores(const uint16_t* q, int64_t q_stride, const smd_paged_cache_t* cache,
@@ -814,13 +822,20 @@ int64_t smd_paged_workspace_bytes(const smd_paged_cache_t* cache);
  *            one. A call that reported an error in `status` may leave counts
  *            behind: zero it again.
  * The other arguments are smd_block_scores'. Codes of tokens that a row does
- * not see never reach its result, whatever they are, nor do scales of pages that
- * it sees nothing of (a finite one that a later verify row sees, and up to 2^100
- * times the row's own). Table entries outside the
- * pool read nothing (their tokens count as zeros). The keys are cut by the
- * lengths of the whole batch and the device's SM count, in a fixed order, so
- * equal calls give equal bits, but a request's bits may change with the
- * others in its batch. Returns SMD_OK, SMD_ERR_NULL, SMD_ERR_SHAPE,
+ * not see never reach its result, whatever they are, nor do the scales of pages
+ * that it sees nothing of (finite ones, of values up to 2^100 times its own, where
+ * a later verify row sees the page). Table entries outside the pool read nothing
+ * (their tokens count as zeros). The keys are cut by the lengths of the whole
+ * batch and the device's SM count, in a fixed order, so equal calls give equal
+ * bits, but a request's bits may change with the others in its batch. Values
+ * beyond about 2^113 may give infinities (weights of up to 2^15 times them are
+ * summed in fp32).
+ * Bounds (SMD_ERR_SHAPE), beside smd_block_scores', with T = 32 tokens (16 at 256
+ * columns) and M = 32 query rows (16):
+ *   (ceil(width * page_size / T) + 4) * heads * ceil(row_group * Hq / heads / M)
+ *   < 2^30; with lists K * page_size < 2^31 and
+ *   (ceil(K * page_size / T) + 4) * row_group * heads * ceil(Hq / heads / M) < 2^30.
+ * Returns SMD_OK, SMD_ERR_NULL, SMD_ERR_SHAPE,
  * SMD_ERR_ALIGN, SMD_ERR_WORKSPACE, SMD_ERR_DEVICE, SMD_ERR_LAUNCH. If a
  * bounded wait for a copy runs out, the rows it was for (out and lse) are NaN
  * and `status` (optional) gets SMD_ERR_TIMEOUT. */

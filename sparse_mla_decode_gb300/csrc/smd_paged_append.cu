@@ -23,7 +23,7 @@
 // Measured (GB300): 96 tokens of as many requests, 8 heads of 128 columns, 2.5 us; 28
 // thousand tokens of 23 requests 37 us (68% of the copy rate for the 173 MB: the
 // slots, a run's loads, its maximum and its stores follow one another, and 20 warps
-// an SM do not quite cover that), 16 thousand of one 37 us (79%).
+// an SM do not quite cover that), 16 thousand of one 21 us (69%).
 #include "smd_internal.h"
 #include "smd_paged.h"
 #include "smd_ptx.cuh"
@@ -501,9 +501,21 @@ __global__ void __launch_bounds__(kThreads, 5) append_many_kernel(const AppendPa
 
 template <int D>
 int launch_append(const AppendParams& p, int sms, smd_stream_t stream) {
-    // Few tokens: lanes for each token. Many: blocks by chunks of tokens. 8 heads of 128
-    // columns, few / many: 1000 tokens of as many requests 5.5 / 23.6 us, 2400 11.3 / 25.4,
-    // 900 tokens of 30 requests 13 / 10.4, 4000 tokens of one request 45 / 14.7.
+    // Few tokens: lanes for each token. Many: blocks by chunks of tokens. The rule is set for
+    // runs of a token or a few, which is what a step writes; it does not know the runs' length,
+    // and a prompt below the limit (2432 tokens at 8 heads, 19456 at one) takes the slower form.
+    // Pages of 64 tokens of 128 columns, few / many in us, * where the rule takes the slower:
+    //                                      1 head         2 heads        4 heads        8 heads
+    //   96 tokens of as many requests      2.3 / 14.0     2.3 / 14.5     2.4 / 14.9     2.5 / 15.2
+    //   1000 of as many                    2.6 / 15.5     3.2 / 16.3     3.3 / 17.3     5.2 / 18.0
+    //   2400 of as many                    2.8 / 16.3     3.4 / 18.1     6.1 / 18.0    10.6 / 21.4
+    //   900 of 30                          6.1 /  7.8     6.4 /  7.9     7.7 /  8.1     9.5 /  8.4 *
+    //   4000 of 30                        10.6 /  5.7 *  13.9 /  5.8 *  21.3 /  6.3 *  29.6 /  8.3
+    //   16000 of 30                       18.4 /  6.7 *  27.8 /  8.6    43.7 / 15.3    62.3 / 23.2
+    //   500 of one                        10.1 /  4.2 *  10.2 /  4.2 *  12.4 /  4.2 *  15.8 /  4.3 *
+    //   1000 of one                        9.9 /  4.1 *  10.4 /  4.2 *  15.2 /  4.3 *  18.6 /  4.5 *
+    //   4000 of one                       10.7 /  4.3 *  14.8 /  4.7 *  21.3 /  5.5 *  29.8 /  6.6
+    //   16000 of one                      19.1 /  5.8 *  28.3 /  6.6    44.1 / 13.3    62.2 / 21.2
     const int64_t units = static_cast<int64_t>(p.T) * p.heads * 2;
     if (units <= static_cast<int64_t>(sms) * 256)
         return launch_pdl(append_few_kernel<D>,

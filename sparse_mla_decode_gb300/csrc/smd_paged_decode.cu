@@ -46,20 +46,28 @@
 // never sees its range.
 //
 // Measured (GB300, device time; of the rate at which the GPU copies):
-//   64 requests of 1024 .. 8192 tokens, 8 query rows of 128 columns   107 us   84%
-//   64 listed pages of 64 tokens in each of 64 requests               101 us   79%
+//   64 requests of 1024 .. 8192 tokens, 8 query rows of 128 columns   108 us   84%
+//   64 listed pages of 64 tokens in each of 64 requests               102 us   78%
 //   16 requests up to 131072 tokens, 32 query rows                    425 us   76%
-//   31 requests up to 5001 tokens, 12 query rows of 64 columns         32 us   37%
-//   one request of 777 tokens                                         9.6 us
+//   31 requests up to 5001 tokens, 12 query rows of 64 columns         33 us   36%
+//   one request of 777 tokens                                         9.5 us
+//   32 requests of 1024 .. 8192 tokens, 8 query rows of 256 columns   109 us   79%
+//   the same, 16 / 32 query rows of 256 columns             127 us   68% / 204 us   43%
+//   16 requests of 4096 .. 65536 tokens, 32 / 64 query rows 223 us   72% / 414 us   39%
+//   128 query heads over one kv head, 16 such requests                129 us   16%
 // What bounds it now. The start costs 4 us before a copy is on its way (lengths,
 // table entry, copy: three round trips and the launch), the joins 5 to 9 us after
 // the last tile: all of the time of one short request, half of that of a small batch.
 // (The joins run once a CTA, from instructions that are not cached yet: they are
 // kept short, which took 1 to 2.5 us off each of these.) At 8 rows the rest is HBM,
 // and its unevenness: some neighbourhoods of SMs stream 7% slower than the others,
-// the same ones every time. At 32 rows the 255 registers a lane leave 8 warps an
+// the same ones every time. At 32 rows the 254 registers a lane leave 8 warps an
 // SM, and the products' and softmax's latencies show (mma.sync takes 8 cycles a
-// sub-partition, 52% of the time in all; issue 38%).
+// sub-partition, 52% of the time in all; issue 38%). Past 32 rows (16 at 256 columns) the
+// cache is read again for each 32, by other warps; past 1024 requests, or 1024 (row, kv head)
+// lists, the call is as many launches as that takes, each with its start and joins (1024
+// requests up to 300 tokens 80 us, 1025 110; 1000 requests with 4 listed pages for each of 8
+// heads, eight launches, 244 us for 82 us of bytes; 256 with 64 pages, two, 373 us: 85%).
 #include <cstring>
 
 #include "smd_internal.h"
@@ -1027,7 +1035,7 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
         };
 #pragma unroll 1
         for (int i0 = me; i0 < u.m_real * (D / 4); i0 += 2 * threads) {
-            // Two pieces of 4 columns, 8 partials of each: one round trip.
+            // Two pieces of 4 columns, kMany partials of each: one round trip.
             constexpr int kMany = 4;
             int row[2], col[2];
             float4 acc[2];
