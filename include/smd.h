@@ -657,7 +657,7 @@ int smd_trace_clear(int32_t kernel);
  *             they were before rounding to E4M3. smd_paged_append keeps them,
  *             smd_block_scores reads them. 16-byte aligned.
  *   pages     >= 1; pages * page_size < 2^31.
- *   heads     key/value heads, >= 1.
+ *   heads     key/value heads, 1 to 65535.
  *   page_size tokens of a page, a multiple of 16 up to 256.
  *   head_dim  64, 128 or 256.
  *   map       filled in by smd_paged_cache_init (the copy descriptors of k and
@@ -717,7 +717,7 @@ int smd_paged_cache_init(smd_paged_cache_t* cache);
  * The outputs must not overlap lengths, new_tokens or state (the step's blocks
  * read them while others write): a caller alternates two buffers. Bounds: 0
  * <= R <= 8192, 0 <= T, 1 <= pages, pages * P < 2^31, 1 <= P, 1 <= width <=
- * table_stride (SMD_ERR_SHAPE). An entry of lengths below 0 or beyond
+ * table_stride, width * P < 2^31 (SMD_ERR_SHAPE). An entry of lengths below 0 or beyond
  * width * P is clamped. Pointers are device memory, 4-byte aligned (state,
  * new_state: 8); `status` may be NULL. */
 int smd_block_tables(const int32_t* lengths, const int32_t* new_tokens, int32_t R,
