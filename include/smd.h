@@ -857,6 +857,183 @@ int smd_paged_decode_ex(const uint16_t* q, int64_t q_stride, const smd_paged_cac
                         int32_t K, uint16_t* out, float* lse, int32_t* status, void* workspace,
                         int64_t workspace_bytes, smd_stream_t stream, const smd_plan_t* force);
 
+/* ---- a paged key/value cache in E2M1, and the step around it --------------------
+ *
+ * The same cache with 4 bits a value: keys and values in E2M1 (0, 0.5, 1, 1.5, 2,
+ * 3, 4, 6 and their negatives) with an E4M3 scale for each token, head and block of
+ * 16 columns, 4.5 bits in all. smd_qk_norm_rope prepares a step's queries and keys,
+ * smd_paged4_append writes, smd_paged4_read reads back, smd_paged4_decode attends;
+ * smd_verify_drafts says which drafted tokens stay, and smd_block_trim gives back
+ * the pages of those that do not. Tables and slots are smd_block_tables', page
+ * scores smd_block_scores' (on a smd_paged_cache_t that has the cache's bounds, and no k and v).
+ *
+ *   k, v      codes, two a byte (column 2 c in the low nibble of byte c): byte c of
+ *             (page p, head h, token t) is at k + p * k_stride[0] + h * k_stride[1]
+ *             + t * k_stride[2] + c. Addresses and strides are multiples of 16 bytes.
+ *   k_scales, v_scales   [pages, heads, page_size, head_dim / 16] E4M3, contiguous,
+ *             16-byte aligned.
+ *   k_exp, v_exp   [heads] int32, or NULL (zeros): a code stands for
+ *             code * block scale * 2^exp. An exponent beyond +-100 counts as +-100.
+ *             Keys or values of a head whose sizes lie between 2^-8 and 2^11 need
+ *             none; others are brought there.
+ *   bounds, pages, heads, page_size, head_dim   as in smd_paged_cache_t.
+ *   map       filled in by smd_paged4_cache_init. */
+typedef struct {
+    uint8_t* k;
+    uint8_t* v;
+    uint8_t* k_scales;
+    uint8_t* v_scales;
+    const int32_t* k_exp;
+    const int32_t* v_exp;
+    uint16_t* bounds;
+    int64_t k_stride[3];
+    int64_t v_stride[3];
+    int32_t pages;
+    int32_t heads;
+    int32_t page_size;
+    int32_t head_dim;
+    uint64_t map[68];
+} smd_paged4_cache_t;
+
+/* Checks the description and fills in `map`. Host only. Returns SMD_OK,
+ * SMD_ERR_NULL (cache, k, v or a scale is NULL), SMD_ERR_SHAPE (the ranges of
+ * smd_paged_cache_t; a token stride below head_dim / 2, or strides that are not
+ * positive or beyond 2^40), SMD_ERR_ALIGN, SMD_ERR_DEVICE. */
+int smd_paged4_cache_init(smd_paged4_cache_t* cache);
+
+/* Writes T tokens' keys and values into the cache; the arguments are
+ * smd_paged_append's. For each token, head and block of 16 columns, with x the
+ * values times 2^-exp of the head (in fp32):
+ *   scale = E4M3(max|x| / 6), to nearest (ties to even), saturating at 448
+ *   code  = E2M1(x / scale), to nearest (ties to even), saturating at +-6; zeros
+ *           where the scale is 0
+ * with quotients that are exact before they are rounded. An infinity counts as larger
+ * than everything finite (scale 448, code +-6). A NaN makes its block's scale NaN, and with
+ * it the block. The sign of a zero is not kept.
+ * A token's codes depend on nothing else: tokens of a page before and after it stay as
+ * they are, and a slot may be written again (rejected tokens). A slot is at most once
+ * in a call.
+ * bounds (unless NULL) becomes what smd_paged_append makes of them, runs as there: a
+ * page may be in one run of a call.
+ * Returns SMD_OK, SMD_ERR_NULL, SMD_ERR_SHAPE, SMD_ERR_ALIGN, SMD_ERR_PLAN (a cache
+ * without smd_paged4_cache_init), SMD_ERR_DEVICE, SMD_ERR_LAUNCH. */
+int smd_paged4_append(const smd_paged4_cache_t* cache, const uint16_t* k, int64_t k_stride,
+                      const uint16_t* v, int64_t v_stride, const int32_t* slots, int32_t T,
+                      smd_stream_t stream);
+
+/* The keys and values of T slots as bfloat16, which holds them exactly: row t of k and v is
+ * [heads, head_dim] and starts at k + t * k_stride (elements; a multiple of 8;
+ * 16-byte aligned). A negative slot, or one beyond the pool, leaves its rows as they
+ * are; a slot may be read many times. k or v may be NULL. T >= 0. Returns as
+ * smd_paged4_append. */
+int smd_paged4_read(const smd_paged4_cache_t* cache, const int32_t* slots, int32_t T, uint16_t* k,
+                    int64_t k_stride, uint16_t* v, int64_t v_stride, smd_stream_t stream);
+
+/* Bytes of workspace smd_paged4_decode needs for this cache on the current
+ * device, whatever the batch. Negative (an smd_status) on failure. */
+int64_t smd_paged4_workspace_bytes(const smd_paged4_cache_t* cache);
+
+/* Attention over the cache: smd_paged_decode's definition, arguments, bounds and
+ * errors, with the values that the codes of this cache stand for. Code times block
+ * scale is exact in f16; the weights enter the second product as f16, at 2^7 for the
+ * running maximum that they are taken from (and up to 2^15), 11 bits while within
+ * 2^-21 of the largest, a bit less for each power of two below; the heads' powers are applied in fp32.
+ * A row that sees a block whose scale is NaN gets NaN (of K: all of the row; of V:
+ * the block's columns); scales of tokens that a row does not see never reach it. */
+int smd_paged4_decode(const uint16_t* q, int64_t q_stride, const smd_paged4_cache_t* cache,
+                      const int32_t* table, int64_t table_stride, int32_t width,
+                      const int32_t* lengths, int32_t R, int32_t row_group, int32_t Hq,
+                      float sm_scale, const int32_t* block_lists, const int32_t* block_counts,
+                      int32_t K, uint16_t* out, float* lse, int32_t* status, void* workspace,
+                      int64_t workspace_bytes, smd_stream_t stream);
+
+/* As smd_paged4_decode, with the testing hooks of smd_paged_decode_ex. */
+int smd_paged4_decode_ex(const uint16_t* q, int64_t q_stride, const smd_paged4_cache_t* cache,
+                         const int32_t* table, int64_t table_stride, int32_t width,
+                         const int32_t* lengths, int32_t R, int32_t row_group, int32_t Hq,
+                         float sm_scale, const int32_t* block_lists, const int32_t* block_counts,
+                         int32_t K, uint16_t* out, float* lse, int32_t* status, void* workspace,
+                         int64_t workspace_bytes, smd_stream_t stream, const smd_plan_t* force);
+
+/* The norm of each query and key head, and the position rotation, in one pass. For
+ * token t and a head's columns x (queries with q_weight, keys with k_weight):
+ *   y = x * w / sqrt(mean(x^2) + eps)     (w NULL: y = x)
+ *   angle_j = sum over axes a of positions[a][t] * freqs[a][j],   j < rot / 2
+ *   (y_u, y_v) -> (y_u cos - y_v sin, y_u sin + y_v cos) with u = j, v = j + rot / 2,
+ *            or u = 2 j, v = 2 j + 1 where `interleaved`; columns from rot on stay y
+ * rounded to bfloat16 once. Sums and products are fp32; an axis' angle is taken modulo a turn
+ * in 64-bit fixed point, right to 2^-20 of a turn for every position and frequency (to 2^-30 for
+ * frequencies up to 1).
+ *   q, k     [T, Hq, head_dim], [T, Hk, head_dim] bfloat16; token t starts at
+ *            q + t * q_stride (elements; a multiple of 8), heads are head_dim apart.
+ *            16-byte aligned. Hk = 0: no keys (k and k_out NULL).
+ *   positions   [axes, T] int32, axis a at positions + a * positions_stride. A token
+ *            whose position on axis 0 is negative is left out: its rows of the outputs
+ *            stay as they are.
+ *   freqs    [axes, rot / 2] float32, radians a position, |f| <= 1024 (what is beyond
+ *            that, or not finite, turns by nothing). An axis that a pair does not
+ *            turn with has 0 there.
+ *   q_weight, k_weight   [head_dim] bfloat16, 16-byte aligned, each may be NULL.
+ *   eps      >= 0, finite.
+ *   q_out, k_out   as q and k; may be q and k themselves, and must not overlap
+ *            them otherwise.
+ * Bounds (SMD_ERR_SHAPE): 0 <= T < 2^30, head_dim 64, 128 or 256, rot a multiple of 16 up to
+ * head_dim (0: no rotation; positions and freqs may then be NULL), axes 1 to 4,
+ * 1 <= Hq, 0 <= Hk, Hq + Hk <= 65535, strides at least a row, positions_stride >= T.
+ * Returns SMD_OK, SMD_ERR_NULL, SMD_ERR_SHAPE, SMD_ERR_ALIGN, SMD_ERR_DEVICE,
+ * SMD_ERR_LAUNCH. */
+int smd_qk_norm_rope(const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride,
+                     int32_t T, int32_t Hq, int32_t Hk, int32_t head_dim, const int32_t* positions,
+                     int64_t positions_stride, int32_t axes, const float* freqs, int32_t rot,
+                     int32_t interleaved, const uint16_t* q_weight, const uint16_t* k_weight,
+                     float eps, uint16_t* q_out, int64_t q_out_stride, uint16_t* k_out,
+                     int64_t k_out_stride, smd_stream_t stream);
+
+/* Which drafted tokens stay, and the token after them, from given random numbers
+ * (speculative sampling: the tokens are distributed as the target's own). Request r has G
+ * rows of target probabilities p_0 .. p_(G-1) (row i after its i-th drafted token) and up to G - 1
+ * drafted tokens d_i, which were drawn from q_i. With u_i = accept[r][i], from i = 0 on:
+ *   d_i stays while u_i * q_i(d_i) < p_i(d_i)   (exactly, of the fp32 values; NaN: it does not)
+ * A drafted token outside [0, V) ends a request's drafts. With a the number that stay:
+ *   w(v) = floor(2^40 * min(max(p_a(v) - q_a(v), 0), 1))   if d_a was refused
+ *   w(v) = floor(2^40 * min(max(p_a(v), 0), 1))   if the drafts ended, or all of the former are 0
+ *   (the difference in fp32; NaN: 0), and the token is the first v at which w(0) + .. + w(v)
+ *   exceeds floor(U * sum w / 2^31), U = floor(2^31 * sample[r]) within [0, 2^31 - 1]
+ *   (NaN: 0). If all w are 0 it is -1.
+ * Whole numbers: no order of adding changes the result. A probability below 2^-40 counts
+ * as none.
+ *   target   [R, G, V] float32, row (r, i) at target + (r * G + i) * target_stride.
+ *   draft    [R, G - 1, V] float32, strides alike, or NULL: d_i was the only choice
+ *            (q_i(d_i) = 1), as drafts from a lookup are.
+ *   tokens   [R, G - 1] int32;  accept [R, G - 1] float32;  sample [R] float32, from
+ *            [0, 1).  (tokens and accept may be NULL where G = 1.)
+ *   out_tokens  [R, G] int32: the a tokens that stay, the drawn one, then -1.
+ *   accepted    [R] int32: a.   rejected  [R] int32: G - 1 - a, what smd_block_trim takes
+ *            off the request's cache. Either may be NULL.
+ * Bounds (SMD_ERR_SHAPE): R >= 0, 1 <= G <= 64, 1 <= V <= 2^22, strides >= V, R * G < 2^31.
+ * Pointers are 4-byte aligned; rows of 16-byte steps are read faster.
+ * Returns SMD_OK, SMD_ERR_NULL, SMD_ERR_SHAPE, SMD_ERR_ALIGN, SMD_ERR_DEVICE,
+ * SMD_ERR_LAUNCH. */
+int smd_verify_drafts(const float* target, int64_t target_stride, const float* draft,
+                      int64_t draft_stride, const int32_t* tokens, const float* accept,
+                      const float* sample, int32_t R, int32_t G, int32_t V, int32_t* out_tokens,
+                      int32_t* accepted, int32_t* rejected, smd_stream_t stream);
+
+/* Takes tokens off the end of requests. Request r keeps new = max(length - drop, 0)
+ * tokens (a negative drop: 0); entries ceil(new / P) .. ceil(length / P) - 1 of its table row
+ * go back to the ring, after state[1], by ascending request, then by their order in the
+ * table. The entries themselves stay as they are.
+ *   lengths, table, ring, state, page_size   as smd_block_tables'; lengths are clamped to
+ *               [0, width * P].
+ *   drop        [R] int32.
+ *   new_lengths [R] int32, new_state [2] int64: must not overlap the inputs, as there.
+ * Bounds as smd_block_tables'. Returns SMD_OK, SMD_ERR_NULL, SMD_ERR_SHAPE,
+ * SMD_ERR_ALIGN, SMD_ERR_DEVICE, SMD_ERR_LAUNCH. */
+int smd_block_trim(const int32_t* lengths, const int32_t* drop, int32_t R, const int32_t* table,
+                   int64_t table_stride, int32_t width, int32_t* ring, int32_t pages,
+                   const int64_t* state, int32_t page_size, int32_t* new_lengths,
+                   int64_t* new_state, smd_stream_t stream);
+
 /* Static text for a status code. */
 const char* smd_status_str(int status);
 

@@ -70,6 +70,17 @@ class SmdPagedCache(ctypes.Structure):
                 ("map", ctypes.c_uint64 * 36)]
 
 
+class SmdPagedCache4(ctypes.Structure):
+    """smd_paged4_cache_t."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("k_exp", ctypes.c_void_p),
+                ("v_exp", ctypes.c_void_p), ("bounds", ctypes.c_void_p),
+                ("k_stride", ctypes.c_int64 * 3), ("v_stride", ctypes.c_int64 * 3),
+                ("pages", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("map", ctypes.c_uint64 * 68)]
+
+
 class SmdError(RuntimeError):
     def __init__(self, status: int, what: str = ""):
         self.status = int(status)
@@ -212,6 +223,31 @@ def lib() -> ctypes.CDLL:
             so.smd_paged_decode.restype = ctypes.c_int
             so.smd_paged_decode_ex.argtypes = so.smd_paged_decode.argtypes + [ctypes.POINTER(SmdPlan)]
             so.smd_paged_decode_ex.restype = ctypes.c_int
+            cache4 = ctypes.POINTER(SmdPagedCache4)
+            so.smd_paged4_cache_init.argtypes = [cache4]
+            so.smd_paged4_cache_init.restype = ctypes.c_int
+            so.smd_paged4_append.argtypes = [cache4, ptr, i64, ptr, i64, ptr, i32, ptr]
+            so.smd_paged4_append.restype = ctypes.c_int
+            so.smd_paged4_read.argtypes = [cache4, ptr, i32, ptr, i64, ptr, i64, ptr]
+            so.smd_paged4_read.restype = ctypes.c_int
+            so.smd_paged4_workspace_bytes.argtypes = [cache4]
+            so.smd_paged4_workspace_bytes.restype = i64
+            so.smd_paged4_decode.argtypes = [cache4 if a is cache else a
+                                             for a in so.smd_paged_decode.argtypes]
+            so.smd_paged4_decode.restype = ctypes.c_int
+            so.smd_paged4_decode_ex.argtypes = so.smd_paged4_decode.argtypes + [
+                ctypes.POINTER(SmdPlan)]
+            so.smd_paged4_decode_ex.restype = ctypes.c_int
+            so.smd_qk_norm_rope.argtypes = [ptr, i64, ptr, i64, i32, i32, i32, i32, ptr, i64, i32, ptr,
+                                            i32, i32, ptr, ptr, ctypes.c_float, ptr, i64, ptr, i64,
+                                            ptr]
+            so.smd_qk_norm_rope.restype = ctypes.c_int
+            so.smd_verify_drafts.argtypes = [ptr, i64, ptr, i64, ptr, ptr, ptr, i32, i32, i32, ptr,
+                                             ptr, ptr, ptr]
+            so.smd_verify_drafts.restype = ctypes.c_int
+            so.smd_block_trim.argtypes = [ptr, ptr, i32, ptr, i64, i32, ptr, i32, ptr, i32, ptr, ptr,
+                                          ptr]
+            so.smd_block_trim.restype = ctypes.c_int
             so.smd_status_str.argtypes = [ctypes.c_int]
             so.smd_version.restype = ctypes.c_int
             so.smd_version.argtypes = []
@@ -1088,7 +1124,7 @@ def _paged_rows(q, cache, table, lengths, row_group):
             row_group, Hq)
 
 
-def block_scores(q, cache: PagedCache, table, lengths, row_group: int = 1, keep_first: int = 0,
+def block_scores(q, cache: PagedCache | PagedCache4, table, lengths, row_group: int = 1, keep_first: int = 0,
                  keep_last: int = 0, out=None, stream=None):
     """The score of each page for each row and kv head (smd_block_scores): an
     upper bound of q . k over the page's keys, the largest over the kv head's
@@ -1097,6 +1133,10 @@ def block_scores(q, cache: PagedCache, table, lengths, row_group: int = 1, keep_
     the pages a row sees; ``scores.flatten(0, 1)`` goes to topk_select."""
     import torch
 
+    if isinstance(cache, PagedCache4):
+        if cache.of_bounds is None:
+            raise ValueError("the cache has no bounds")
+        cache = cache.of_bounds
     args, dev = _paged_rows(q, cache, table, lengths, row_group), cache.device
     B, heads, width = q.shape[0], cache.heads, table.shape[1]
     if out is None:  # rows of a multiple of 8 scores: topk_select reads them in 16-byte pieces
@@ -1137,6 +1177,13 @@ def paged_decode(q, cache: PagedCache, table, lengths, sm_scale: float, row_grou
     CUDA tensor: without one, a wait that runs out shows in NaN rows only. ``plan`` sets the
     testing hooks (smd_paged_decode_ex). Returns (out [R * row_group, Hq, head_dim] bfloat16,
     lse [R * row_group, Hq] float32)."""
+    return _decode_call("smd_paged_decode", paged_workspace_bytes, q, cache, table, lengths, sm_scale,
+                        row_group, block_lists, block_counts, out, lse, status, workspace, stream, plan)
+
+
+def _decode_call(name, workspace_bytes, q, cache, table, lengths, sm_scale, row_group, block_lists,
+                 block_counts, out, lse, status, workspace, stream, plan):
+    """The decode ``name`` of a paged cache, whatever its bits."""
     import torch
 
     args, dev = _paged_rows(q, cache, table, lengths, row_group), cache.device
@@ -1162,7 +1209,7 @@ def paged_decode(q, cache: PagedCache, table, lengths, sm_scale: float, row_grou
     else:
         _vector(lse, "lse", torch.float32, dev, B * Hq)
     if workspace is None:
-        workspace = _new(torch.zeros, stream, paged_workspace_bytes(cache), torch.uint8, q.device)
+        workspace = _new(torch.zeros, stream, workspace_bytes(cache), torch.uint8, q.device)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
     if status is not None:
@@ -1172,9 +1219,279 @@ def paged_decode(q, cache: PagedCache, table, lengths, sm_scale: float, row_grou
              _ptr(status), workspace.data_ptr(),
              workspace.numel() * workspace.element_size(), _stream(stream, dev))
     if plan is None:
-        rc = _entry("smd_paged_decode", dev)(*args)
+        rc = _entry(name, dev)(*args)
     else:
-        rc = _entry("smd_paged_decode_ex", dev)(*args, ctypes.byref(_as_plan(plan)))
+        rc = _entry(name + "_ex", dev)(*args, ctypes.byref(_as_plan(plan)))
     if rc != SMD_OK:
-        raise SmdError(rc, "smd_paged_decode")
+        raise SmdError(rc, name)
     return out, lse
+
+
+# ---- the paged cache in 4 bits, and the step around it -------------------------------------
+
+class PagedCache4:
+    """A paged key/value cache in E2M1 with an E4M3 scale for each token, head and
+    block of 16 columns (smd_paged4_cache_t), over the caller's tensors, which it keeps
+    alive.
+
+    k, v: [pages, heads, page_size, head_dim / 2] uint8 (two codes a byte, the even
+    column in the low bits), any strides in 16-byte steps with contiguous bytes (a
+    token-major pool is passed as ``pool.transpose(1, 2)``); k_scales, v_scales: [pages,
+    heads, page_size, head_dim / 16] E4M3 (uint8 or float8_e4m3fn), contiguous; k_exp,
+    v_exp: [heads] int32 exponents of the heads' powers of two, or None (zeros); bounds:
+    [pages, heads, 2, head_dim] bfloat16 or None. All on one GPU. block_scores takes
+    such a cache too, if it has bounds."""
+
+    def __init__(self, k, v, k_scales, v_scales, k_exp=None, v_exp=None, bounds=None):
+        import torch
+
+        c = SmdPagedCache4()
+        shape = None
+        for name, t in (("k", k), ("v", v)):
+            if t.dtype != torch.uint8 or t.dim() != 4 or t.stride(3) != 1:
+                raise ValueError(f"{name} must be uint8 [pages, heads, page_size, head_dim / 2] with "
+                                 "contiguous bytes")
+            if shape is not None and tuple(t.shape) != shape:
+                raise ValueError("k and v must have one shape")
+            shape = tuple(t.shape)
+            setattr(c, name, _ptr(t))
+            setattr(c, name + "_stride", (ctypes.c_int64 * 3)(*t.stride()[:3]))
+        pages, heads, page_size, D = *shape[:3], 2 * shape[3]
+        codes8 = (torch.uint8, torch.float8_e4m3fn)
+        for name, t, want, dtypes in (
+                ("k_scales", k_scales, (pages, heads, page_size, D // 16), codes8),
+                ("v_scales", v_scales, (pages, heads, page_size, D // 16), codes8),
+                ("k_exp", k_exp, (heads,), (torch.int32,)),
+                ("v_exp", v_exp, (heads,), (torch.int32,)),
+                ("bounds", bounds, (pages, heads, 2, D), (torch.bfloat16,))):
+            if t is None and name[1:] != "_scales":
+                continue
+            if t is None or tuple(t.shape) != want or t.dtype not in dtypes or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous {dtypes[0]} tensor of shape {want}")
+            setattr(c, name, _ptr(t))
+        self.device = _gpu(k, "the cache")
+        for name, t in (("v", v), ("k_scales", k_scales), ("v_scales", v_scales), ("k_exp", k_exp),
+                        ("v_exp", v_exp), ("bounds", bounds)):
+            if t is not None and t.get_device() != self.device:
+                raise ValueError(f"{name} must be on cuda:{self.device}")
+        c.pages, c.heads, c.page_size, c.head_dim = pages, heads, page_size, D
+        rc = lib().smd_paged4_cache_init(ctypes.byref(c))
+        if rc != SMD_OK:
+            raise SmdError(rc, "smd_paged4_cache_init")
+        self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
+        self.k_exp, self.v_exp, self.bounds = k_exp, v_exp, bounds
+        self.pages, self.heads, self.page_size, self.head_dim = pages, heads, page_size, D
+        self.c, self.ref = c, ctypes.byref(c)
+        # What block_scores reads: the bounds.
+        self.of_bounds = PagedCache(bounds=bounds, page_size=page_size) if bounds is not None else None
+
+    @classmethod
+    def empty(cls, pages: int, heads: int, page_size: int, head_dim: int, bounds: bool = True,
+              k_exp=None, v_exp=None, device="cuda"):
+        """A cache of newly allocated tensors (zeros: nothing written yet)."""
+        import torch
+
+        def zeros(*shape, dtype=torch.uint8):
+            return torch.zeros(shape, dtype=dtype, device=device)
+
+        codes, scales = (pages, heads, page_size, head_dim // 2), (pages, heads, page_size, head_dim // 16)
+        b = zeros(pages, heads, 2, head_dim, dtype=torch.bfloat16) if bounds else None
+        return cls(zeros(*codes), zeros(*codes), zeros(*scales), zeros(*scales), k_exp, v_exp, b)
+
+
+def _token_rows(t, name: str, T: int, heads: int, D: int, dev: int):
+    """Pointer and token stride of bfloat16 [T, heads, D] whose tokens may lie apart."""
+    import torch
+
+    if t.get_device() != dev or t.dtype != torch.bfloat16 or t.shape != (T, heads, D):
+        raise ValueError(f"{name} must be a bfloat16 tensor [{T}, {heads}, {D}] on cuda:{dev}")
+    steps = t.stride()
+    if steps[2] != 1 or (heads > 1 and steps[1] != D):
+        raise ValueError(f"{name}: a token's heads must be contiguous")
+    return t.data_ptr(), steps[0] if T > 1 else heads * D
+
+
+def paged4_append(cache: PagedCache4, k, v, slots, stream=None) -> None:
+    """Writes new keys and values into the cache (smd_paged4_append). k, v
+    [T, heads, head_dim] bfloat16 CUDA tensors whose tokens may lie apart
+    (slices of a fused projection); slots [T] int32."""
+    import torch
+
+    dev = cache.device
+    _vector(slots, "slots", torch.int32, dev)
+    T = slots.numel()
+    rc = _entry("smd_paged4_append", dev)(
+        cache.ref, *_token_rows(k, "k", T, cache.heads, cache.head_dim, dev),
+        *_token_rows(v, "v", T, cache.heads, cache.head_dim, dev), slots.data_ptr(), T,
+        _stream(stream, dev))
+    if rc != SMD_OK:
+        raise SmdError(rc, "smd_paged4_append")
+
+
+def paged4_read(cache: PagedCache4, slots, k=None, v=None, stream=None):
+    """The keys and values of slots [T] int32 as bfloat16 [T, heads, head_dim] each
+    (smd_paged4_read), into ``k`` and ``v`` if given (whose tokens may lie apart). Rows of
+    slots outside the pool are left as they are. Returns (k, v)."""
+    import torch
+
+    dev = cache.device
+    _vector(slots, "slots", torch.int32, dev)
+    T, heads, D = slots.numel(), cache.heads, cache.head_dim
+    if k is None:
+        k = _new(torch.zeros, stream, (T, heads, D), torch.bfloat16, slots.device)
+    if v is None:
+        v = _new(torch.zeros, stream, (T, heads, D), torch.bfloat16, slots.device)
+    rc = _entry("smd_paged4_read", dev)(cache.ref, slots.data_ptr(), T,
+                                        *_token_rows(k, "k", T, heads, D, dev),
+                                        *_token_rows(v, "v", T, heads, D, dev), _stream(stream, dev))
+    if rc != SMD_OK:
+        raise SmdError(rc, "smd_paged4_read")
+    return k, v
+
+
+def paged4_workspace_bytes(cache: PagedCache4) -> int:
+    """Bytes of workspace paged4_decode needs for this cache, whatever the batch."""
+    n = int(_entry("smd_paged4_workspace_bytes", cache.device)(cache.ref))
+    if n < 0:
+        raise SmdError(n, "smd_paged4_workspace_bytes")
+    return n
+
+
+def paged4_decode(q, cache: PagedCache4, table, lengths, sm_scale: float, row_group: int = 1,
+                  block_lists=None, block_counts=None, out=None, lse=None, status=None,
+                  workspace=None, stream=None, plan: SmdPlan | dict | None = None):
+    """Attention over the cache (smd_paged4_decode); the arguments and results are
+    paged_decode's, the workspace is of paged4_workspace_bytes(cache) bytes."""
+    return _decode_call("smd_paged4_decode", paged4_workspace_bytes, q, cache, table, lengths, sm_scale,
+                        row_group, block_lists, block_counts, out, lse, status, workspace, stream, plan)
+
+
+def qk_norm_rope(q, k, positions, freqs, q_weight=None, k_weight=None, eps: float = 1e-6,
+                 interleaved: bool = False, q_out=None, k_out=None, stream=None):
+    """The norm of each query and key head and the position rotation, in one pass
+    (smd_qk_norm_rope). q [T, Hq, head_dim] and k [T, Hk, head_dim] (or None) bfloat16 CUDA
+    tensors whose tokens may lie apart; positions [T] or [axes, T] int32; freqs [rot / 2] or
+    [axes, rot / 2] float32, radians a position, 0 where a pair does not turn with an axis; both
+    None: no rotation. q_weight, k_weight [head_dim] bfloat16 or None (no norm). q_out, k_out:
+    outputs, which may be q and k themselves; new tensors if None. Returns (q_out, k_out);
+    tokens whose position on the first axis is negative are left as they are (zeros in new
+    tensors)."""
+    import torch
+
+    dev = _gpu(q, "q")
+    if q.dim() != 3:
+        raise ValueError("q must be [T, Hq, head_dim]")
+    T, Hq, D = q.shape
+    Hk = 0 if k is None else k.shape[1]
+    args = (*_token_rows(q, "q", T, Hq, D, dev),
+            *(_token_rows(k, "k", T, Hk, D, dev) if k is not None else (0, 0)))
+    if (positions is None) != (freqs is None):
+        raise ValueError("positions and freqs go together")
+    axes, rot, pos_ptr, pos_step, f_ptr = 1, 0, 0, 0, 0
+    if positions is not None:
+        if positions.get_device() != dev or positions.dtype != torch.int32 or positions.dim() not in (1, 2) \
+                or positions.shape[-1] != T or (T > 1 and positions.stride(-1) != 1):
+            raise ValueError(f"positions must be an int32 tensor [{T}] or [axes, {T}] on cuda:{dev} with "
+                             "contiguous rows")
+        axes = positions.shape[0] if positions.dim() == 2 else 1
+        pos_ptr, pos_step = positions.data_ptr(), positions.stride(0) if axes > 1 else T
+        _vector(freqs, "freqs", torch.float32, dev)
+        if freqs.dim() != positions.dim() or (freqs.dim() == 2 and freqs.shape[0] != axes):
+            raise ValueError("freqs must be [rot / 2] or [axes, rot / 2], as positions")
+        rot, f_ptr = 2 * freqs.shape[-1], freqs.data_ptr()
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _vector(w, name, torch.bfloat16, dev)
+            if w.numel() != D:
+                raise ValueError(f"{name} must have {D} elements")
+    if q_out is None:
+        q_out = _new(torch.zeros, stream, (T, Hq, D), torch.bfloat16, q.device)
+    if k is None:
+        if k_out is not None:
+            raise ValueError("k_out without k")
+    elif k_out is None:
+        k_out = _new(torch.zeros, stream, (T, Hk, D), torch.bfloat16, q.device)
+    out = (*_token_rows(q_out, "q_out", T, Hq, D, dev),
+           *(_token_rows(k_out, "k_out", T, Hk, D, dev) if k is not None else (0, 0)))
+    rc = _entry("smd_qk_norm_rope", dev)(*args, T, Hq, Hk, D, pos_ptr, pos_step, axes, f_ptr, rot,
+                                         int(bool(interleaved)), _ptr(q_weight), _ptr(k_weight), eps,
+                                         *out, _stream(stream, dev))
+    if rc != SMD_OK:
+        raise SmdError(rc, "smd_qk_norm_rope")
+    return q_out, k_out
+
+
+def _probability_rows(t, name: str, rows: tuple, dev: int):
+    """Pointer and row stride of float32 [R, n, V] whose rows are evenly spaced."""
+    import torch
+
+    if t.get_device() != dev or t.dtype != torch.float32 or t.dim() != 3 or tuple(t.shape[:2]) != rows:
+        raise ValueError(f"{name} must be a float32 tensor [{rows[0]}, {rows[1]}, V] on cuda:{dev}")
+    (R, n, V), steps = t.shape, t.stride()
+    if V > 1 and steps[2] != 1 or (R > 1 and n > 1 and steps[0] != n * steps[1]):
+        raise ValueError(f"{name}: rows must be contiguous and evenly spaced")
+    return t.data_ptr(), steps[1] if n > 1 else steps[0] if R > 1 else V
+
+
+def verify_drafts(target, tokens, accept, sample, draft=None, out_tokens=None, accepted=None,
+                  rejected=None, stream=None):
+    """Which drafted tokens stay, and the token after them (smd_verify_drafts). target
+    [R, G, V] float32: the target's probabilities after each of 0 .. G - 1 drafted tokens; tokens
+    [R, G - 1] int32: the drafted ones (one outside the vocabulary ends a request's drafts); accept
+    [R, G - 1] and sample [R] float32: random numbers from [0, 1); draft [R, G - 1, V] float32: what the
+    drafted tokens were drawn from, or None (each was the only choice). Returns (out_tokens [R, G]: the
+    tokens that stay, the one drawn after them, then -1; accepted [R]; rejected [R], which block_trim takes
+    off), int32."""
+    import torch
+
+    dev = _gpu(target, "target")
+    if target.dim() != 3:
+        raise ValueError("target must be [R, G, V]")
+    R, G, V = target.shape
+    args = _probability_rows(target, "target", (R, G), dev)
+    _vector(sample, "sample", torch.float32, dev, R)
+    _vector(tokens, "tokens", torch.int32, dev, R * (G - 1))
+    _vector(accept, "accept", torch.float32, dev, R * (G - 1))
+    draft_args = (0, 0)
+    if draft is not None:
+        draft_args = _probability_rows(draft, "draft", (R, G - 1), dev)
+        if draft.shape[2] != V:
+            raise ValueError(f"draft must be [{R}, {G - 1}, {V}]")
+    if out_tokens is None:
+        out_tokens = _new(torch.empty, stream, (R, G), torch.int32, target.device)
+    else:
+        _vector(out_tokens, "out_tokens", torch.int32, dev, R * G)
+    accepted = _output(accepted, "accepted", torch.int32, R, target, stream)
+    rejected = _output(rejected, "rejected", torch.int32, R, target, stream)
+    rc = _entry("smd_verify_drafts", dev)(*args, *draft_args, tokens.data_ptr(), accept.data_ptr(),
+                                          sample.data_ptr(), R, G, V, out_tokens.data_ptr(),
+                                          accepted.data_ptr(), rejected.data_ptr(), _stream(stream, dev))
+    if rc != SMD_OK:
+        raise SmdError(rc, "smd_verify_drafts")
+    return out_tokens, accepted, rejected
+
+
+def block_trim(lengths, drop, table, ring, state, page_size: int, new_lengths=None, new_state=None,
+               stream=None):
+    """Takes drop [R] int32 tokens off the end of requests (smd_block_trim): their pages
+    past the new lengths go back to the ring. lengths, table, ring and state as in block_tables. Returns
+    (new_lengths [R], new_state [2]), which may be given and may not be the inputs."""
+    import torch
+
+    R, dev = lengths.numel(), _gpu(lengths, "lengths")
+    _vector(lengths, "lengths", torch.int32, dev)
+    _vector(drop, "drop", torch.int32, dev, R)
+    _vector(ring, "ring", torch.int32, dev)
+    _vector(state, "state", torch.int64, dev, 2)
+    width, step = _table(table, R, dev)
+    new_lengths = _output(new_lengths, "new_lengths", torch.int32, R, lengths, stream)
+    new_state = _output(new_state, "new_state", torch.int64, 2, lengths, stream)
+    if new_lengths.data_ptr() == lengths.data_ptr() and R or new_state.data_ptr() == state.data_ptr():
+        raise ValueError("new_lengths and new_state may not be lengths and state")
+    rc = _entry("smd_block_trim", dev)(
+        lengths.data_ptr(), drop.data_ptr(), R, table.data_ptr(), step, width, ring.data_ptr(),
+        ring.numel(), state.data_ptr(), page_size, new_lengths.data_ptr(), new_state.data_ptr(),
+        _stream(stream, dev))
+    if rc != SMD_OK:
+        raise SmdError(rc, "smd_block_trim")
+    return new_lengths, new_state

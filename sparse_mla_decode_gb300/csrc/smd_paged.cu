@@ -1,5 +1,5 @@
-// The description of a paged cache (smd_paged_cache_init) and the checks that
-// the calls on it share. Host code only.
+// The descriptions of paged caches (smd_paged_cache_init, smd_paged4_cache_init) and the
+// checks that the calls on them share. Host code only.
 #include <cstring>
 
 #include "smd_internal.h"
@@ -9,11 +9,19 @@ namespace smd {
 
 namespace {
 
-bool strides_ok(const int64_t (&s)[3], int head_dim) {
+bool strides_ok(const int64_t (&s)[3], int row_bytes) {
     for (int i = 0; i < 3; ++i)
         if (s[i] <= 0 || s[i] >= (1ll << 40)) return false;
-    return s[2] >= head_dim;
+    return s[2] >= row_bytes;
 }
+
+bool shape_ok(int pages, int heads, int page_size, int head_dim) {
+    return pages >= 1 && heads >= 1 && heads <= 65535 && page_size >= 16 && page_size <= 256 &&
+           page_size % 16 == 0 && (head_dim == 64 || head_dim == 128 || head_dim == 256) &&
+           static_cast<int64_t>(pages) * page_size < (1ll << 31);
+}
+
+bool steps_of_16(const int64_t (&s)[3]) { return s[0] % 16 == 0 && s[1] % 16 == 0 && s[2] % 16 == 0; }
 
 // cuTensorMapEncodeTiled, looked up through the runtime (the library does not
 // link the driver library, so it loads on machines without one).
@@ -37,6 +45,52 @@ EncodeTiledFn encode_fn() {
     return fn;
 }
 
+// The tensor map of codes over (byte of a token, token, head, page), with a box of up to 128
+// bytes by page_box_tokens() tokens, swizzled over its row. False if encoding failed.
+bool encode_codes(CUtensorMap* out, const void* ptr, const int64_t (&stride)[3], int row_bytes,
+                  const CacheShape& c) {
+    EncodeTiledFn encode = encode_fn();
+    if (encode == nullptr) return false;
+    const cuuint64_t dims[4] = {
+        static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(c.page_size),
+        static_cast<cuuint64_t>(c.heads), static_cast<cuuint64_t>(c.pages)};
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(stride[2]),
+                                   static_cast<cuuint64_t>(stride[1]),
+                                   static_cast<cuuint64_t>(stride[0])};
+    const cuuint32_t box[4] = {static_cast<cuuint32_t>(row_bytes < 128 ? row_bytes : 128),
+                               static_cast<cuuint32_t>(page_box_tokens(c.page_size, c.head_dim)), 1, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    // L2 fetches no more than a row where rows of 64 bytes lie apart (E4M3, 310 requests of up to
+    // 5001 tokens, 12 query rows, token-major pages of 16: 185 us against 273 at 128 bytes, whose
+    // other half is another head's; 31 requests 32.9 against 34.1).
+    const bool apart = row_bytes < 128 && stride[2] != row_bytes;
+    const CUtensorMapL2promotion fetch = !apart            ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                                         : row_bytes == 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_64B
+                                                           : CU_TENSOR_MAP_L2_PROMOTION_NONE;
+    return encode(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(ptr), dims, strides, box,
+                  estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  row_bytes == 32   ? CU_TENSOR_MAP_SWIZZLE_32B
+                  : row_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                    : CU_TENSOR_MAP_SWIZZLE_128B,
+                  fetch, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The tensor map of block scales [pages, heads, tokens * head_dim / 16], with a box of
+// page_box_tokens() tokens' scales (at most 256 bytes): a page outside the pool reads as zeros.
+bool encode_scales(CUtensorMap* out, const void* ptr, const CacheShape& c) {
+    EncodeTiledFn encode = encode_fn();
+    if (encode == nullptr) return false;
+    const cuuint64_t row = static_cast<cuuint64_t>(c.page_size) * c.head_dim / 16;
+    const cuuint64_t dims[3] = {row, static_cast<cuuint64_t>(c.heads), static_cast<cuuint64_t>(c.pages)};
+    const cuuint64_t strides[2] = {row, row * c.heads};
+    const cuuint32_t box[3] = {
+        static_cast<cuuint32_t>(page_box_tokens(c.page_size, c.head_dim) * c.head_dim / 16), 1, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return encode(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(ptr), dims, strides, box,
+                  estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace
 
 int device_sms() {
@@ -49,41 +103,15 @@ int device_sms() {
     return sms;
 }
 
-bool encode_page_map(CUtensorMap* out, const void* ptr, const int64_t (&stride)[3],
-                     const smd_paged_cache_t& c) {
-    EncodeTiledFn encode = encode_fn();
-    if (encode == nullptr) return false;
-    const cuuint64_t dims[4] = {
-        static_cast<cuuint64_t>(c.head_dim), static_cast<cuuint64_t>(c.page_size),
-        static_cast<cuuint64_t>(c.heads), static_cast<cuuint64_t>(c.pages)};
-    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(stride[2]),
-                                   static_cast<cuuint64_t>(stride[1]),
-                                   static_cast<cuuint64_t>(stride[0])};
-    const cuuint32_t box[4] = {static_cast<cuuint32_t>(c.head_dim < 128 ? c.head_dim : 128),
-                               static_cast<cuuint32_t>(page_box_tokens(c)), 1, 1};
-    const cuuint32_t estr[4] = {1, 1, 1, 1};
-    // L2 fetches no more than a row where rows of 64 bytes lie apart (310 requests of up to
-    // 5001 tokens, 12 query rows, token-major pages of 16: 185 us against 273 at 128 bytes, whose
-    // other half is another head's; 31 requests 32.9 against 34.1).
-    const CUtensorMapL2promotion fetch = c.head_dim < 128 && stride[2] != c.head_dim
-                                             ? CU_TENSOR_MAP_L2_PROMOTION_L2_64B
-                                             : CU_TENSOR_MAP_L2_PROMOTION_L2_128B;
-    return encode(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(ptr), dims, strides, box,
-                  estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  c.head_dim < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, fetch,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-int check_paged_rows(const uint16_t* q, int64_t q_stride, const smd_paged_cache_t* cache,
+int check_paged_rows(const uint16_t* q, int64_t q_stride, const CacheShape& cache,
                      const int32_t* table, int64_t table_stride, int32_t width,
                      const int32_t* lengths, int32_t R, int32_t row_group, int32_t Hq, bool* skip) {
     *skip = false;
-    if (cache == nullptr) return SMD_ERR_NULL;
-    if (!paged_ready(cache)) return SMD_ERR_PLAN;
-    const int64_t row = static_cast<int64_t>(Hq) * cache->head_dim;
-    if (R < 0 || row_group < 1 || row_group > kPagedMaxGroup || Hq < 1 || Hq % cache->heads != 0 ||
-        Hq / cache->heads > kPagedMaxHeads || Hq > 65535 || width < 1 || table_stride < width ||
-        static_cast<int64_t>(width) * cache->page_size >= (1ll << 31) ||
+    if (!cache.ready) return SMD_ERR_PLAN;
+    const int64_t row = static_cast<int64_t>(Hq) * cache.head_dim;
+    if (R < 0 || row_group < 1 || row_group > kPagedMaxGroup || Hq < 1 || Hq % cache.heads != 0 ||
+        Hq / cache.heads > kPagedMaxHeads || Hq > 65535 || width < 1 || table_stride < width ||
+        static_cast<int64_t>(width) * cache.page_size >= (1ll << 31) ||
         static_cast<int64_t>(R) * row_group * Hq >= (1ll << 31) || q_stride < row ||
         q_stride % 8 != 0)
         return SMD_ERR_SHAPE;
@@ -106,25 +134,46 @@ extern "C" int smd_paged_cache_init(smd_paged_cache_t* c) {
     if (kv != (c->v != nullptr) || (!kv && c->bounds == nullptr) ||
         (kv && (c->k_scale == nullptr || c->v_scale == nullptr)))
         return SMD_ERR_NULL;
-    if (c->pages < 1 || c->heads < 1 || c->heads > 65535 || c->page_size < 16 ||
-        c->page_size > 256 || c->page_size % 16 != 0 ||
-        (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) ||
-        static_cast<int64_t>(c->pages) * c->page_size >= (1ll << 31))
+    if (!shape_ok(c->pages, c->heads, c->page_size, c->head_dim))
         return SMD_ERR_SHAPE;
     if (!aligned(c->bounds, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))
         return SMD_ERR_ALIGN;
     if (kv) {
         if (!strides_ok(c->k_stride, c->head_dim) || !strides_ok(c->v_stride, c->head_dim))
             return SMD_ERR_SHAPE;
-        for (int i = 0; i < 3; ++i)
-            if (c->k_stride[i] % 16 != 0 || c->v_stride[i] % 16 != 0) return SMD_ERR_ALIGN;
+        if (!steps_of_16(c->k_stride) || !steps_of_16(c->v_stride)) return SMD_ERR_ALIGN;
         if (!aligned(c->k, 16) || !aligned(c->v, 16)) return SMD_ERR_ALIGN;
         CUtensorMap maps[2];
-        if (!encode_page_map(&maps[0], c->k, c->k_stride, *c) ||
-            !encode_page_map(&maps[1], c->v, c->v_stride, *c))
+        const CacheShape shape = shape_of(c);
+        if (!encode_codes(&maps[0], c->k, c->k_stride, c->head_dim, shape) ||
+            !encode_codes(&maps[1], c->v, c->v_stride, c->head_dim, shape))
             return SMD_ERR_DEVICE;
         std::memcpy(&c->map[1], maps, sizeof maps);
     }
     c->map[0] = kPagedMark;
+    return SMD_OK;
+}
+
+extern "C" int smd_paged4_cache_init(smd_paged4_cache_t* c) {
+    using namespace smd;
+    if (c == nullptr) return SMD_ERR_NULL;
+    std::memset(c->map, 0, sizeof c->map);
+    if (c->k == nullptr || c->v == nullptr || c->k_scales == nullptr || c->v_scales == nullptr)
+        return SMD_ERR_NULL;
+    if (!shape_ok(c->pages, c->heads, c->page_size, c->head_dim) ||
+        !strides_ok(c->k_stride, c->head_dim / 2) || !strides_ok(c->v_stride, c->head_dim / 2))
+        return SMD_ERR_SHAPE;
+    if (!steps_of_16(c->k_stride) || !steps_of_16(c->v_stride) || !aligned(c->k, 16) ||
+        !aligned(c->v, 16) || !aligned(c->k_scales, 16) || !aligned(c->v_scales, 16) ||
+        !aligned(c->k_exp, 4) || !aligned(c->v_exp, 4) || !aligned(c->bounds, 16))
+        return SMD_ERR_ALIGN;
+    CUtensorMap maps[4];
+    const CacheShape shape = shape_of(c);
+    if (!encode_codes(&maps[0], c->k, c->k_stride, c->head_dim / 2, shape) ||
+        !encode_codes(&maps[1], c->v, c->v_stride, c->head_dim / 2, shape) ||
+        !encode_scales(&maps[2], c->k_scales, shape) || !encode_scales(&maps[3], c->v_scales, shape))
+        return SMD_ERR_DEVICE;
+    std::memcpy(&c->map[1], maps, sizeof maps);
+    c->map[0] = kPaged4Mark;
     return SMD_OK;
 }

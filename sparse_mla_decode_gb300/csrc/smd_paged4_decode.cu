@@ -1,0 +1,67 @@
+// Attention over a paged E2M1 cache (smd_paged4_decode); the kernel is in
+// smd_paged_decode.cuh.
+#include <cstring>
+
+#include "smd_paged_decode.cuh"
+
+extern "C" int64_t smd_paged4_workspace_bytes(const smd_paged4_cache_t* cache) {
+    if (cache == nullptr) return SMD_ERR_NULL;
+    if (!smd::paged_ready(cache)) return SMD_ERR_PLAN;
+    const int sms = smd::device_sms();
+    if (sms <= 0) return SMD_ERR_DEVICE;
+    return smd::workspace_bytes(sms, cache->head_dim);
+}
+
+extern "C" int smd_paged4_decode(const uint16_t* q, int64_t q_stride, const smd_paged4_cache_t* cache,
+                                 const int32_t* table, int64_t table_stride, int32_t width,
+                                 const int32_t* lengths, int32_t R, int32_t row_group, int32_t Hq,
+                                 float sm_scale, const int32_t* block_lists,
+                                 const int32_t* block_counts, int32_t K, uint16_t* out, float* lse,
+                                 int32_t* status, void* workspace, int64_t workspace_bytes,
+                                 smd_stream_t stream) {
+    return smd_paged4_decode_ex(q, q_stride, cache, table, table_stride, width, lengths, R, row_group, Hq,
+                                sm_scale, block_lists, block_counts, K, out, lse, status, workspace,
+                                workspace_bytes, stream, nullptr);
+}
+
+extern "C" int smd_paged4_decode_ex(const uint16_t* q, int64_t q_stride,
+                                    const smd_paged4_cache_t* cache, const int32_t* table,
+                                    int64_t table_stride, int32_t width, const int32_t* lengths,
+                                    int32_t R, int32_t row_group, int32_t Hq, float sm_scale,
+                                    const int32_t* block_lists, const int32_t* block_counts,
+                                    int32_t K, uint16_t* out, float* lse, int32_t* status,
+                                    void* workspace, int64_t workspace_bytes, smd_stream_t stream,
+                                    const smd_plan_t* force) {
+    using namespace smd;
+    if (cache == nullptr) return SMD_ERR_NULL;
+    PagedParams p{};
+    p.k_exp = cache->k_exp;
+    p.v_exp = cache->v_exp;
+    Maps<4> maps;
+    std::memcpy(&maps, &cache->map[1], sizeof maps);
+    const int D = cache->head_dim;
+    const DecodeCall call{q, q_stride, table, table_stride, width, lengths, R, row_group, Hq, sm_scale,
+                          block_lists, block_counts, K, out, lse, status, workspace, workspace_bytes,
+                          stream, force};
+    return run_decode(call, shape_of(cache), p, [&](const PagedParams& p, int64_t tiles, int RT, int sms) {
+        const bool halves = page_box_tokens(cache->page_size, D) < (D == 256 ? 16 : 32);  // a tile spans two pages
+        const auto launch = [&](auto shape) {
+            return launch_decode<decltype(shape)>(p, maps, sms, tiles, stream);
+        };
+        if (D == 64)
+            return halves    ? (RT == 1   ? launch(Shape<64, 1, 32, 2, 3, 3, 4>{})
+                              : RT == 2 ? launch(Shape<64, 2, 32, 2, 3, 3, 4>{})
+                                        : launch(Shape<64, 4, 32, 2, 4, 2, 4>{}))
+                 : RT == 1 ? launch(Shape<64, 1, 32, 1, 3, 3, 4>{})
+                 : RT == 2 ? launch(Shape<64, 2, 32, 1, 3, 3, 4>{})
+                           : launch(Shape<64, 4, 32, 1, 4, 2, 4>{});
+        if (D == 128)
+            return halves    ? (RT == 1   ? launch(Shape<128, 1, 32, 2, 3, 3, 4>{})
+                              : RT == 2 ? launch(Shape<128, 2, 32, 2, 3, 3, 4>{})
+                                        : launch(Shape<128, 4, 32, 2, 3, 2, 4>{}))
+                 : RT == 1 ? launch(Shape<128, 1, 32, 1, 3, 3, 4>{})
+                 : RT == 2 ? launch(Shape<128, 2, 32, 1, 3, 3, 4>{})
+                           : launch(Shape<128, 4, 32, 1, 3, 2, 4>{});
+        return RT == 1 ? launch(Shape<256, 1, 16, 1, 3, 3, 4>{}) : launch(Shape<256, 2, 16, 1, 3, 2, 4>{});
+    });
+}

@@ -26,6 +26,7 @@
 // an SM do not quite cover that), 16 thousand of one 21 us (69%).
 #include "smd_internal.h"
 #include "smd_paged.h"
+#include "smd_paged_append.cuh"
 #include "smd_ptx.cuh"
 
 namespace smd {
@@ -44,26 +45,6 @@ struct AppendParams {
     uint16_t* bounds;
     int32_t pages, heads, P;
 };
-
-__device__ __forceinline__ uint32_t bmax2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-
-__device__ __forceinline__ uint32_t bmin2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("min.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-
-// Infinities as the largest finite bf16.
-__device__ __forceinline__ uint32_t finite2(uint32_t a) {
-    return bmin2(bmax2(a, 0xff7fff7fu), 0x7f7f7f7fu);
-}
-
-__device__ __forceinline__ float lo_f(uint32_t v) { return __uint_as_float(v << 16); }
-__device__ __forceinline__ float hi_f(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
 // The least power of two at which a / 2^e is at most 448 = 1.75 * 2^8.
 __device__ __forceinline__ float power_of(float a) {
@@ -107,45 +88,16 @@ __device__ __forceinline__ bool starts_run(const AppendParams& p, int t, int slo
 
 // What a page holds before a run: its scale and, of 8 columns from `col` on, its bounds
 // (loaded ahead of the run's values, so that nothing waits for them afterwards).
-struct Before {
+struct Before : Extremes {
     float scale;
-    uint4 hi, lo;
 };
 
 template <int D>
 __device__ __forceinline__ Before before(const AppendParams& p, int64_t at, int side, int o, int col) {
     Before b;
     b.scale = o > 0 ? p.scale[side][at] : __uint_as_float(static_cast<uint32_t>(kMinExponent + 127) << 23);
-    b.hi = make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);  // -infinity
-    b.lo = make_uint4(0x7f807f80u, 0x7f807f80u, 0x7f807f80u, 0x7f807f80u);
-    if (side == 0 && o > 0 && p.bounds != nullptr) {
-        const uint4* const w = reinterpret_cast<const uint4*>(p.bounds + at * 2 * D + col);
-        b.hi = w[0];
-        b.lo = w[D / 8];
-    }
+    if (side == 0 && o > 0 && p.bounds != nullptr) b.read(p.bounds + at * 2 * D, D, col);
     return b;
-}
-
-// The largest and smallest of a run's keys, joined with the bounds before and
-// written: 8 columns from `col` on.
-__device__ __forceinline__ void write_bounds(uint16_t* bounds, int D, int col, const Before& was,
-                                             uint32_t (&hi)[4], uint32_t (&lo)[4]) {
-    uint4* const b = reinterpret_cast<uint4*>(bounds + col);
-    const uint4 h = was.hi, l = was.lo;
-    b[0] = make_uint4(finite2(bmax2(hi[0], h.x)), finite2(bmax2(hi[1], h.y)), finite2(bmax2(hi[2], h.z)),
-                      finite2(bmax2(hi[3], h.w)));
-    b[D / 8] = make_uint4(finite2(bmin2(lo[0], l.x)), finite2(bmin2(lo[1], l.y)), finite2(bmin2(lo[2], l.z)),
-                          finite2(bmin2(lo[3], l.w)));
-}
-
-// Takes 8 values into the extremes.
-__device__ __forceinline__ void take(const uint4& v, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        hi[j] = bmax2(hi[j], w[j]);
-        lo[j] = bmin2(lo[j], w[j]);
-    }
 }
 
 // The largest size: the largest of hi and -lo, or 0 where nothing but NaN was met
@@ -371,12 +323,6 @@ __device__ __forceinline__ void write_run_block(const AppendParams& p, const Run
             *reinterpret_cast<uint2*>(pool + (o + m) * ts + col) =
                 encode8<false>(*reinterpret_cast<const uint4*>(x + m * xs), now, inv);
     }
-}
-
-// The lanes of this lane's group of N.
-template <int N>
-__device__ __forceinline__ unsigned group_mask(int lane) {
-    return N == 32 ? 0xffffffffu : ((1u << (N & 31)) - 1u) << (lane / N * N);
 }
 
 constexpr int kThreads = 128;

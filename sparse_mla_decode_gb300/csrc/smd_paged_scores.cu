@@ -253,8 +253,9 @@ extern "C" int smd_block_scores(const uint16_t* q, int64_t q_stride, const smd_p
                                 int32_t keep_first, int32_t keep_last, uint16_t* scores,
                                 int64_t score_stride, smd_stream_t stream) {
     using namespace smd;
+    if (cache == nullptr) return SMD_ERR_NULL;
     bool skip;
-    int rc = check_paged_rows(q, q_stride, cache, table, table_stride, width, lengths, R, row_group,
+    int rc = check_paged_rows(q, q_stride, shape_of(cache), table, table_stride, width, lengths, R, row_group,
                               Hq, &skip);
     if (rc != SMD_OK) return rc;
     if (cache->bounds == nullptr) return SMD_ERR_NULL;
