@@ -1,7 +1,7 @@
 """Decode steps over a paged cache, put together from the library's calls.
 
     python -m sparse_mla_decode_gb300.paged_step [--requests 32] [--context 32768]
-        [--steps 8] [--pages 64]
+        [--steps 8] [--pages 64] [--bits 8] [--drafts 0]
 
 Requests of up to ``--context`` tokens hold pages of a grouped-query cache (64
 query heads over 8 key/value heads of 128 columns). A prompt is written once;
@@ -9,7 +9,11 @@ then every step gives each request a slot for its new token (block_tables),
 writes the token's keys and values (paged_append), scores the pages for the
 step's queries (block_scores), selects ``--pages`` of them for each request and
 key/value head (topk_select, the first and the last two always among them)
-and attends over those (paged_decode). Values are random. The step is
+and attends over those (paged_decode). ``--bits 4``: the cache is in E2M1 with block scales
+(paged4_append, paged4_decode), after the norm of queries and keys and the position
+rotation (qk_norm_rope). ``--drafts N``: a step writes and attends N drafted tokens more
+for each request, their verification against random distributions (verify_drafts) follows, and what
+is refused gives its pages back (block_trim). Values are random. The step is
 captured in a CUDA graph and replayed; the same step with attention over all
 tokens is timed beside it, and the selected pages' share of the attention
 weight is printed.
@@ -17,6 +21,7 @@ weight is printed.
 from __future__ import annotations
 
 import argparse
+import math
 
 
 class PagedStep:
@@ -24,11 +29,12 @@ class PagedStep:
     attention over all tokens."""
 
     def __init__(self, requests, width, pool_pages, q_heads=64, heads=8, head_dim=128, page_size=64,
-                 pages=None, device="cuda"):
+                 pages=None, device="cuda", bits=8):
         import torch
         from . import binding
 
-        self.cache = binding.PagedCache.empty(pool_pages, heads, page_size, head_dim, device=device)
+        kind = {8: binding.PagedCache, 4: binding.PagedCache4}[bits]
+        self.cache, self.bits = kind.empty(pool_pages, heads, page_size, head_dim, device=device), bits
         self.pages, self.sm_scale = pages, head_dim ** -0.5
         self.table = torch.zeros((requests, width), dtype=torch.int32, device=device)
         self.ring = torch.arange(pool_pages, dtype=torch.int32, device=device)
@@ -37,8 +43,8 @@ class PagedStep:
         self.lengths = [torch.zeros(requests, dtype=torch.int32, device=device) for _ in range(2)]
         self.state = [torch.tensor([0, pool_pages], dtype=torch.int64, device=device) for _ in range(2)]
         self.status = torch.zeros(1, dtype=torch.int32, device=device)
-        self.workspace = torch.zeros(binding.paged_workspace_bytes(self.cache), dtype=torch.uint8,
-                                     device=device)
+        room = binding.paged_workspace_bytes if bits == 8 else binding.paged4_workspace_bytes
+        self.workspace = torch.zeros(room(self.cache), dtype=torch.uint8, device=device)
         self.now = 0
 
     def grant(self, new_tokens, max_tokens):
@@ -57,7 +63,7 @@ class PagedStep:
         """Keys and values [T, heads, head_dim] bf16 of granted tokens."""
         from . import binding
 
-        binding.paged_append(self.cache, k, v, slots)
+        (binding.paged_append if self.bits == 8 else binding.paged4_append)(self.cache, k, v, slots)
 
     def attend(self, q, row_group=1):
         """Attention of the queries [R * row_group, q_heads, head_dim] bf16. Returns
@@ -74,9 +80,22 @@ class PagedStep:
             flat = scores.as_strided((B * heads, width), (scores.stride(1), 1))
             idx, cnt = binding.topk_select(flat, self.pages)
             lists, counts = idx.view(B, heads, self.pages), cnt
-        return binding.paged_decode(q, self.cache, self.table, lengths, self.sm_scale,
-                                    row_group=row_group, block_lists=lists, block_counts=counts,
-                                    status=self.status, workspace=self.workspace)
+        decode = binding.paged_decode if self.bits == 8 else binding.paged4_decode
+        return decode(q, self.cache, self.table, lengths, self.sm_scale, row_group=row_group,
+                      block_lists=lists, block_counts=counts, status=self.status,
+                      workspace=self.workspace)
+
+    def keep(self, target, tokens, accept, sample, draft=None):
+        """Verification of the last G - 1 tokens that each request was granted (verify_drafts' arguments);
+        those that are refused come off, and their pages go back. Returns (out_tokens, accepted)."""
+        from . import binding
+
+        a, b = self.now, 1 - self.now
+        out, accepted, rejected = binding.verify_drafts(target, tokens, accept, sample, draft=draft)
+        binding.block_trim(self.lengths[a], rejected, self.table, self.ring, self.state[a],
+                           self.cache.page_size, new_lengths=self.lengths[b], new_state=self.state[b])
+        self.now = b
+        return out, accepted
 
 
 def main(argv=None) -> int:
@@ -85,7 +104,11 @@ def main(argv=None) -> int:
     ap.add_argument("--context", type=int, default=32768)
     ap.add_argument("--steps", type=int, default=8)
     ap.add_argument("--pages", type=int, default=64)
+    ap.add_argument("--bits", type=int, default=8, choices=(8, 4))
+    ap.add_argument("--drafts", type=int, default=0)
     args = ap.parse_args(argv)
+    if not 0 <= args.drafts <= 7:
+        ap.error("--drafts must be 0 to 7")
     for name in ("requests", "context", "steps", "pages"):
         if getattr(args, name) < 1:
             ap.error(f"--{name} must be at least 1")
@@ -94,12 +117,14 @@ def main(argv=None) -> int:
     replays = (args.steps + 1) // 2  # of two steps each
 
     import torch
+    from . import binding
 
     R, P, heads, q_heads, D = args.requests, 64, 8, 64, 128
     g = torch.Generator(device="cuda").manual_seed(0)
     lengths = torch.randint(max(1, args.context // 4), args.context + 1, (R,), generator=g, device="cuda")
-    width = -(-(args.context + 4 * args.steps + 8) // P)
-    s = PagedStep(R, width, R * width, q_heads, heads, D, P, pages=args.pages)
+    G = 1 + args.drafts
+    width = -(-(args.context + G * (4 * args.steps + 8)) // P)
+    s = PagedStep(R, width, R * width, q_heads, heads, D, P, pages=args.pages, bits=args.bits)
 
     def random(n, h):
         return torch.randn(n, h, D, generator=g, device="cuda").bfloat16()
@@ -114,13 +139,27 @@ def main(argv=None) -> int:
         left -= share
     assert int(s.status) == 0, "a request was refused"
 
-    one = torch.ones(R, dtype=torch.int32, device="cuda")
-    q, k, v = random(R, q_heads), random(R, heads), random(R, heads)
+    new = torch.full((R,), G, dtype=torch.int32, device="cuda")
+    q, k, v = random(R * G, q_heads), random(R * G, heads), random(R * G, heads)
+    freqs = torch.exp(torch.arange(D // 2, device="cuda") * (-2 / D * math.log(10000.0)))
+    weight = torch.ones(D, dtype=torch.bfloat16, device="cuda")
+    if G > 1:
+        V = 32768
+        target = torch.softmax(2 * torch.randn(R, G, V, generator=g, device="cuda"), -1)
+        tokens = target[:, 1:].argmax(-1).int()
+        accept = 0.1 * torch.rand(R, G - 1, generator=g, device="cuda")
+        sample = torch.rand(R, generator=g, device="cuda")
 
     def step():
-        _, slots, _ = s.grant(one, R)
-        s.write(k, v, slots)
-        return s.attend(q)
+        _, slots, positions = s.grant(new, R * G)
+        qt, kt = q, k
+        if args.bits == 4:
+            qt, kt = binding.qk_norm_rope(q, k, positions, freqs, weight, weight)
+        s.write(kt, v, slots)
+        out = s.attend(qt, row_group=G)
+        if G > 1:
+            s.keep(target, tokens, accept, sample)
+        return out
 
     times = {}
     for name, pages in (("selected", args.pages), ("all", None)):
@@ -141,13 +180,14 @@ def main(argv=None) -> int:
         times[name] = start.elapsed_time(end) * 1e3 / (2 * replays)
         assert int(s.status) == 0, "device status"
         if pages is not None:
-            _, lse = s.attend(q)
+            _, lse = s.attend(q, row_group=G)
             s.pages = None
-            _, lse_all = s.attend(q)
+            _, lse_all = s.attend(q, row_group=G)
             kept = torch.exp(lse - lse_all).mean()
         del result
     n = int(s.lengths[s.now].sum())
-    print(f"{R} requests, {n} tokens ({n * heads * D * 2 / 1e9:.2f} GB of keys and values)")
+    print(f"{R} requests, {n} tokens ({n * heads * D * (2 if args.bits == 8 else 1.125) / 1e9:.2f} GB of keys and "
+          "values)")
     print(f"step over {args.pages} pages of each request and head: {times['selected']:.1f} us "
           f"({100 * float(kept):.1f}% of the attention weight of random values)")
     print(f"step over all tokens: {times['all']:.1f} us")
