@@ -46,8 +46,8 @@ EncodeTiledFn encode_fn() {
 }
 
 // The tensor map of codes over (byte of a token, token, head, page), with a box of up to 128
-// bytes by page_box_tokens() tokens, swizzled over its row. False if encoding failed.
-bool encode_codes(CUtensorMap* out, const void* ptr, const int64_t (&stride)[3], int row_bytes,
+// bytes by `tokens`, swizzled over its row. False if encoding failed.
+bool encode_codes(CUtensorMap* out, const void* ptr, const int64_t (&stride)[3], int row_bytes, int tokens,
                   const CacheShape& c) {
     EncodeTiledFn encode = encode_fn();
     if (encode == nullptr) return false;
@@ -58,7 +58,7 @@ bool encode_codes(CUtensorMap* out, const void* ptr, const int64_t (&stride)[3],
                                    static_cast<cuuint64_t>(stride[1]),
                                    static_cast<cuuint64_t>(stride[0])};
     const cuuint32_t box[4] = {static_cast<cuuint32_t>(row_bytes < 128 ? row_bytes : 128),
-                               static_cast<cuuint32_t>(page_box_tokens(c.page_size, c.head_dim)), 1, 1};
+                               static_cast<cuuint32_t>(tokens), 1, 1};
     const cuuint32_t estr[4] = {1, 1, 1, 1};
     // L2 fetches no more than a row where rows of 64 bytes lie apart (E4M3, 310 requests of up to
     // 5001 tokens, 12 query rows, token-major pages of 16: 185 us against 273 at 128 bytes, whose
@@ -75,20 +75,22 @@ bool encode_codes(CUtensorMap* out, const void* ptr, const int64_t (&stride)[3],
                   fetch, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The tensor map of block scales [pages, heads, tokens * head_dim / 16], with a box of
-// page_box_tokens() tokens' scales (at most 256 bytes): a page outside the pool reads as zeros.
-bool encode_scales(CUtensorMap* out, const void* ptr, const CacheShape& c) {
+// The tensor map of block scales [pages, heads, tokens * head_dim / 16] in elements of `element`
+// bytes (1 or 8), with a box of `tokens` tokens' scales (at most 256 elements): a page outside the
+// pool reads as zeros.
+bool encode_scales(CUtensorMap* out, const void* ptr, int element, int tokens, const CacheShape& c) {
     EncodeTiledFn encode = encode_fn();
     if (encode == nullptr) return false;
-    const cuuint64_t row = static_cast<cuuint64_t>(c.page_size) * c.head_dim / 16;
-    const cuuint64_t dims[3] = {row, static_cast<cuuint64_t>(c.heads), static_cast<cuuint64_t>(c.pages)};
+    const int token = c.head_dim / 16;  // bytes
+    const cuuint64_t row = static_cast<cuuint64_t>(c.page_size) * token;
+    const cuuint64_t dims[3] = {row / element, static_cast<cuuint64_t>(c.heads), static_cast<cuuint64_t>(c.pages)};
     const cuuint64_t strides[2] = {row, row * c.heads};
-    const cuuint32_t box[3] = {
-        static_cast<cuuint32_t>(page_box_tokens(c.page_size, c.head_dim) * c.head_dim / 16), 1, 1};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(tokens * token / element), 1, 1};
     const cuuint32_t estr[3] = {1, 1, 1};
-    return encode(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(ptr), dims, strides, box,
-                  estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode(out, element == 8 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT64 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3,
+                  const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
@@ -145,8 +147,9 @@ extern "C" int smd_paged_cache_init(smd_paged_cache_t* c) {
         if (!aligned(c->k, 16) || !aligned(c->v, 16)) return SMD_ERR_ALIGN;
         CUtensorMap maps[2];
         const CacheShape shape = shape_of(c);
-        if (!encode_codes(&maps[0], c->k, c->k_stride, c->head_dim, shape) ||
-            !encode_codes(&maps[1], c->v, c->v_stride, c->head_dim, shape))
+        const int box = page_box_tokens(c->page_size, c->head_dim);
+        if (!encode_codes(&maps[0], c->k, c->k_stride, c->head_dim, box, shape) ||
+            !encode_codes(&maps[1], c->v, c->v_stride, c->head_dim, box, shape))
             return SMD_ERR_DEVICE;
         std::memcpy(&c->map[1], maps, sizeof maps);
     }
@@ -167,12 +170,17 @@ extern "C" int smd_paged4_cache_init(smd_paged4_cache_t* c) {
         !aligned(c->v, 16) || !aligned(c->k_scales, 16) || !aligned(c->v_scales, 16) ||
         !aligned(c->k_exp, 4) || !aligned(c->v_exp, 4) || !aligned(c->bounds, 16))
         return SMD_ERR_ALIGN;
-    CUtensorMap maps[4];
+    CUtensorMap maps[8] = {};
     const CacheShape shape = shape_of(c);
-    if (!encode_codes(&maps[0], c->k, c->k_stride, c->head_dim / 2, shape) ||
-        !encode_codes(&maps[1], c->v, c->v_stride, c->head_dim / 2, shape) ||
-        !encode_scales(&maps[2], c->k_scales, shape) || !encode_scales(&maps[3], c->v_scales, shape))
-        return SMD_ERR_DEVICE;
+    for (int i = 0; i < (c->head_dim == 128 ? 2 : 1); ++i) {
+        const int box = i == 1 ? tc_box_tokens(c->page_size) : page_box_tokens(c->page_size, c->head_dim);
+        CUtensorMap* const m = maps + 4 * i;
+        if (!encode_codes(&m[0], c->k, c->k_stride, c->head_dim / 2, box, shape) ||
+            !encode_codes(&m[1], c->v, c->v_stride, c->head_dim / 2, box, shape) ||
+            !encode_scales(&m[2], c->k_scales, i == 1 ? 8 : 1, box, shape) ||
+            !encode_scales(&m[3], c->v_scales, i == 1 ? 8 : 1, box, shape))
+            return SMD_ERR_DEVICE;
+    }
     std::memcpy(&c->map[1], maps, sizeof maps);
     c->map[0] = kPaged4Mark;
     return SMD_OK;

@@ -17,10 +17,11 @@ constexpr int kPagedMaxHeads = 128;  // query heads of a kv head
 
 // What smd_paged_cache_init leaves in smd_paged_cache_t::map: a mark, then the
 // tensor maps of k and v (absent in a cache of bounds only). smd_paged4_cache_init: a mark of its
-// own, then the maps of k, v and their block scales.
+// own, then the maps of k, v and their block scales for the mma.sync kernel, then, at 128 columns,
+// for the tcgen05 kernel.
 constexpr uint64_t kPagedMark = 0x736d645061676564ull, kPaged4Mark = 0x736d645061673465ull;
 static_assert(sizeof(CUtensorMap) == 128, "two maps and the mark fit smd_paged_cache_t::map");
-static_assert(sizeof(smd_paged4_cache_t::map) >= 4 * sizeof(CUtensorMap) + 8, "four maps and the mark");
+static_assert(sizeof(smd_paged4_cache_t::map) >= 8 * sizeof(CUtensorMap) + 8, "eight maps and the mark");
 
 inline bool paged_ready(const smd_paged_cache_t* c) { return c->map[0] == kPagedMark; }
 inline bool paged_ready(const smd_paged4_cache_t* c) { return c->map[0] == kPaged4Mark; }
@@ -48,6 +49,11 @@ __device__ __forceinline__ int pages_of(int tokens, int P) {
 // 256 columns, where the decode's tile holds 16 tokens).
 inline int page_box_tokens(int page_size, int head_dim) {
     return page_size % 32 == 0 && head_dim < 256 ? 32 : 16;
+}
+
+// The same where a tile holds 128 tokens: the largest of 128, 64, 32 and 16 that divides a page.
+inline int tc_box_tokens(int page_size) {
+    return page_size % 128 == 0 ? 128 : page_size % 64 == 0 ? 64 : page_size % 32 == 0 ? 32 : 16;
 }
 
 // Rows of queries as smd_block_scores and the decodes take them, checked;

@@ -2,6 +2,7 @@
 // smd_paged_decode.cuh.
 #include <cstring>
 
+#include "smd_paged4_tc.h"
 #include "smd_paged_decode.cuh"
 
 extern "C" int64_t smd_paged4_workspace_bytes(const smd_paged4_cache_t* cache) {
@@ -44,6 +45,16 @@ extern "C" int smd_paged4_decode_ex(const uint16_t* q, int64_t q_stride,
                           block_lists, block_counts, K, out, lse, status, workspace, workspace_bytes,
                           stream, force};
     return run_decode(call, shape_of(cache), p, [&](const PagedParams& p, int64_t tiles, int RT, int sms) {
+        // 128 columns: tcgen05 for more than 8 query rows, unless small pages make many copies of a
+        // tile's 128 tokens. 64 requests of 1024 .. 8192 tokens, tcgen05 / mma.sync in us, pages of 16, 32,
+        // 64, 128 tokens: 8 rows 100 / 84 (64); 16 rows 178 / 119, 123 / 111, 99 / 111, 92 / 111; 32 rows
+        // 198 / 179, 145 / 168, 126 / 167, 126 / 167.
+        const int box = tc_box_tokens(cache->page_size);
+        if (D == 128 && RT > 1 && box >= (RT == 2 ? 64 : 32)) {
+            Maps<4> tc;
+            std::memcpy(&tc, &cache->map[1 + sizeof maps / 8], sizeof tc);
+            return paged4_tc(p, tc, box, RT == 2 ? 16 : 32, sms, (tiles + 3) / 4, stream);
+        }
         const bool halves = page_box_tokens(cache->page_size, D) < (D == 256 ? 16 : 32);  // a tile spans two pages
         const auto launch = [&](auto shape) {
             return launch_decode<decltype(shape)>(p, maps, sms, tiles, stream);
@@ -57,11 +68,10 @@ extern "C" int smd_paged4_decode_ex(const uint16_t* q, int64_t q_stride,
                            : launch(Shape<64, 4, 32, 1, 4, 2, 4>{});
         if (D == 128)
             return halves    ? (RT == 1   ? launch(Shape<128, 1, 32, 2, 3, 3, 4>{})
-                              : RT == 2 ? launch(Shape<128, 2, 32, 2, 3, 3, 4>{})
-                                        : launch(Shape<128, 4, 32, 2, 3, 2, 4>{}))
-                 : RT == 1 ? launch(Shape<128, 1, 32, 1, 3, 3, 4>{})
-                 : RT == 2 ? launch(Shape<128, 2, 32, 1, 3, 3, 4>{})
-                           : launch(Shape<128, 4, 32, 1, 3, 2, 4>{});
+                                : RT == 2 ? launch(Shape<128, 2, 32, 2, 3, 3, 4>{})
+                                          : launch(Shape<128, 4, 32, 2, 3, 2, 4>{}))
+                   : RT == 1 ? launch(Shape<128, 1, 32, 1, 3, 3, 4>{})
+                             : launch(Shape<128, 2, 32, 1, 3, 3, 4>{});
         return RT == 1 ? launch(Shape<256, 1, 16, 1, 3, 3, 4>{}) : launch(Shape<256, 2, 16, 1, 3, 2, 4>{});
     });
 }

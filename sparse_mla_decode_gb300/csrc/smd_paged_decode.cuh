@@ -58,20 +58,6 @@
 #include "smd_ptx.cuh"
 
 namespace smd {
-namespace {
-
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kMaxEntries = 1024;  // requests (or (row, kv head) lists) of one launch
-constexpr float kPShift = 7.0f;    // weights are 2^7 at the maximum kept
-constexpr float kSlack = 8.0f;     // which is moved when a logit exceeds it by 2^8
-constexpr float kNone = -3.402823466e38f;  // no logit met
-// What a unit's begin and end cost a warp, in tiles. 0 / 1 / 3 / 6: 31 requests up to 5001
-// tokens of 64 columns 44 / 39 / 34 / 33 us, 1000 up to 300 tokens of 128 columns 93 / 81 /
-// 78 / 78, 64 up to 8192 tokens 111 / 110 / 109 / 109; twice as much at 64 columns: no gain.
-constexpr int kUnitCost = 3;
-constexpr int kMinTiles = 2;       // least range of a warp, in tiles (1 to 8: the same times)
-constexpr int kFan = 32;           // neighbouring CTAs of a first join (8 to 64: the same times)
 
 struct PagedParams {
     const uint16_t* q;
@@ -108,6 +94,31 @@ struct PagedParams {
     float2* head_ml;    // the same without columns: maximum, sum
     float2* part_ml;
 };
+
+// The copies' descriptors: codes, and the block scales of 4-bit ones.
+template <int BITS>
+struct Maps {
+    CUtensorMap k, v;
+};
+template <>
+struct Maps<4> {
+    CUtensorMap k, v, k_scales, v_scales;
+};
+
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kMaxEntries = 1024;  // requests (or (row, kv head) lists) of one launch
+constexpr float kPShift = 7.0f;    // weights are 2^7 at the maximum kept
+constexpr float kSlack = 8.0f;     // which is moved when a logit exceeds it by 2^8
+constexpr float kNone = -3.402823466e38f;  // no logit met
+// What a unit's begin and end cost a warp, in tiles. 0 / 1 / 3 / 6: 31 requests up to 5001
+// tokens of 64 columns 44 / 39 / 34 / 33 us, 1000 up to 300 tokens of 128 columns 93 / 81 /
+// 78 / 78, 64 up to 8192 tokens 111 / 110 / 109 / 109; twice as much at 64 columns: no gain.
+constexpr int kUnitCost = 3;
+constexpr int kMinTiles = 2;       // least range of a warp, in tiles (1 to 8: the same times)
+constexpr int kFan = 32;           // neighbouring CTAs of a first join (8 to 64: the same times)
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                         uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -271,16 +282,6 @@ __device__ __forceinline__ uint32_t piece(int row, int c) {
     return (c >> 3) * (KT * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
 }
 
-// The copies' descriptors: codes, and the block scales of 4-bit ones.
-template <int BITS>
-struct Maps {
-    CUtensorMap k, v;
-};
-template <>
-struct Maps<4> {
-    CUtensorMap k, v, k_scales, v_scales;
-};
-
 // Eight E2M1 codes -> four f16 pairs (low nibbles first), exactly.
 __device__ __forceinline__ void e2m1_to_f16(uint32_t v, uint32_t (&f)[4]) {
     asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
@@ -306,13 +307,18 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
     return r;
 }
 
-// Codes of two tokens (the halves of v: four columns each) with the tokens side by side:
-// byte n holds column n of both.
-__device__ __forceinline__ uint32_t pair_tokens(uint32_t v) {
-    const uint32_t x = __byte_perm(v, 0, 0x3120);
-    const uint32_t even = (x & 0x000f000fu) | ((x >> 4) & 0x00f000f0u);
-    const uint32_t odd = (x & 0xf000f000u) | ((x << 4) & 0x0f000f00u);
-    return even | odd;
+// Four columns of two tokens (the codes in the halves of v) -> f16 pairs of the tokens, exactly. The
+// tokens' nibbles are put side by side in bytes 2 and 3 by multiplications: the logic pipe
+// (which converts, too) is what bounds the conversions, the multipliers have room.
+__device__ __forceinline__ void pairs_to_f16(uint32_t v, uint32_t (&f)[4]) {
+    const uint32_t e = (v * 16u) & 0xf0f0f0f0u, o = v & 0xf0f0f0f0u;  // columns 0 and 2; 1 and 3
+    asm("{\n\t.reg .b8 u, w, a, b, c, d;\n\t.reg .b32 x, y;\n\t"
+        "mul.lo.u32 x, %4, 4097;\n\tmul.lo.u32 y, %5, 4097;\n\t"
+        "mov.b32 {u, w, a, b}, x;\n\tmov.b32 {u, w, c, d}, y;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, c;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(f[0]), "=r"(f[1]), "=r"(f[2]), "=r"(f[3])
+        : "r"(e), "r"(o));
 }
 
 // N bytes (4, 8 or 16) of shared memory as words.
@@ -412,6 +418,229 @@ struct Left {
     Unit ended_unit, open_unit;
 };
 
+// What is left when a CTA's workers are through: the units that cuts between workers, and
+// between CTAs, divide. base: the workers' memory, worker_bytes each, with the partials of open units.
+// kMore: the CTA has more threads than the THREADS that join.
+template <int D, int ROWS, int THREADS, int WORKERS, bool kMore = false>
+__device__ __forceinline__ void join_units(const PagedParams& p, uint32_t base, uint32_t worker_bytes,
+                                           const Left* s_left, const float2* s_ml) {
+    const int tid = threadIdx.x;
+    // The CTA's warps: the units that cuts between them divide. Open partials of
+    // neighbours and the end that follows them are one unit.
+    __threadfence_block();
+    __syncthreads();
+    const int cta = static_cast<int>(blockIdx.x);
+    // The units that this CTA goes on with (0) and begins (1) and does not hold whole.
+    bool goes[2] = {false, false};
+    Unit unit[2];
+#pragma unroll 1
+    for (int i = 0; i < 2 * WORKERS;) {  // warp i / 2: what it ended, then what it leaves open
+        const int first = i >> 1;
+        const bool is_open = (i & 1) != 0;
+        ++i;
+        if ((is_open ? s_left[first].open : s_left[first].ended) < 0) continue;
+        const bool begins = is_open && s_left[first].open_begins != 0;
+        const Unit u = is_open ? s_left[first].open_unit : s_left[first].ended_unit;
+        int opens = is_open ? 1 : 0, end_at = is_open ? -1 : first;
+        while (end_at < 0 && i < 2 * WORKERS) {
+            if (s_left[i >> 1].ended >= 0) {
+                end_at = i >> 1;
+                ++i;
+            } else {
+                ++opens;
+                i += 2;
+            }
+        }
+        const bool whole = begins && end_at >= 0;
+        if (!whole) {
+            if (begins) unit[1] = u, goes[1] = true;
+            else unit[0] = u, goes[0] = true;
+        }
+        const int64_t slot = static_cast<int64_t>(4 * cta + (begins ? 2 : 0)) * ROWS;
+#pragma unroll 1
+        for (int idx = kMore && tid >= THREADS ? u.m_real * D : tid; idx < u.m_real * (D / 4); idx += THREADS) {
+            const int row = idx / (D / 4), col = idx % (D / 4);
+            // The open warps' partials in order, then the end.
+            float4 end_v[1] = {make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
+            float2 end_ml[1] = {make_float2(-INFINITY, 0.0f)};
+            if (end_at >= 0) {
+                const int64_t at = (static_cast<int64_t>(cta) * WORKERS + end_at) * ROWS + row;
+                end_v[0] = __ldcg(reinterpret_cast<const float4*>(p.head + at * D) + col);
+                end_ml[0] = __ldcg(p.head_ml + at);
+            }
+            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            float top = -INFINITY, sum = 0.0f;
+#pragma unroll 1
+            for (int j = 0; j < opens; ++j) {
+                const float4 v[1] = {lds_f4(base + (first + j) * worker_bytes + row * D * 4 +
+                                            ((col ^ (((row >> 1) & 3) << 1)) << 4))};
+                const float2 ml[1] = {s_ml[(first + j) * ROWS + row]};
+                add_partials<1>(acc, top, sum, v, ml);
+            }
+            if (end_at >= 0) add_partials<1>(acc, top, sum, end_v, end_ml);
+            if (whole) {
+                write_row(p, u, D, row, 4 * col, acc, top, sum);
+            } else {
+                reinterpret_cast<float4*>(p.part + (slot + row) * D)[col] = acc;
+                if (col == 0) p.part_ml[slot + row] = make_float2(top, sum);
+            }
+        }
+    }
+    if (!goes[0] && !goes[1]) return;
+
+    // The units that cuts between CTAs divide, level 0: among kFan neighbours from the unit's
+    // first CTA on, level 1: among these groups. The CTA that arrives last at a join
+    // makes it.
+    __shared__ int s_joins[2];
+    const int ctas = static_cast<int>(gridDim.x);
+    const auto span = [&](int q, int level, int& from, int& n) {  // the first CTA of a join, its partials
+        const int c0 = unit[q].first_cta, c1 = unit[q].last_cta;
+        from = level == 0 ? c0 + (cta - c0) / kFan * kFan : c0;
+        n = level == 0 ? min(c1, from + kFan - 1) - from + 1 : (c1 - c0) / kFan + 1;
+    };
+#pragma unroll 1
+    for (int level = 0; level < 2; ++level) {
+        __threadfence();
+        __syncthreads();
+        if ((tid & 31) == 0 && tid < 64) {
+            const int q = tid >> 5;
+            bool joins = goes[q];
+            if (joins) {
+                int from, n;
+                span(q, level, from, n);
+                if (n > 1) {
+                    int* const count = p.arrived + level * 2 * ctas +
+                                       2 * from + (unit[q].first_cta == from ? 1 : 0);
+                    joins = atomicAdd(count, 1) == n - 1;
+                    if (joins) *count = 0;  // for the next call
+                }
+            }
+            s_joins[q] = joins;
+        }
+        __syncthreads();
+        goes[0] = s_joins[0] != 0;
+        goes[1] = s_joins[1] != 0;
+        if (!goes[0] && !goes[1]) return;
+        __threadfence();
+        // Two joins are made by half of the threads each.
+        const bool both = goes[0] && goes[1];
+        const int threads = both ? THREADS / 2 : THREADS, me = tid % threads;
+        const int q = both ? min(tid / (THREADS / 2), 1) : goes[1] ? 1 : 0;
+        const Unit u = q == 0 ? unit[0] : unit[1];
+        int from, n;
+        span(q, level, from, n);
+        const bool done[2] = {
+            level == 1 || unit[0].last_cta - unit[0].first_cta < kFan,
+            level == 1 || unit[1].last_cta - unit[1].first_cta < kFan};
+        const auto slot = [&](int c, int stage) {
+            return static_cast<int64_t>(4 * c + (c == u.first_cta ? 2 : 0) + stage) * ROWS;
+        };
+#pragma unroll 1
+        for (int i0 = kMore && tid >= THREADS ? u.m_real * D : me; i0 < u.m_real * (D / 4); i0 += 2 * threads) {
+            // Two pieces of 4 columns, kMany partials of each: one round trip.
+            constexpr int kMany = 4;
+            int row[2], col[2];
+            float4 acc[2];
+            float top[2], sum[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                row[i] = min((i0 + i * threads) / (D / 4), u.m_real - 1);
+                col[i] = (i0 + i * threads) % (D / 4);
+                acc[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                top[i] = -INFINITY;
+                sum[i] = 0.0f;
+            }
+#pragma unroll 1
+            for (int j0 = 0; j0 < n; j0 += kMany) {
+                float4 v[2][kMany];
+                float2 ml[2][kMany];
+#pragma unroll
+                for (int z = 0; z < kMany; ++z) {
+                    const int c = from + (j0 + z) * (level == 0 ? 1 : kFan);
+                    const int64_t at = slot(c, level);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        v[i][z] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        ml[i][z] = make_float2(-INFINITY, 0.0f);
+                        if (j0 + z < n) {
+                            v[i][z] = __ldcg(reinterpret_cast<const float4*>(p.part + (at + row[i]) * D) + col[i]);
+                            ml[i][z] = __ldcg(p.part_ml + at + row[i]);
+                        }
+                    }
+                }
+                add_partials<kMany>(acc[0], top[0], sum[0], v[0], ml[0]);
+                add_partials<kMany>(acc[1], top[1], sum[1], v[1], ml[1]);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (i0 + i * threads >= u.m_real * (D / 4)) break;
+                if (q == 0 ? done[0] : done[1]) {
+                    write_row(p, u, D, row[i], 4 * col[i], acc[i], top[i], sum[i]);
+                } else {
+                    const int64_t to = slot(from, 1) + row[i];
+                    reinterpret_cast<float4*>(p.part + to * D)[col[i]] = acc[i];
+                    if (col[i] == 0) p.part_ml[to] = make_float2(top[i], sum[i]);
+                }
+            }
+        }
+        goes[0] = goes[0] && !done[0];
+        goes[1] = goes[1] && !done[1];
+        if (!goes[0] && !goes[1]) return;
+    }
+}
+
+// Prefix sums of the entries' tiles of KT tokens: at least one for each unit, so that one without
+// tokens still writes its zeros. prefix [entries + 1], lens [entries], scan [warps]; the total.
+template <int KT, int THREADS>
+__device__ __forceinline__ int scan_entries(const PagedParams& p, int32_t* prefix, int32_t* lens, int32_t* scan) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const bool lists = p.lists != nullptr;
+    const auto tiles_of = [&](int e) {
+        if (e >= p.entries) return 0;
+        const int b = lists ? e / p.heads : e, r = lists ? b / p.G : e;  // row, or request
+        int len = max(min(p.lengths[r], p.width * p.page_size), 0), n = len;
+        if (lists) {
+            // The tokens that the list's row sees: a listed page past them is not read, so its
+            // scales reach nothing either.
+            len = max(len - p.G + 1 + b - r * p.G, 0);
+            n = max(min(p.counts != nullptr ? p.counts[e] : p.K, p.K), 0) * p.page_size;
+        }
+        lens[e] = len;
+        return max(n / KT + (n % KT != 0 ? 1 : 0), 1) * p.x_units;
+    };
+    constexpr int kPer = kMaxEntries / THREADS;
+    const int each = (p.entries + THREADS - 1) / THREADS;  // entries of a thread
+    int v[kPer], sum = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        v[j] = j < each ? tiles_of(tid * each + j) : 0;
+        sum += v[j];
+    }
+    int inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += u;
+    }
+    if (lane == 31) scan[warp] = inc;
+    __syncthreads();
+    int before = inc - sum;
+    int total = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+        if (w < warp) before += scan[w];
+        total += scan[w];
+    }
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        if (j < each && tid * each + j < p.entries) prefix[tid * each + j] = before;
+        before += v[j];
+    }
+    if (tid == 0) prefix[p.entries] = total;
+    __syncthreads();
+    return total;
+}
+
 template <typename S>
 __global__ void __launch_bounds__(kThreads, S::CTAS)
     paged_decode_kernel(const PagedParams p, const __grid_constant__ Maps<S::bits> maps) {
@@ -454,55 +683,7 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
     pdl_entry();
     fence_proxy_async_global();  // the cache may have been written by the kernel before
 
-    // Prefix sums of the entries' tiles: at least one for each unit, so that one without
-    // tokens still writes its zeros.
-    int total;
-    {
-        const auto tiles_of = [&](int e) {
-            if (e >= p.entries) return 0;
-            const int b = lists ? e / p.heads : e, r = lists ? b / p.G : e;  // row, or request
-            int len = max(min(p.lengths[r], p.width * p.page_size), 0), n = len;
-            if (lists) {
-                // The tokens that the list's row sees: a listed page past them is not read, so its
-                // scales reach nothing either.
-                len = max(len - p.G + 1 + b - r * p.G, 0);
-                n = max(min(p.counts != nullptr ? p.counts[e] : p.K, p.K), 0) * p.page_size;
-            }
-            lens[e] = len;
-            return max(n / KT + (n % KT != 0 ? 1 : 0), 1) * p.x_units;
-        };
-        constexpr int kPer = kMaxEntries / kThreads;
-        const int each = (p.entries + kThreads - 1) / kThreads;  // entries of a thread
-        int v[kPer], sum = 0;
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-            v[j] = j < each ? tiles_of(tid * each + j) : 0;
-            sum += v[j];
-        }
-        int inc = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += u;
-        }
-        int32_t* const scan = reinterpret_cast<int32_t*>(gbase + S::off_scan);
-        if (lane == 31) scan[warp] = inc;
-        __syncthreads();
-        int before = inc - sum;
-        total = 0;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            if (w < warp) before += scan[w];
-            total += scan[w];
-        }
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-            if (j < each && tid * each + j < p.entries) prefix[tid * each + j] = before;
-            before += v[j];
-        }
-        if (tid == 0) prefix[p.entries] = total;
-    }
-    __syncthreads();
+    const int total = scan_entries<KT, kThreads>(p, prefix, lens, reinterpret_cast<int32_t*>(gbase + S::off_scan));
 
     // The grid is cut evenly by cost: each unit counts kUnitCost besides its tiles, laid
     // before them, so unit u of the batch starts its tiles kUnitCost (u + 1) further on.
@@ -1038,7 +1219,7 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
                             for (int y = 0; y < 2; ++y) {
                                 const uint32_t by = scale_pair(vsc[y][pc >> 1], vsc[y][S::scale_row / 4 + (pc >> 1)],
                                                                sel + (pc & 1) * 0x22u);
-                                e2m1_to_f16(pair_tokens(vr[2 * z + y]), f[y]);
+                                pairs_to_f16(vr[2 * z + y], f[y]);
 #pragma unroll
                                 for (int j = 0; j < 4; ++j) f[y][j] = mul_f16x2(f[y][j], by);
                             }
@@ -1154,171 +1335,20 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
             mbar_wait(bars + 8 * (j % ST), (j / ST) & 1, done, p.status, p.budget_ns, true);
         }
 
-    // The CTA's warps: the units that cuts between them divide. Open partials of
-    // neighbours and the end that follows them are one unit.
-    __threadfence_block();
-    __syncthreads();
-    const int cta = static_cast<int>(blockIdx.x);
-    // The units that this CTA goes on with (0) and begins (1) and does not hold whole.
-    bool goes[2] = {false, false};
-    Unit unit[2];
-#pragma unroll 1
-    for (int i = 0; i < 2 * kWarps;) {  // warp i / 2: what it ended, then what it leaves open
-        const int first = i >> 1;
-        const bool is_open = (i & 1) != 0;
-        ++i;
-        if ((is_open ? s_left[first].open : s_left[first].ended) < 0) continue;
-        const bool begins = is_open && s_left[first].open_begins != 0;
-        const Unit u = is_open ? s_left[first].open_unit : s_left[first].ended_unit;
-        int opens = is_open ? 1 : 0, end_at = is_open ? -1 : first;
-        while (end_at < 0 && i < 2 * kWarps) {
-            if (s_left[i >> 1].ended >= 0) {
-                end_at = i >> 1;
-                ++i;
-            } else {
-                ++opens;
-                i += 2;
-            }
-        }
-        const bool whole = begins && end_at >= 0;
-        if (!whole) {
-            if (begins) unit[1] = u, goes[1] = true;
-            else unit[0] = u, goes[0] = true;
-        }
-        const int64_t slot = static_cast<int64_t>(4 * cta + (begins ? 2 : 0)) * S::rows;
-#pragma unroll 1
-        for (int idx = tid; idx < u.m_real * (D / 4); idx += kThreads) {
-            const int row = idx / (D / 4), col = idx % (D / 4);
-            // The open warps' partials in order, then the end.
-            float4 end_v[1] = {make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
-            float2 end_ml[1] = {make_float2(-INFINITY, 0.0f)};
-            if (end_at >= 0) {
-                const int64_t at = (static_cast<int64_t>(cta) * kWarps + end_at) * S::rows + row;
-                end_v[0] = __ldcg(reinterpret_cast<const float4*>(p.head + at * D) + col);
-                end_ml[0] = __ldcg(p.head_ml + at);
-            }
-            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            float top = -INFINITY, sum = 0.0f;
-#pragma unroll 1
-            for (int j = 0; j < opens; ++j) {
-                const float4 v[1] = {lds_f4(base + (first + j) * S::warp_bytes + row * D * 4 +
-                                            ((col ^ (((row >> 1) & 3) << 1)) << 4))};
-                const float2 ml[1] = {s_ml[(first + j) * S::rows + row]};
-                add_partials<1>(acc, top, sum, v, ml);
-            }
-            if (end_at >= 0) add_partials<1>(acc, top, sum, end_v, end_ml);
-            if (whole) {
-                write_row(p, u, D, row, 4 * col, acc, top, sum);
-            } else {
-                reinterpret_cast<float4*>(p.part + (slot + row) * D)[col] = acc;
-                if (col == 0) p.part_ml[slot + row] = make_float2(top, sum);
-            }
-        }
-    }
-    if (!goes[0] && !goes[1]) return;
-
-    // The units that cuts between CTAs divide, level 0: among kFan neighbours from the unit's
-    // first CTA on, level 1: among these groups. The CTA that arrives last at a join
-    // makes it.
-    __shared__ int s_joins[2];
-    const int ctas = static_cast<int>(gridDim.x);
-    const auto span = [&](int q, int level, int& from, int& n) {  // the first CTA of a join, its partials
-        const int c0 = unit[q].first_cta, c1 = unit[q].last_cta;
-        from = level == 0 ? c0 + (cta - c0) / kFan * kFan : c0;
-        n = level == 0 ? min(c1, from + kFan - 1) - from + 1 : (c1 - c0) / kFan + 1;
-    };
-#pragma unroll 1
-    for (int level = 0; level < 2; ++level) {
-        __threadfence();
-        __syncthreads();
-        if ((tid & 31) == 0 && tid < 64) {
-            const int q = tid >> 5;
-            bool joins = goes[q];
-            if (joins) {
-                int from, n;
-                span(q, level, from, n);
-                if (n > 1) {
-                    int* const count = p.arrived + level * 2 * ctas +
-                                       2 * from + (unit[q].first_cta == from ? 1 : 0);
-                    joins = atomicAdd(count, 1) == n - 1;
-                    if (joins) *count = 0;  // for the next call
-                }
-            }
-            s_joins[q] = joins;
-        }
-        __syncthreads();
-        goes[0] = s_joins[0] != 0;
-        goes[1] = s_joins[1] != 0;
-        if (!goes[0] && !goes[1]) return;
-        __threadfence();
-        // Two joins are made by half of the threads each.
-        const bool both = goes[0] && goes[1];
-        const int threads = both ? kThreads / 2 : kThreads, me = tid & (threads - 1);
-        const int q = both ? tid / (kThreads / 2) : goes[1] ? 1 : 0;
-        const Unit u = q == 0 ? unit[0] : unit[1];
-        int from, n;
-        span(q, level, from, n);
-        const bool done[2] = {
-            level == 1 || unit[0].last_cta - unit[0].first_cta < kFan,
-            level == 1 || unit[1].last_cta - unit[1].first_cta < kFan};
-        const auto slot = [&](int c, int stage) {
-            return static_cast<int64_t>(4 * c + (c == u.first_cta ? 2 : 0) + stage) * S::rows;
-        };
-#pragma unroll 1
-        for (int i0 = me; i0 < u.m_real * (D / 4); i0 += 2 * threads) {
-            // Two pieces of 4 columns, kMany partials of each: one round trip.
-            constexpr int kMany = 4;
-            int row[2], col[2];
-            float4 acc[2];
-            float top[2], sum[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                row[i] = min((i0 + i * threads) / (D / 4), u.m_real - 1);
-                col[i] = (i0 + i * threads) % (D / 4);
-                acc[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                top[i] = -INFINITY;
-                sum[i] = 0.0f;
-            }
-#pragma unroll 1
-            for (int j0 = 0; j0 < n; j0 += kMany) {
-                float4 v[2][kMany];
-                float2 ml[2][kMany];
-#pragma unroll
-                for (int z = 0; z < kMany; ++z) {
-                    const int c = from + (j0 + z) * (level == 0 ? 1 : kFan);
-                    const int64_t at = slot(c, level);
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        v[i][z] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                        ml[i][z] = make_float2(-INFINITY, 0.0f);
-                        if (j0 + z < n) {
-                            v[i][z] = __ldcg(reinterpret_cast<const float4*>(p.part + (at + row[i]) * D) + col[i]);
-                            ml[i][z] = __ldcg(p.part_ml + at + row[i]);
-                        }
-                    }
-                }
-                add_partials<kMany>(acc[0], top[0], sum[0], v[0], ml[0]);
-                add_partials<kMany>(acc[1], top[1], sum[1], v[1], ml[1]);
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                if (i0 + i * threads >= u.m_real * (D / 4)) break;
-                if (q == 0 ? done[0] : done[1]) {
-                    write_row(p, u, D, row[i], 4 * col[i], acc[i], top[i], sum[i]);
-                } else {
-                    const int64_t to = slot(from, 1) + row[i];
-                    reinterpret_cast<float4*>(p.part + to * D)[col[i]] = acc[i];
-                    if (col[i] == 0) p.part_ml[to] = make_float2(top[i], sum[i]);
-                }
-            }
-        }
-        goes[0] = goes[0] && !done[0];
-        goes[1] = goes[1] && !done[1];
-        if (!goes[0] && !goes[1]) return;
-    }
+    join_units<D, S::rows, kThreads, kWarps>(p, base, S::warp_bytes, s_left, s_ml);
 }
 
 constexpr int kWorkersPerSm = 12;  // most warps on an SM (the workspace has room for them)
+
+// Where a launch's counts and partials lie in the workspace (p.arrived): of `rows` rows of
+// D columns for each of the most workers that a grid has.
+inline void set_workspace(PagedParams& p, int sms, int rows, int D) {
+    const int64_t most = static_cast<int64_t>(sms) * kWorkersPerSm, part_rows = most * rows;
+    p.head = reinterpret_cast<float*>(p.arrived) + 4 * most;
+    p.part = p.head + part_rows * D;
+    p.head_ml = reinterpret_cast<float2*>(p.part + part_rows * D);
+    p.part_ml = p.head_ml + part_rows;
+}
 
 template <typename S>
 int launch_decode(PagedParams p, const Maps<S::bits>& maps, int sms, int64_t tiles,
@@ -1329,18 +1359,11 @@ int launch_decode(PagedParams p, const Maps<S::bits>& maps, int sms, int64_t til
     auto kernel = paged_decode_kernel<S>;
     const int rc = limit.raise(kernel, S::smem(kMaxEntries));
     if (rc != SMD_OK) return rc;
-    const int64_t most = static_cast<int64_t>(sms) * kWorkersPerSm;
     const int64_t want = (tiles + kWarps - 1) / kWarps;  // a tile for each warp
     int64_t grid = static_cast<int64_t>(sms) * S::CTAS;
     if (grid > want) grid = want;
     p.workers = static_cast<int>(grid) * kWarps;
-    // The workspace: counts, then the partials of warps and CTAs.
-    float* at = reinterpret_cast<float*>(p.arrived) + 4 * most;
-    const int64_t part_rows = most * S::rows;
-    p.head = at;
-    p.part = p.head + part_rows * S::D;
-    p.head_ml = reinterpret_cast<float2*>(p.part + part_rows * S::D);
-    p.part_ml = p.head_ml + part_rows;
+    set_workspace(p, sms, S::rows, S::D);
     return launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), kThreads, S::smem(p.entries), stream,
                       p, maps);
 }
