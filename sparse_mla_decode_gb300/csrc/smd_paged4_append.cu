@@ -14,11 +14,11 @@
 // page's bounds (8 D bytes) where it is touched: HBM for prompts, the dependent
 // loads slot -> x for a decode step.
 //
-// D / 8 lanes hold a token of one head and side, 8 columns (16 bytes of bf16) each; two
-// neighbours share a block's scale. A token's codes depend on nothing else, so the lanes are
-// dealt out without regard to pages. Bounds are of runs (tokens whose slots continue one
-// another inside a page): few tokens: the lanes whose token begins a run read its
-// other keys too; many: a block takes the runs that begin in its chunk of tokens.
+// A lane holds a block of 16 columns, D / 16 lanes a token of one head and side. A token's
+// codes depend on nothing else, so the lanes are dealt out without regard to pages. Bounds are of
+// runs (tokens whose slots continue one another inside a page), D / 8 lanes of 8 columns: few
+// tokens: the lanes whose token begins a run read its keys too; many: a block takes the runs that
+// begin in its chunk of tokens.
 #include "smd_internal.h"
 #include "smd_paged.h"
 #include "smd_paged_append.cuh"
@@ -58,8 +58,20 @@ __device__ __forceinline__ float power(const int32_t* exps, int head, int sign) 
     return __uint_as_float(static_cast<uint32_t>(127 + sign * e) << 23);
 }
 
-// Two values' codes in a byte, from their quotients.
-__device__ __forceinline__ uint32_t codes_of(const float (&q)[8]) {
+// Eight codes of the nearest values to x `by`, the low nibble first.
+__device__ __forceinline__ uint32_t codes_of(const uint4& v, float by) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    float q[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        float x = lo_f(w[j]), y = hi_f(w[j]);
+        asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %2};\n\tmov.b64 c, {%3, %3};\n\t"
+            "fma.rn.f32x2 a, a, b, c;\n\tmov.b64 c, {%4, %4};\n\tadd.rn.f32x2 a, a, c;\n\tmov.b64 {%0, %1}, a;\n\t}"
+            : "+f"(x), "+f"(y)
+            : "f"(by), "f"(1024.0f), "f"(-1024.0f));
+        q[2 * j] = x;
+        q[2 * j + 1] = y;
+    }
     uint32_t r;
     asm("{\n\t.reg .b8 a, b, c, d;\n\t"
         "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
@@ -70,14 +82,14 @@ __device__ __forceinline__ uint32_t codes_of(const float (&q)[8]) {
     return r;
 }
 
-// Eight values (half a block: the lane beside has the other half; `mask`: the lanes that run
-// together): their codes, and the block's scale as E4M3.
-__device__ __forceinline__ uint32_t quantise(const uint4& v, float down, unsigned mask, uint32_t& scale) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t m = w[0] & 0x7fff7fffu;
+// A block of 16 values: their codes, and the scale as E4M3.
+__device__ __forceinline__ uint2 quantise(const uint4 (&v)[2], float down, uint32_t& scale) {
+    uint32_t m = 0;
 #pragma unroll
-    for (int j = 1; j < 4; ++j) m = bmax2_nan(m, w[j] & 0x7fff7fffu);
-    m = bmax2_nan(m, __shfl_xor_sync(mask, m, 1));
+    for (int j = 0; j < 2; ++j) {
+        m = bmax2_nan(m, bmax2_nan(v[j].x & 0x7fff7fffu, v[j].y & 0x7fff7fffu));
+        m = bmax2_nan(m, bmax2_nan(v[j].z & 0x7fff7fffu, v[j].w & 0x7fff7fffu));
+    }
     float a;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(a) : "f"(lo_f(m)), "f"(hi_f(m)));
     asm("min.NaN.f32 %0, %1, %2;" : "=f"(a) : "f"(a * down), "f"(65536.0f));  // far above 6 * 448
@@ -92,13 +104,7 @@ __device__ __forceinline__ uint32_t quantise(const uint4& v, float down, unsigne
     float by;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(by) : "f"(s));
     by = s > 0.0f ? by * down : 0.0f;
-    float q[8];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        q[2 * j] = fmaf(lo_f(w[j]), by, 1024.0f) - 1024.0f;
-        q[2 * j + 1] = fmaf(hi_f(w[j]), by, 1024.0f) - 1024.0f;
-    }
-    return codes_of(q);
+    return make_uint2(codes_of(v[0], by), codes_of(v[1], by));
 }
 
 // Whether the slot is in the pool.
@@ -106,22 +112,31 @@ __device__ __forceinline__ bool in_pool(const Append4Params& p, int slot) {
     return slot >= 0 && slot / p.P < p.pages;
 }
 
+// Block i of a token.
 template <int D>
 __device__ __forceinline__ void store(const Append4Params& p, int side, int head, int slot, int i,
-                                      uint32_t codes, uint32_t scale) {
+                                      const uint2& codes, uint32_t scale) {
     const int page = slot / p.P, o = slot - page * p.P;
     const int64_t* const st = p.stride[side];
-    *reinterpret_cast<uint32_t*>(p.pool[side] + page * st[0] + head * st[1] + o * st[2] + 4 * i) = codes;
-    if ((i & 1) == 0)
-        p.scales[side][((static_cast<int64_t>(page) * p.heads + head) * p.P + o) * (D / 16) + (i >> 1)] =
-            static_cast<uint8_t>(scale);
+    *reinterpret_cast<uint2*>(p.pool[side] + page * st[0] + head * st[1] + o * st[2] + 8 * i) = codes;
+    p.scales[side][((static_cast<int64_t>(page) * p.heads + head) * p.P + o) * (D / 16) + i] =
+        static_cast<uint8_t>(scale);
 }
 
-// The extremes of n keys from token t on: 8 columns, every `step`-th token.
+// The extremes of n keys: 8 columns, every `step`-th token, kLoads of them in flight.
+template <int kLoads>
 __device__ __forceinline__ void scan_keys(const uint16_t* x, int64_t xs, int n, int step, uint32_t (&hi)[4],
                                           uint32_t (&lo)[4]) {
-#pragma unroll 4
-    for (int m = 0; m < n; m += step) take(*reinterpret_cast<const uint4*>(x + m * xs), hi, lo);
+#pragma unroll 1
+    for (int m0 = 0; m0 < n; m0 += kLoads * step) {
+        uint4 v[kLoads];
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j)
+            if (m0 + j * step < n) v[j] = __ldg(reinterpret_cast<const uint4*>(x + (m0 + j * step) * xs));
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j)
+            if (m0 + j * step < n) take(v[j], hi, lo);
+    }
 }
 
 __device__ __forceinline__ void nothing_met(uint32_t (&hi)[4], uint32_t (&lo)[4]) {
@@ -141,29 +156,30 @@ __device__ __forceinline__ void run_bounds(const Append4Params& p, int64_t t, in
     if (o > 0) was.read(bounds, D, 8 * i);
     uint32_t hi[4], lo[4];
     nothing_met(hi, lo);
-    scan_keys(p.x[0] + t * p.x_stride[0] + head * D + 8 * i, p.x_stride[0], n, 1, hi, lo);
+    scan_keys<4>(p.x[0] + t * p.x_stride[0] + head * D + 8 * i, p.x_stride[0], n, 1, hi, lo);
     write_bounds(bounds, D, 8 * i, was, hi, lo);
 }
 
-// D / 8 lanes for each (token, head, side).
+// D / 8 lanes for each (token, head): one half the keys, the other the values.
 template <int D>
 __global__ void __launch_bounds__(kThreads) append4_few_kernel(const Append4Params p) {
     constexpr int N = D / 8;
     pdl_entry();
-    const int lane = threadIdx.x & 31, i = threadIdx.x % N;
+    const int lane = threadIdx.x & 31, i = threadIdx.x % N, side = i / (N / 2), b = i % (N / 2);
     const unsigned mask = group_mask<N>(lane);
     const int64_t unit = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / N;
-    const int t = static_cast<int>(unit / (2 * p.heads)), hs = static_cast<int>(unit % (2 * p.heads));
+    const int t = static_cast<int>(unit / p.heads), head = static_cast<int>(unit % p.heads);
     if (t >= p.T) return;
-    const int side = hs & 1, head = hs >> 1;
-    const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p.x[side] + t * p.x_stride[side] + head * D + 8 * i));
+    const uint4* const x =
+        reinterpret_cast<const uint4*>(p.x[side] + t * p.x_stride[side] + head * D + 16 * b);
+    const uint4 v[2] = {__ldg(x), __ldg(x + 1)};
     const int slot = p.slots[t];
+    const int before = p.bounds != nullptr && t > 0 ? p.slots[t - 1] : -2;
     if (!in_pool(p, slot)) return;
     uint32_t scale;
-    const uint32_t codes = quantise(v, power(p.exps[side], head, -1), mask, scale);
-    store<D>(p, side, head, slot, i, codes, scale);
-    if (p.bounds == nullptr || side != 0) return;
-    if (t > 0 && slot % p.P != 0 && p.slots[t - 1] == slot - 1) return;  // not a run's first
+    const uint2 codes = quantise(v, power(p.exps[side], head, -1), scale);
+    store<D>(p, side, head, slot, b, codes, scale);
+    if (p.bounds == nullptr || (slot % p.P != 0 && before == slot - 1)) return;  // not a run's first
     const int most = min(p.P - slot % p.P, p.T - t);
     int n = 1;
     while (n < most) {
@@ -176,103 +192,132 @@ __global__ void __launch_bounds__(kThreads) append4_few_kernel(const Append4Para
     run_bounds<D>(p, t, n, slot, head, i);
 }
 
-// A block for each chunk of tokens and head.
-template <int D>
-__global__ void __launch_bounds__(kThreads) append4_many_kernel(const Append4Params p) {
+// A block for each chunk of tokens and head. kBounds: then the bounds of the runs that begin in the
+// chunk, whose keys are read again, from L1 or L2.
+template <int D, bool kBounds>
+__global__ void __launch_bounds__(kThreads, 8) append4_many_kernel(const Append4Params p) {
     constexpr int N = D / 8, kGroups = kThreads / N;
     __shared__ int s_slot[kChunk];
     __shared__ int2 s_runs[kChunk];  // first token and length: short runs from the front, long from the back
     __shared__ uint32_t s_goes[(kChunk + kMostPage) / 32], s_lead[kChunk / 32];
     __shared__ int s_short, s_long;
     __shared__ uint4 s_hi[kGroups][N], s_lo[kGroups][N];
-    const int tid = threadIdx.x, lane = tid & 31, i = tid % N, group = tid / N;
-    const unsigned mask = group_mask<N>(lane);
-    const int head = blockIdx.y;
-    if (tid == 0) s_short = s_long = 0;
+    const int tid = threadIdx.x, lane = tid & 31, head = blockIdx.y;
     pdl_entry();
     const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kChunk;
     const int span = static_cast<int>(min(static_cast<int64_t>(p.T) - t0, static_cast<int64_t>(kChunk)));
-    const float down[2] = {power(p.exps[0], head, -1), power(p.exps[1], head, -1)};
     if (tid < span) s_slot[tid] = p.slots[t0 + tid];
-    __syncthreads();
-    // Codes: a group's unit is a token and a side.
-#pragma unroll 1
-    for (int u0 = group; u0 < 2 * span; u0 += kAtOnce * kGroups) {
-        uint4 v[kAtOnce];
-#pragma unroll
-        for (int j = 0; j < kAtOnce; ++j) {
-            const int u = u0 + j * kGroups, t = u >> 1, side = u & 1;
-            v[j] = make_uint4(0, 0, 0, 0);
-            if (u < 2 * span)
-                v[j] = *reinterpret_cast<const uint4*>(p.x[side] + (t0 + t) * p.x_stride[side] + head * D + 8 * i);
-        }
-#pragma unroll
-        for (int j = 0; j < kAtOnce; ++j) {
-            const int u = u0 + j * kGroups, t = u >> 1, side = u & 1;
-            if (u >= 2 * span) break;  // the same in a group's lanes
-            uint32_t scale;
-            const uint32_t codes = quantise(v[j], down[side], mask, scale);
-            if (in_pool(p, s_slot[t])) store<D>(p, side, head, s_slot[t], i, codes, scale);
-        }
-    }
-    if (p.bounds == nullptr) return;
-
-    // Bounds. A token goes on with the run of the one before it, or it leads one; a run of this
-    // chunk may go on into the next chunks.
-    const int seen = static_cast<int>(min(static_cast<int64_t>(p.T) - t0, static_cast<int64_t>(kChunk) + p.P));
-    for (int j0 = 0; j0 < kChunk + p.P; j0 += kThreads) {
-        const int j = j0 + tid;
-        bool goes = false, lead = false;
-        if (j < seen) {
-            const int slot = p.slots[t0 + j], before = t0 + j > 0 ? p.slots[t0 + j - 1] : -2;
-            if (in_pool(p, slot)) {
-                goes = slot % p.P != 0 && before == slot - 1;
-                lead = !goes && j < span;
+    if constexpr (kBounds) {
+        // A token goes on with the run of the one before it, or it leads one; a run of this chunk may go
+        // on into the next chunks.
+        if (tid == 0) s_short = s_long = 0;
+        const int seen = static_cast<int>(min(static_cast<int64_t>(p.T) - t0, static_cast<int64_t>(kChunk) + p.P));
+        for (int j0 = 0; j0 < kChunk + p.P; j0 += kThreads) {
+            const int j = j0 + tid;
+            bool goes = false, lead = false;
+            if (j < seen) {
+                const int slot = p.slots[t0 + j], before = t0 + j > 0 ? p.slots[t0 + j - 1] : -2;
+                if (in_pool(p, slot)) {
+                    goes = slot % p.P != 0 && before == slot - 1;
+                    lead = !goes && j < span;
+                }
+            }
+            const uint32_t g = __ballot_sync(0xffffffffu, goes), l = __ballot_sync(0xffffffffu, lead);
+            if (lane == 0 && j < kChunk + kMostPage) {
+                s_goes[j >> 5] = g;
+                if (j < kChunk) s_lead[j >> 5] = l;
             }
         }
-        const uint32_t g = __ballot_sync(0xffffffffu, goes), l = __ballot_sync(0xffffffffu, lead);
-        if (lane == 0 && j < kChunk + kMostPage) {
-            s_goes[j >> 5] = g;
-            if (j < kChunk) s_lead[j >> 5] = l;
-        }
-    }
-    __syncthreads();
-    constexpr int kShort = 8;  // runs up to this length go to a group of lanes each
-    if (tid < kChunk && (s_lead[tid >> 5] >> (tid & 31) & 1) != 0) {
-        int end = tid + 1;  // the first token after this one that does not go on
-        while (end < kChunk + p.P) {
-            const uint32_t stop = ~s_goes[end >> 5] >> (end & 31);
-            if (stop != 0) {
-                end += __ffs(stop) - 1;
-                break;
+        __syncthreads();
+        constexpr int kShort = 4;  // runs up to this length go to D / 8 lanes each
+        if (tid < kChunk && (s_lead[tid >> 5] >> (tid & 31) & 1) != 0) {
+            int end = tid + 1;  // the first token after this one that does not go on
+            while (end < kChunk + p.P) {
+                const uint32_t stop = ~s_goes[end >> 5] >> (end & 31);
+                if (stop != 0) {
+                    end += __ffs(stop) - 1;
+                    break;
+                }
+                end = (end | 31) + 1;
             }
-            end = (end | 31) + 1;
+            const int n = min(end, seen) - tid;
+            const int at = n <= kShort ? atomicAdd(&s_short, 1) : kChunk - 1 - atomicAdd(&s_long, 1);
+            s_runs[at] = make_int2(tid, n);
         }
-        const int n = min(end, seen) - tid;
-        const int at = n <= kShort ? atomicAdd(&s_short, 1) : kChunk - 1 - atomicAdd(&s_long, 1);
-        s_runs[at] = make_int2(tid, n);
     }
     __syncthreads();
+    {
+        // Codes: a unit of D / 16 lanes is a token and a side.
+        constexpr int NB = D / 16, kUnits = kThreads / NB;  // units at a time: as many of each side
+        const int i = tid % NB, unit = tid / NB, side = unit & 1;
+        const float by = power(p.exps[side], head, -1);
+        const uint16_t* const x = p.x[side] + t0 * p.x_stride[side] + head * D + 16 * i;
 #pragma unroll 1
-    for (int u = group; u < s_short; u += kGroups) {
-        const int2 r = s_runs[u];
-        run_bounds<D>(p, t0 + r.x, r.y, s_slot[r.x], head, i);
+        for (int m0 = unit >> 1; m0 < span; m0 += kAtOnce * (kUnits / 2)) {
+            uint4 v[kAtOnce][2];
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) {
+                const int m = m0 + j * (kUnits / 2);
+                if (m < span) {
+                    const uint4* const at = reinterpret_cast<const uint4*>(x + m * p.x_stride[side]);
+                    v[j][0] = __ldg(at);
+                    v[j][1] = __ldg(at + 1);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) {
+                const int m = m0 + j * (kUnits / 2);
+                if (m >= span) break;
+                uint32_t scale;
+                const uint2 codes = quantise(v[j], by, scale);
+                if (in_pool(p, s_slot[m])) store<D>(p, side, head, s_slot[m], i, codes, scale);
+            }
+        }
+    }
+    if constexpr (!kBounds) return;
+    const int i = tid % N, group = tid / N;
+    __syncthreads();
+    const uint16_t* const x = p.x[0] + t0 * p.x_stride[0] + head * D + 8 * i;
+    const auto extremes = [&](const int2& r, int first, int step, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+        nothing_met(hi, lo);
+#pragma unroll 4
+        for (int m = r.x + first; m < r.x + r.y; m += step)
+            take(__ldg(reinterpret_cast<const uint4*>(x + m * p.x_stride[0])), hi, lo);
+    };
+    const auto bounds_of = [&](int slot) {
+        return p.bounds + (static_cast<int64_t>(slot / p.P) * p.heads + head) * 2 * D;
+    };
+    constexpr int kRuns = 4;  // short runs of a group whose pages' bounds are on their way together
+#pragma unroll 1
+    for (int u0 = group; u0 < s_short; u0 += kRuns * kGroups) {
+        Extremes was[kRuns];
+#pragma unroll
+        for (int j = 0; j < kRuns; ++j)
+            if (u0 + j * kGroups < s_short) {
+                const int slot = s_slot[s_runs[u0 + j * kGroups].x];
+                if (slot % p.P != 0) was[j].read(bounds_of(slot), D, 8 * i);
+            }
+#pragma unroll
+        for (int j = 0; j < kRuns; ++j)
+            if (u0 + j * kGroups < s_short) {
+                const int2 r = s_runs[u0 + j * kGroups];
+                uint32_t hi[4], lo[4];
+                extremes(r, 0, 1, hi, lo);
+                write_bounds(bounds_of(s_slot[r.x]), D, 8 * i, was[j], hi, lo);
+            }
     }
 #pragma unroll 1
     for (int u = 0; u < s_long; ++u) {
         const int2 r = s_runs[kChunk - 1 - u];
+        const int slot = s_slot[r.x];
+        Extremes was;
+        if (group == 0 && slot % p.P != 0) was.read(bounds_of(slot), D, 8 * i);
         uint32_t hi[4], lo[4];
-        nothing_met(hi, lo);
-        scan_keys(p.x[0] + (t0 + r.x + group) * p.x_stride[0] + head * D + 8 * i, p.x_stride[0], r.y - group,
-                  kGroups, hi, lo);
+        extremes(r, group, kGroups, hi, lo);
         s_hi[group][i] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         s_lo[group][i] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         __syncthreads();
         if (group == 0) {
-            const int slot = s_slot[r.x], page = slot / p.P, o = slot - page * p.P;
-            uint16_t* const bounds = p.bounds + (static_cast<int64_t>(page) * p.heads + head) * 2 * D;
-            Extremes was;
-            if (o > 0) was.read(bounds, D, 8 * i);
 #pragma unroll
             for (int g = 1; g < kGroups; ++g) {
                 const uint4 h = s_hi[g][i], l = s_lo[g][i];
@@ -281,7 +326,7 @@ __global__ void __launch_bounds__(kThreads) append4_many_kernel(const Append4Par
                 lo[0] = bmin2(lo[0], l.x), lo[1] = bmin2(lo[1], l.y);
                 lo[2] = bmin2(lo[2], l.z), lo[3] = bmin2(lo[3], l.w);
             }
-            write_bounds(bounds, D, 8 * i, was, hi, lo);
+            write_bounds(bounds_of(slot), D, 8 * i, was, hi, lo);
         }
         __syncthreads();
     }
@@ -298,65 +343,90 @@ struct Read4Params {
     int64_t out_stride[2];
     int32_t pages, heads, P;
     int32_t first, sides;  // the first side that is read, and how many
+    int32_t shares;        // units that share a token's heads
 };
 
-// D / 8 lanes for each (token, side, head): 8 columns each.
+// D / 16 lanes for each (token, side) and share of the heads: a block of 16 columns each.
 template <int D>
 __global__ void __launch_bounds__(kThreads) read4_kernel(const Read4Params p) {
-    constexpr int N = D / 8;
+    constexpr int N = D / 16;
     pdl_entry();
     const int i = threadIdx.x % N;
     const int64_t unit = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / N;
-    const int head = static_cast<int>(unit % p.heads);
-    const int64_t ts = unit / p.heads;
-    const int64_t t = ts / p.sides;
+    const int64_t ts = unit / p.shares, t = ts / p.sides;
     const int side = p.first + static_cast<int>(ts % p.sides);
     if (t >= p.T) return;
     const int slot = p.slots[t], page = slot / p.P, o = slot - page * p.P;
     if (slot < 0 || page >= p.pages) return;
     const int64_t* const st = p.stride[side];
-    const uint32_t codes =
-        *reinterpret_cast<const uint32_t*>(p.pool[side] + page * st[0] + head * st[1] + o * st[2] + 4 * i);
-    const uint32_t scale =
-        p.scales[side][((static_cast<int64_t>(page) * p.heads + head) * p.P + o) * (D / 16) + (i >> 1)];
-    const float up = power(p.exps[side], head, 1);
-    uint32_t w[4];
-    asm("{\n\t.reg .b8 a, b, c, d;\n\t.reg .b16 s;\n\t.reg .b32 t;\n\t"
-        "cvt.u16.u32 s, %5;\n\tcvt.rn.f16x2.e4m3x2 t, s;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t"
-        "mul.rn.f16x2 %0, %0, t;\n\tmul.rn.f16x2 %1, %1, t;\n\t"
-        "mul.rn.f16x2 %2, %2, t;\n\tmul.rn.f16x2 %3, %3, t;\n\t}"
-        : "=&r"(w[0]), "=&r"(w[1]), "=&r"(w[2]), "=&r"(w[3])
-        : "r"(codes), "r"(scale * 0x101u));
+    const uint8_t* const pool = p.pool[side] + page * st[0] + o * st[2] + 8 * i;
+    const uint8_t* const scales =
+        p.scales[side] + (static_cast<int64_t>(page) * p.heads * p.P + o) * (D / 16) + i;
+    uint16_t* const out = p.out[side] + t * p.out_stride[side] + 16 * i;
+#pragma unroll 1
+    for (int h0 = static_cast<int>(unit % p.shares); h0 < p.heads; h0 += kAtOnce * p.shares) {
+        uint2 codes[kAtOnce];
+        uint32_t scale[kAtOnce];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        float a, b;
-        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
-            : "=f"(a), "=f"(b)
-            : "r"(w[j]));
-        w[j] = bf16x2(a * up, b * up);
+        for (int j = 0; j < kAtOnce; ++j) {
+            const int h = h0 + j * p.shares;
+            if (h < p.heads) {
+                codes[j] = __ldg(reinterpret_cast<const uint2*>(pool + h * st[1]));
+                scale[j] = __ldg(scales + static_cast<int64_t>(h) * p.P * (D / 16));
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+            const int h = h0 + j * p.shares;
+            if (h >= p.heads) break;
+            const float up = power(p.exps[side], h, 1);
+            uint32_t w[8];
+#pragma unroll
+            for (int z = 0; z < 2; ++z)
+                asm("{\n\t.reg .b8 a, b, c, d;\n\t.reg .b16 s;\n\t.reg .b32 t;\n\t"
+                    "cvt.u16.u32 s, %5;\n\tcvt.rn.f16x2.e4m3x2 t, s;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+                    "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+                    "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t"
+                    "mul.rn.f16x2 %0, %0, t;\n\tmul.rn.f16x2 %1, %1, t;\n\t"
+                    "mul.rn.f16x2 %2, %2, t;\n\tmul.rn.f16x2 %3, %3, t;\n\t}"
+                    : "=&r"(w[4 * z]), "=&r"(w[4 * z + 1]), "=&r"(w[4 * z + 2]), "=&r"(w[4 * z + 3])
+                    : "r"(z == 0 ? codes[j].x : codes[j].y), "r"(scale[j] * 0x101u));
+#pragma unroll
+            for (int z = 0; z < 8; ++z) {
+                float a, b;
+                asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
+                    : "=f"(a), "=f"(b)
+                    : "r"(w[z]));
+                w[z] = bf16x2(a * up, b * up);
+            }
+            uint4* const to = reinterpret_cast<uint4*>(out + h * D);
+            __stcs(to, make_uint4(w[0], w[1], w[2], w[3]));
+            __stcs(to + 1, make_uint4(w[4], w[5], w[6], w[7]));
+        }
     }
-    *reinterpret_cast<uint4*>(p.out[side] + t * p.out_stride[side] + head * D + 8 * i) =
-        make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 template <int D>
 int launch_append(const Append4Params& p, int sms, smd_stream_t stream) {
-    const int64_t units = static_cast<int64_t>(p.T) * p.heads * 2;
-    if (units <= static_cast<int64_t>(sms) * 256)
+    const int64_t units = static_cast<int64_t>(p.T) * p.heads;
+    if (units <= static_cast<int64_t>(sms) * 128)
         return launch_pdl(append4_few_kernel<D>,
                           dim3(static_cast<unsigned>((units * (D / 8) + kThreads - 1) / kThreads)),
                           kThreads, 0, stream, p);
-    return launch_pdl(append4_many_kernel<D>,
-                      dim3(static_cast<unsigned>((static_cast<int64_t>(p.T) + kChunk - 1) / kChunk),
-                           static_cast<unsigned>(p.heads)),
-                      kThreads, 0, stream, p);
+    const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(p.T) + kChunk - 1) / kChunk),
+                    static_cast<unsigned>(p.heads));
+    return p.bounds != nullptr ? launch_pdl(append4_many_kernel<D, true>, grid, kThreads, 0, stream, p)
+                               : launch_pdl(append4_many_kernel<D, false>, grid, kThreads, 0, stream, p);
 }
 
 template <int D>
-int launch_read(const Read4Params& p, smd_stream_t stream) {
-    const int64_t blocks = (static_cast<int64_t>(p.T) * p.heads * p.sides * (D / 8) + kThreads - 1) / kThreads;
+int launch_read(Read4Params p, int sms, smd_stream_t stream) {
+    // A token's heads go to one unit, kAtOnce at a time, unless that leaves SMs without work (96
+    // tokens of 8 heads: 2.6 us by one unit or two, 1.8 by eight).
+    const int64_t units = static_cast<int64_t>(p.T) * p.sides, want = static_cast<int64_t>(sms) * 2 * kThreads / (D / 16);
+    const int64_t shares = (want + units - 1) / units;
+    p.shares = static_cast<int32_t>(shares < 1 ? 1 : shares < p.heads ? shares : p.heads);
+    const int64_t blocks = (units * p.shares * (D / 16) + kThreads - 1) / kThreads;
     if (blocks >= (1ll << 31)) return SMD_ERR_SHAPE;
     return launch_pdl(read4_kernel<D>, dim3(static_cast<unsigned>(blocks)), kThreads, 0, stream, p);
 }
@@ -439,7 +509,9 @@ extern "C" int smd_paged4_read(const smd_paged4_cache_t* cache, const int32_t* s
     p.P = cache->page_size;
     p.first = k != nullptr ? 0 : 1;
     p.sides = (k != nullptr ? 1 : 0) + (v != nullptr ? 1 : 0);
-    return cache->head_dim == 64    ? launch_read<64>(p, stream)
-           : cache->head_dim == 128 ? launch_read<128>(p, stream)
-                                    : launch_read<256>(p, stream);
+    const int sms = device_sms();
+    if (sms <= 0) return SMD_ERR_DEVICE;
+    return cache->head_dim == 64    ? launch_read<64>(p, sms, stream)
+           : cache->head_dim == 128 ? launch_read<128>(p, sms, stream)
+                                    : launch_read<256>(p, sms, stream);
 }
