@@ -19,6 +19,13 @@
 // runs (tokens whose slots continue one another inside a page), D / 8 lanes of 8 columns: few
 // tokens: the lanes whose token begins a run read its keys too; many: a block takes the runs that
 // begin in its chunk of tokens.
+//
+// Measured (GB300, device time): 96 tokens of as many requests, 8 heads of 128 columns, 2.6 us (1.8
+// without bounds); 28 thousand tokens of 23 requests 35 us, 63% of the copy rate for the 146 MB (27
+// without bounds, 80%: the bounds read the keys again from L2 and follow the codes), 256 columns 62 (71%),
+// 64 columns in pages of 16 29 (38%). Read: 96 tokens 2.0 us, 28 thousand 31.5 (69%: conversions, 4 heads
+// on their way in a lane). Tried for the bounds: blocks of their own beside those of the codes 36 us, behind them
+// 44 (the keys have left L2), keys kept in shared memory 41.
 #include "smd_internal.h"
 #include "smd_paged.h"
 #include "smd_paged_append.cuh"
@@ -408,8 +415,16 @@ __global__ void __launch_bounds__(kThreads) read4_kernel(const Read4Params p) {
 
 template <int D>
 int launch_append(const Append4Params& p, int sms, smd_stream_t stream) {
+    // Few tokens: lanes for each. Many: blocks by chunks of tokens. Few / many in us, 8 heads of 128
+    // columns, pages of 64 (in brackets without bounds):
+    //   96 tokens of as many requests   2.6 /  8.3  ( 1.8 /  4.3)
+    //   3000 of as many                 7.4 / 13.5  ( 4.7 /  6.7)
+    //   8000 of as many                19.7 / 20.5  (10.1 /  9.7)
+    //   500 of one                      8.0 /  6.3  ( 2.3 /  4.3)
+    //   4000 of one, of 30             11.5 / 10.4, 11.7  ( 5.7 /  8.2)
+    //   16000 of one                   28.3 / 19.8  (18.9 / 15.2)
     const int64_t units = static_cast<int64_t>(p.T) * p.heads;
-    if (units <= static_cast<int64_t>(sms) * 128)
+    if (units <= static_cast<int64_t>(sms) * 384)
         return launch_pdl(append4_few_kernel<D>,
                           dim3(static_cast<unsigned>((units * (D / 8) + kThreads - 1) / kThreads)),
                           kThreads, 0, stream, p);

@@ -16,7 +16,12 @@
 // columns, so that both columns of a pair are in one lane in either order of pairs, and loads
 // and stores are 16 bytes. A block takes a few tokens: its threads compute a sine and cosine
 // each, into shared memory; a group of lanes then keeps those of its token in
-// registers over its heads.
+// registers over its heads, three heads on their way at a time. Weights are in shared memory too, in fp32.
+//
+// Measured (GB300, device time): 28 thousand tokens, 64 + 8 heads of 128 columns, three axes 165 us, 93% of the
+// copy rate (159 without norm; 256 columns 92%, 64 89%, 16 of 128 columns turning 89%); 1000 tokens 8.4
+// (66%: start); 96 tokens 3.3; 28 thousand tokens of 5 heads 28 (38%: angles). With 80 registers a thread
+// the kernel spills and takes 204.
 #include "smd_internal.h"
 #include "smd_paged.h"
 #include "smd_ptx.cuh"
@@ -26,7 +31,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxAxes = 4;
-constexpr int kAtOnce = 3;  // heads of a group in flight
 
 struct RopeParams {
     const uint16_t* x[2];  // queries, keys
@@ -56,52 +60,104 @@ __device__ __forceinline__ uint64_t turns(float f) {
     return (u >> 31) != 0 ? 0 - t : t;
 }
 
+// Two fp32 values in a register pair, and operations on both.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 __device__ __forceinline__ float lo_f(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float hi_f(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
-__device__ __forceinline__ void widen(const uint4& v, float* f) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// A lane's 16 columns as the first and second columns of 8 pairs that turn together: chunk 0 with
+// chunk 1, or (kInter) even columns with odd ones.
+template <bool kInter>
+__device__ __forceinline__ void widen(const uint4& c0, const uint4& c1, uint64_t (&x)[4], uint64_t (&y)[4]) {
+    const uint32_t a[4] = {c0.x, c0.y, c0.z, c0.w}, b[4] = {c1.x, c1.y, c1.z, c1.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        f[2 * j] = lo_f(w[j]);
-        f[2 * j + 1] = hi_f(w[j]);
+        if (kInter) {
+            const uint32_t u = j < 2 ? a[2 * j] : b[2 * j - 4], v = j < 2 ? a[2 * j + 1] : b[2 * j - 3];
+            x[j] = pack2(lo_f(u), lo_f(v));
+            y[j] = pack2(hi_f(u), hi_f(v));
+        } else {
+            x[j] = pack2(lo_f(a[j]), hi_f(a[j]));
+            y[j] = pack2(lo_f(b[j]), hi_f(b[j]));
+        }
     }
 }
 
-__device__ __forceinline__ uint4 narrow(const float* f) {
-    return make_uint4(bf16x2(f[0], f[1]), bf16x2(f[2], f[3]), bf16x2(f[4], f[5]), bf16x2(f[6], f[7]));
+template <bool kInter>
+__device__ __forceinline__ void narrow(const uint64_t (&x)[4], const uint64_t (&y)[4], uint4& c0, uint4& c1) {
+    uint32_t a[4], b[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        float x0, x1, y0, y1;
+        unpack2(x[j], x0, x1);
+        unpack2(y[j], y0, y1);
+        if (kInter) {
+            (j < 2 ? a[2 * j] : b[2 * j - 4]) = bf16x2(x0, y0);
+            (j < 2 ? a[2 * j + 1] : b[2 * j - 3]) = bf16x2(x1, y1);
+        } else {
+            a[j] = bf16x2(x0, x1);
+            b[j] = bf16x2(y0, y1);
+        }
+    }
+    c0 = make_uint4(a[0], a[1], a[2], a[3]);
+    c1 = make_uint4(b[0], b[1], b[2], b[3]);
 }
 
-// TB tokens of a block; kInter: pairs (2 j, 2 j + 1).
-template <int D, int TB, bool kInter>
-__global__ void __launch_bounds__(kThreads) qk_rope_kernel(const RopeParams p) {
+// TB tokens of a block; kInter: pairs (2 j, 2 j + 1); kNorm: a weight is given.
+template <int D, int TB, bool kInter, bool kNorm>
+__global__ void __launch_bounds__(kThreads, TB == 512 / D ? 2 : 3) qk_rope_kernel(const RopeParams p) {
+    constexpr int kAtOnce = TB == 512 / D ? 3 : 1;          // heads of a group in flight
     constexpr int N = D / 16, kGroups = kThreads / N / TB;  // lanes of a head; groups of a token
+    static_assert(kGroups >= 1, "a group for each token");
     __shared__ uint64_t s_freq[kMaxAxes][D / 2];
-    __shared__ __align__(16) float s_cos[TB][D / 2], s_sin[TB][D / 2];
+    __shared__ __align__(16) float s_cos[TB][D / 2], s_sin[TB][D / 2], s_w[2][kNorm ? D : 4];  // [2][D / 8] four columns
     const int tid = threadIdx.x, half = p.rot / 2, turning = p.rot / 16;
     pdl_entry();
     for (int i = tid; i < p.axes * half; i += kThreads) s_freq[i / half][i % half] = turns(__ldg(p.freqs + i));
+    if (kNorm)  // in the order of widen(): the first four columns of each chunk, then the others
+        for (int u = tid; u < 2 * D; u += kThreads) {
+            const int side = u / D, c = u % D, k = kInter ? (c & 1) * 4 + (c & 7) / 2 : c & 7;
+            s_w[side][(k >> 2) * (D / 2) + c / 8 * 4 + (k & 3)] =
+                p.w[side] == nullptr ? 1.0f : lo_f(__ldg(p.w[side] + c));
+        }
+    const bool normed[2] = {p.w[0] != nullptr, p.w[1] != nullptr};
     const int i = tid % N, group = tid / N, tl = group / kGroups, g = group % kGroups;
     // The lane's chunks of 8 columns.
     const bool turns_here = i < turning;
-    const int c0 = turns_here ? i : 2 * i, c1 = turns_here ? i + turning : 2 * i + 1;
+    const int c0 = turns_here ? i : i + turning, c1 = turns_here ? i + turning : i + N;
     const int slice = static_cast<int>(blockIdx.x) % p.slices, step = kGroups * p.slices;
     const int chunks = (p.T + TB - 1) / TB, stride = static_cast<int>(gridDim.x) / p.slices;
+    const unsigned mask = N == 32 ? 0xffffffffu : ((1u << N) - 1u) << ((tid & 31) / N * N);
 #pragma unroll 1
     for (int chunk = static_cast<int>(blockIdx.x) / p.slices; chunk < chunks; chunk += stride) {
         const int t0 = chunk * TB, t = t0 + tl;
         const bool live = t < p.T && (p.positions == nullptr || __ldg(p.positions + t) >= 0);
-        const auto row = [&](int h) {  // a head's first column
-            const int side = h >= p.Hq ? 1 : 0;
-            return p.x[side] + t * p.x_stride[side] + static_cast<int64_t>(h - side * p.Hq) * D;
-        };
-        uint4 v[kAtOnce][2];
+        uint4 v[kAtOnce][2] = {};
         const auto load = [&](int h0) {
 #pragma unroll
             for (int j = 0; j < kAtOnce; ++j) {
-                const int h = h0 + j * step;
+                const int h = h0 + j * step, side = h >= p.Hq ? 1 : 0;
                 if (live && h < p.H) {
-                    const uint4* const x = reinterpret_cast<const uint4*>(row(h));
+                    const uint4* const x = reinterpret_cast<const uint4*>(
+                        p.x[side] + t * p.x_stride[side] + static_cast<int64_t>(h - side * p.Hq) * D);
                     v[j][0] = __ldcs(x + c0);
                     v[j][1] = __ldcs(x + c1);
                 }
@@ -122,89 +178,107 @@ __global__ void __launch_bounds__(kThreads) qk_rope_kernel(const RopeParams p) {
             sincospif(x, &s_sin[tt][j], &s_cos[tt][j]);
         }
         __syncthreads();
-        if (live) {
-            // Pairs of the lane: 8 i .. 8 i + 7; interleaved: 4 c0 .., 4 c1 ..
-            float cs[8], sn[8];
-            if (turns_here) {
+        if (!live) continue;
+        // Pairs of the lane: 8 i .. 8 i + 7; interleaved: 4 c0 .., 4 c1 ..
+        uint64_t cs[4], sn[4];
 #pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                    const int at = kInter ? 4 * (z == 0 ? c0 : c1) : 8 * i + 4 * z;
-                    const float4 c = *reinterpret_cast<const float4*>(&s_cos[tl][at]);
-                    const float4 s = *reinterpret_cast<const float4*>(&s_sin[tl][at]);
-                    cs[4 * z] = c.x, cs[4 * z + 1] = c.y, cs[4 * z + 2] = c.z, cs[4 * z + 3] = c.w;
-                    sn[4 * z] = s.x, sn[4 * z + 1] = s.y, sn[4 * z + 2] = s.z, sn[4 * z + 3] = s.w;
-                }
-            }
-            uint4 w[2];
-            int w_side = -1;
-            const unsigned mask = N == 32 ? 0xffffffffu : ((1u << N) - 1u) << ((tid & 31) / N * N);
+        for (int z = 0; z < 2; ++z) {
+            const int at = !turns_here ? 0 : kInter ? 4 * (z == 0 ? c0 : c1) : 8 * i + 4 * z;
+            const float4 c = *reinterpret_cast<const float4*>(&s_cos[tl][at]);
+            const float4 s = *reinterpret_cast<const float4*>(&s_sin[tl][at]);
+            cs[2 * z] = pack2(c.x, c.y), cs[2 * z + 1] = pack2(c.z, c.w);
+            sn[2 * z] = pack2(s.x, s.y), sn[2 * z + 1] = pack2(s.z, s.w);
+        }
 #pragma unroll 1
-            while (h0 < p.H) {
+        while (h0 < p.H) {
+            uint64_t x[kAtOnce][4], y[kAtOnce][4];
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) widen<kInter>(v[j][0], v[j][1], x[j], y[j]);
+            const int h1 = h0;
+            h0 += kAtOnce * step;
+            load(h0);
+            if (kNorm) {
+                float sum[kAtOnce];
 #pragma unroll
                 for (int j = 0; j < kAtOnce; ++j) {
-                    const int h = h0 + j * step;
-                    if (h >= p.H) break;  // the same in a head's lanes
-                    const int side = h >= p.Hq ? 1 : 0;
-                    float f[16];
-                    widen(v[j][0], f);
-                    widen(v[j][1], f + 8);
-                    if (p.w[side] != nullptr) {
-                        if (w_side != side) {
-                            const uint4* const at = reinterpret_cast<const uint4*>(p.w[side]);
-                            w[0] = __ldg(at + c0);
-                            w[1] = __ldg(at + c1);
-                            w_side = side;
-                        }
-                        float sum = 0.0f;
+                    uint64_t s = mul2(x[j][0], x[j][0]);
 #pragma unroll
-                        for (int z = 0; z < 16; ++z) sum = fmaf(f[z], f[z], sum);
+                    for (int z = 1; z < 4; ++z) s = fma2(x[j][z], x[j][z], s);
 #pragma unroll
-                        for (int s = 1; s < N; s <<= 1) sum += __shfl_xor_sync(mask, sum, s);
-                        const float r = rsqrtf(fmaf(sum, 1.0f / D, p.eps));
-                        float by[16];
-                        widen(w[0], by);
-                        widen(w[1], by + 8);
+                    for (int z = 0; z < 4; ++z) s = fma2(y[j][z], y[j][z], s);
+                    float a, b;
+                    unpack2(s, a, b);
+                    sum[j] = a + b;
+                }
 #pragma unroll
-                        for (int z = 0; z < 16; ++z) f[z] *= r * by[z];
+                for (int o = 1; o < N; o <<= 1)
+#pragma unroll
+                    for (int j = 0; j < kAtOnce; ++j) sum[j] += __shfl_xor_sync(mask, sum[j], o);
+#pragma unroll
+                for (int j = 0; j < kAtOnce; ++j) {
+                    const int side = h1 + j * step >= p.Hq ? 1 : 0;
+                    const float r = normed[side] ? rsqrtf(fmaf(sum[j], 1.0f / D, p.eps)) : 1.0f;
+                    const uint64_t rr = pack2(r, r);
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) {
+                        // Four weights: pairs 2 (z & 1) and the next of x or y, out of chunk 0 or 1.
+                        const bool of_y = kInter ? (z & 1) != 0 : z >= 2;
+                        const int first = kInter ? 2 * (z >> 1) : 2 * (z & 1);
+                        const int at = (z & 1) * (D / 2) + 4 * (z < 2 ? c0 : c1);
+                        const float4 w = *reinterpret_cast<const float4*>(&s_w[side][at]);
+                        uint64_t (&to)[4] = of_y ? y[j] : x[j];
+                        to[first] = mul2(mul2(to[first], rr), pack2(w.x, w.y));
+                        to[first + 1] = mul2(mul2(to[first + 1], rr), pack2(w.z, w.w));
                     }
-                    if (turns_here) {
+                }
+            }
 #pragma unroll
-                        for (int z = 0; z < 8; ++z) {
-                            const int a = kInter ? 2 * z : z, b = kInter ? 2 * z + 1 : z + 8;
-                            const float x = f[a], y = f[b];
-                            f[a] = fmaf(x, cs[z], -y * sn[z]);
-                            f[b] = fmaf(x, sn[z], y * cs[z]);
-                        }
+            for (int j = 0; j < kAtOnce; ++j) {
+                const int h = h1 + j * step, side = h >= p.Hq ? 1 : 0;
+                if (turns_here) {
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) {
+                        const uint64_t u = mul2(y[j][z], sn[z]), w = mul2(y[j][z], cs[z]);
+                        y[j][z] = fma2(x[j][z], sn[z], w);
+                        x[j][z] = fma2(x[j][z], cs[z], u ^ 0x8000000080000000ull);
                     }
+                }
+                if (h < p.H) {
                     uint4* const out = reinterpret_cast<uint4*>(
                         p.y[side] + t * p.y_stride[side] + static_cast<int64_t>(h - side * p.Hq) * D);
-                    out[c0] = narrow(f);
-                    out[c1] = narrow(f + 8);
+                    uint4 o0, o1;
+                    narrow<kInter>(x[j], y[j], o0, o1);
+                    out[c0] = o0;
+                    out[c1] = o1;
                 }
-                h0 += kAtOnce * step;
-                load(h0);
             }
         }
     }
 }
 
-template <int D>
+template <int D, int TB>
 int launch_rope(RopeParams p, bool inter, int sms, smd_stream_t stream) {
-    constexpr int kMany = 512 / D;  // tokens of a block whose angles are one a thread
-    const bool many = p.T >= 2 * sms * kMany;
-    const int groups = kThreads / (D / 16);
-    if (many) {
+    if (TB > 1) {
         p.slices = 1;
     } else {  // heads over blocks while SMs are idle
-        const int most = (p.H + groups - 1) / groups, want = 2 * sms / p.T;
+        constexpr int kUnits = kThreads / (D / 16);
+        const int most = (p.H + kUnits - 1) / kUnits, want = 2 * sms / p.T;
         p.slices = want < 1 ? 1 : want < most ? want : most;
     }
-    const int64_t chunks = many ? (p.T + kMany - 1) / kMany : p.T;
-    const int64_t most = static_cast<int64_t>(sms) * 8 / p.slices;
+    const int64_t chunks = (p.T + TB - 1) / TB, most = static_cast<int64_t>(sms) * 6 / p.slices;
     const unsigned grid = static_cast<unsigned>((chunks < most ? chunks : most) * p.slices);
-    auto kernel = many ? (inter ? qk_rope_kernel<D, kMany, true> : qk_rope_kernel<D, kMany, false>)
-                       : (inter ? qk_rope_kernel<D, 1, true> : qk_rope_kernel<D, 1, false>);
+    const bool norm = p.w[0] != nullptr || p.w[1] != nullptr;
+    auto kernel = norm ? (inter ? qk_rope_kernel<D, TB, true, true> : qk_rope_kernel<D, TB, false, true>)
+                       : (inter ? qk_rope_kernel<D, TB, true, false> : qk_rope_kernel<D, TB, false, false>);
     return launch_pdl(kernel, dim3(grid), kThreads, 0, stream, p);
+}
+
+template <int D>
+int launch_rope(const RopeParams& p, bool inter, int sms, smd_stream_t stream) {
+    constexpr int kMany = 512 / D;  // tokens whose angles are one a thread
+    if (p.T < 2 * sms) return launch_rope<D, 1>(p, inter, sms, stream);
+    return p.H >= 16 ? launch_rope<D, kMany>(p, inter, sms, stream)
+                     : launch_rope<D, 4 * kMany>(p, inter, sms, stream);
 }
 
 }  // namespace
