@@ -939,7 +939,11 @@ int64_t smd_paged4_workspace_bytes(const smd_paged4_cache_t* cache);
  * running maximum that they are taken from (and up to 2^15), 11 bits while within
  * 2^-21 of the largest, a bit less for each power of two below; the heads' powers are applied in fp32.
  * A row that sees a block whose scale is NaN gets NaN (of K: all of the row; of V:
- * the block's columns); scales of tokens that a row does not see never reach it. */
+ * the block's columns); scales of tokens that a row does not see never reach it. A query row
+ * with a NaN (at 128 columns with an infinity, too) gets NaN if it sees a token. At 128 columns a query
+ * value below 2^-8 of the largest of its 16 columns is taken to within 2^-16 of that (or of 2^-14 of the row's
+ * largest, where that is more); the others, and at other sizes all above 2^-28 of the row's largest, are
+ * exact. */
 int smd_paged4_decode(const uint16_t* q, int64_t q_stride, const smd_paged4_cache_t* cache,
                       const int32_t* table, int64_t table_stride, int32_t width,
                       const int32_t* lengths, int32_t R, int32_t row_group, int32_t Hq,

@@ -45,15 +45,13 @@ extern "C" int smd_paged4_decode_ex(const uint16_t* q, int64_t q_stride,
                           block_lists, block_counts, K, out, lse, status, workspace, workspace_bytes,
                           stream, force};
     return run_decode(call, shape_of(cache), p, [&](const PagedParams& p, int64_t tiles, int RT, int sms) {
-        // 128 columns: tcgen05 for more than 8 query rows, unless small pages make many copies of a
-        // tile's 128 tokens. 64 requests of 1024 .. 8192 tokens, tcgen05 / mma.sync in us, pages of 16, 32,
-        // 64, 128 tokens: 8 rows 100 / 84 (64); 16 rows 178 / 119, 123 / 111, 99 / 111, 92 / 111; 32 rows
-        // 198 / 179, 145 / 168, 126 / 167, 126 / 167.
-        const int box = tc_box_tokens(cache->page_size);
-        if (D == 128 && RT > 1 && box >= (RT == 2 ? 64 : 32)) {
+        // 128 columns: tcgen05. mma.sync (smd_paged_decode.cuh), measured in its place with 64 requests of
+        // 1024 .. 8192 tokens, tcgen05 / mma.sync in us: pages of 64 tokens, 8 / 16 / 32 query rows 74 / 84,
+        // 83 / 111, 117 / 167; pages of 16 88 / 92, 94 / 119, 135 / 179; one request of 777 tokens 12.6 / 11.3.
+        if (D == 128) {
             Maps<4> tc;
             std::memcpy(&tc, &cache->map[1 + sizeof maps / 8], sizeof tc);
-            return paged4_tc(p, tc, box, RT == 2 ? 16 : 32, sms, (tiles + 3) / 4, stream);
+            return paged4_tc(p, tc, tc_box_tokens(cache->page_size), 8 * RT, sms, (tiles + 3) / 4, stream);
         }
         const bool halves = page_box_tokens(cache->page_size, D) < (D == 256 ? 16 : 32);  // a tile spans two pages
         const auto launch = [&](auto shape) {
@@ -66,12 +64,6 @@ extern "C" int smd_paged4_decode_ex(const uint16_t* q, int64_t q_stride,
                  : RT == 1 ? launch(Shape<64, 1, 32, 1, 3, 3, 4>{})
                  : RT == 2 ? launch(Shape<64, 2, 32, 1, 3, 3, 4>{})
                            : launch(Shape<64, 4, 32, 1, 4, 2, 4>{});
-        if (D == 128)
-            return halves    ? (RT == 1   ? launch(Shape<128, 1, 32, 2, 3, 3, 4>{})
-                                : RT == 2 ? launch(Shape<128, 2, 32, 2, 3, 3, 4>{})
-                                          : launch(Shape<128, 4, 32, 2, 3, 2, 4>{}))
-                   : RT == 1 ? launch(Shape<128, 1, 32, 1, 3, 3, 4>{})
-                             : launch(Shape<128, 2, 32, 1, 3, 3, 4>{});
         return RT == 1 ? launch(Shape<256, 1, 16, 1, 3, 3, 4>{}) : launch(Shape<256, 2, 16, 1, 3, 2, 4>{});
     });
 }
