@@ -1299,16 +1299,15 @@ class PagedCache4:
         return cls(zeros(*codes), zeros(*codes), zeros(*scales), zeros(*scales), k_exp, v_exp, b)
 
 
-def _token_rows(t, name: str, T: int, heads: int, D: int, dev: int):
+def _token_rows(t, name: str, shape: tuple, bfloat16, dev: int):
     """Pointer and token stride of bfloat16 [T, heads, D] whose tokens may lie apart."""
-    import torch
-
-    if t.get_device() != dev or t.dtype != torch.bfloat16 or t.shape != (T, heads, D):
-        raise ValueError(f"{name} must be a bfloat16 tensor [{T}, {heads}, {D}] on cuda:{dev}")
-    steps = t.stride()
-    if steps[2] != 1 or (heads > 1 and steps[1] != D):
+    if t.get_device() != dev or t.dtype != bfloat16 or t.shape != shape:
+        raise ValueError(f"{name} must be a bfloat16 tensor {list(shape)} on cuda:{dev}")
+    token, head, column = t.stride()
+    T, heads, D = shape
+    if column != 1 or (heads > 1 and head != D):
         raise ValueError(f"{name}: a token's heads must be contiguous")
-    return t.data_ptr(), steps[0] if T > 1 else heads * D
+    return t.data_ptr(), token if T > 1 else heads * D
 
 
 def paged4_append(cache: PagedCache4, k, v, slots, stream=None) -> None:
@@ -1319,11 +1318,11 @@ def paged4_append(cache: PagedCache4, k, v, slots, stream=None) -> None:
 
     dev = cache.device
     _vector(slots, "slots", torch.int32, dev)
-    T = slots.numel()
+    T, bfloat16 = slots.numel(), torch.bfloat16
+    shape = (T, cache.heads, cache.head_dim)
     rc = _entry("smd_paged4_append", dev)(
-        cache.ref, *_token_rows(k, "k", T, cache.heads, cache.head_dim, dev),
-        *_token_rows(v, "v", T, cache.heads, cache.head_dim, dev), slots.data_ptr(), T,
-        _stream(stream, dev))
+        cache.ref, *_token_rows(k, "k", shape, bfloat16, dev), *_token_rows(v, "v", shape, bfloat16, dev),
+        slots.data_ptr(), T, _stream(stream, dev))
     if rc != SMD_OK:
         raise SmdError(rc, "smd_paged4_append")
 
@@ -1336,14 +1335,15 @@ def paged4_read(cache: PagedCache4, slots, k=None, v=None, stream=None):
 
     dev = cache.device
     _vector(slots, "slots", torch.int32, dev)
-    T, heads, D = slots.numel(), cache.heads, cache.head_dim
+    T, bfloat16 = slots.numel(), torch.bfloat16
+    shape = (T, cache.heads, cache.head_dim)
     if k is None:
-        k = _new(torch.zeros, stream, (T, heads, D), torch.bfloat16, slots.device)
+        k = _new(torch.zeros, stream, shape, bfloat16, slots.device)
     if v is None:
-        v = _new(torch.zeros, stream, (T, heads, D), torch.bfloat16, slots.device)
-    rc = _entry("smd_paged4_read", dev)(cache.ref, slots.data_ptr(), T,
-                                        *_token_rows(k, "k", T, heads, D, dev),
-                                        *_token_rows(v, "v", T, heads, D, dev), _stream(stream, dev))
+        v = _new(torch.zeros, stream, shape, bfloat16, slots.device)
+    rc = _entry("smd_paged4_read", dev)(
+        cache.ref, slots.data_ptr(), T, *_token_rows(k, "k", shape, bfloat16, dev),
+        *_token_rows(v, "v", shape, bfloat16, dev), _stream(stream, dev))
     if rc != SMD_OK:
         raise SmdError(rc, "smd_paged4_read")
     return k, v
@@ -1381,38 +1381,48 @@ def qk_norm_rope(q, k, positions, freqs, q_weight=None, k_weight=None, eps: floa
     dev = _gpu(q, "q")
     if q.dim() != 3:
         raise ValueError("q must be [T, Hq, head_dim]")
-    T, Hq, D = q.shape
-    Hk = 0 if k is None else k.shape[1]
-    args = (*_token_rows(q, "q", T, Hq, D, dev),
-            *(_token_rows(k, "k", T, Hk, D, dev) if k is not None else (0, 0)))
+    bfloat16 = torch.bfloat16
+    q_shape = tuple(q.shape)
+    T, Hq, D = q_shape
+    if k is not None:
+        Hk = k.shape[1]
+        k_shape = (T, Hk, D)
+        k_args = _token_rows(k, "k", k_shape, bfloat16, dev)
+    elif k_out is None:
+        Hk, k_args = 0, (0, 0)
+    else:
+        raise ValueError("k_out without k")
     if (positions is None) != (freqs is None):
         raise ValueError("positions and freqs go together")
     axes, rot, pos_ptr, pos_step, f_ptr = 1, 0, 0, 0, 0
     if positions is not None:
-        if positions.get_device() != dev or positions.dtype != torch.int32 or positions.dim() not in (1, 2) \
-                or positions.shape[-1] != T or (T > 1 and positions.stride(-1) != 1):
+        steps, shape = positions.stride(), positions.shape
+        if positions.get_device() != dev or positions.dtype != torch.int32 or len(shape) not in (1, 2) \
+                or shape[-1] != T or (T > 1 and steps[-1] != 1):
             raise ValueError(f"positions must be an int32 tensor [{T}] or [axes, {T}] on cuda:{dev} with "
                              "contiguous rows")
-        axes = positions.shape[0] if positions.dim() == 2 else 1
-        pos_ptr, pos_step = positions.data_ptr(), positions.stride(0) if axes > 1 else T
+        pos_ptr, pos_step = positions.data_ptr(), T
+        if len(shape) == 2:
+            axes = shape[0]
+            if axes > 1:
+                pos_step = steps[0]
         _vector(freqs, "freqs", torch.float32, dev)
-        if freqs.dim() != positions.dim() or (freqs.dim() == 2 and freqs.shape[0] != axes):
+        f_shape = freqs.shape
+        if len(f_shape) != len(shape) or (len(f_shape) == 2 and f_shape[0] != axes):
             raise ValueError("freqs must be [rot / 2] or [axes, rot / 2], as positions")
-        rot, f_ptr = 2 * freqs.shape[-1], freqs.data_ptr()
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        rot, f_ptr = 2 * f_shape[-1], freqs.data_ptr()
+    for w in (q_weight, k_weight):
         if w is not None:
-            _vector(w, name, torch.bfloat16, dev)
+            _vector(w, "q_weight" if w is q_weight else "k_weight", bfloat16, dev)
             if w.numel() != D:
-                raise ValueError(f"{name} must have {D} elements")
+                raise ValueError(f"{'q_weight' if w is q_weight else 'k_weight'} must have {D} elements")
     if q_out is None:
-        q_out = _new(torch.zeros, stream, (T, Hq, D), torch.bfloat16, q.device)
-    if k is None:
-        if k_out is not None:
-            raise ValueError("k_out without k")
-    elif k_out is None:
-        k_out = _new(torch.zeros, stream, (T, Hk, D), torch.bfloat16, q.device)
-    out = (*_token_rows(q_out, "q_out", T, Hq, D, dev),
-           *(_token_rows(k_out, "k_out", T, Hk, D, dev) if k is not None else (0, 0)))
+        q_out = _new(torch.zeros, stream, q_shape, bfloat16, q.device)
+    if k is not None and k_out is None:
+        k_out = _new(torch.zeros, stream, k_shape, bfloat16, q.device)
+    args = (*_token_rows(q, "q", q_shape, bfloat16, dev), *k_args)
+    out = (*_token_rows(q_out, "q_out", q_shape, bfloat16, dev),
+           *(_token_rows(k_out, "k_out", k_shape, bfloat16, dev) if k is not None else k_args))
     rc = _entry("smd_qk_norm_rope", dev)(*args, T, Hq, Hk, D, pos_ptr, pos_step, axes, f_ptr, rot,
                                          int(bool(interleaved)), _ptr(q_weight), _ptr(k_weight), eps,
                                          *out, _stream(stream, dev))
@@ -1421,16 +1431,14 @@ def qk_norm_rope(q, k, positions, freqs, q_weight=None, k_weight=None, eps: floa
     return q_out, k_out
 
 
-def _probability_rows(t, name: str, rows: tuple, dev: int):
+def _probability_rows(t, name: str, shape: tuple, float32, dev: int):
     """Pointer and row stride of float32 [R, n, V] whose rows are evenly spaced."""
-    import torch
-
-    if t.get_device() != dev or t.dtype != torch.float32 or t.dim() != 3 or tuple(t.shape[:2]) != rows:
-        raise ValueError(f"{name} must be a float32 tensor [{rows[0]}, {rows[1]}, V] on cuda:{dev}")
-    (R, n, V), steps = t.shape, t.stride()
-    if V > 1 and steps[2] != 1 or (R > 1 and n > 1 and steps[0] != n * steps[1]):
+    if t.get_device() != dev or t.dtype != float32 or t.shape != shape:
+        raise ValueError(f"{name} must be a float32 tensor {list(shape)} on cuda:{dev}")
+    (R, n, V), (request, row, column) = shape, t.stride()
+    if V > 1 and column != 1 or (R > 1 and n > 1 and request != n * row):
         raise ValueError(f"{name}: rows must be contiguous and evenly spaced")
-    return t.data_ptr(), steps[1] if n > 1 else steps[0] if R > 1 else V
+    return t.data_ptr(), row if n > 1 else request if R > 1 else V
 
 
 def verify_drafts(target, tokens, accept, sample, draft=None, out_tokens=None, accepted=None,
@@ -1447,16 +1455,15 @@ def verify_drafts(target, tokens, accept, sample, draft=None, out_tokens=None, a
     dev = _gpu(target, "target")
     if target.dim() != 3:
         raise ValueError("target must be [R, G, V]")
-    R, G, V = target.shape
-    args = _probability_rows(target, "target", (R, G), dev)
-    _vector(sample, "sample", torch.float32, dev, R)
+    shape, float32 = tuple(target.shape), torch.float32
+    R, G, V = shape
+    args = _probability_rows(target, "target", shape, float32, dev)
+    _vector(sample, "sample", float32, dev, R)
     _vector(tokens, "tokens", torch.int32, dev, R * (G - 1))
-    _vector(accept, "accept", torch.float32, dev, R * (G - 1))
+    _vector(accept, "accept", float32, dev, R * (G - 1))
     draft_args = (0, 0)
     if draft is not None:
-        draft_args = _probability_rows(draft, "draft", (R, G - 1), dev)
-        if draft.shape[2] != V:
-            raise ValueError(f"draft must be [{R}, {G - 1}, {V}]")
+        draft_args = _probability_rows(draft, "draft", (R, G - 1, V), float32, dev)
     if out_tokens is None:
         out_tokens = _new(torch.empty, stream, (R, G), torch.int32, target.device)
     else:
