@@ -965,7 +965,9 @@ int smd_paged4_decode_ex(const uint16_t* q, int64_t q_stride, const smd_paged4_c
  *   angle_j = sum over axes a of positions[a][t] * freqs[a][j],   j < rot / 2
  *   (y_u, y_v) -> (y_u cos - y_v sin, y_u sin + y_v cos) with u = j, v = j + rot / 2,
  *            or u = 2 j, v = 2 j + 1 where `interleaved`; columns from rot on stay y
- * rounded to bfloat16 once. Sums and products are fp32; an axis' angle is taken modulo a turn
+ * rounded to bfloat16 once. Sums and products are fp32 (a head whose squares add up to what that type
+ * does not hold, values of 2^60 and more, or of 2^-60 and less under an eps of next to nothing, comes out
+ * as that arithmetic gives it); an axis' angle is taken modulo a turn
  * in 64-bit fixed point, right to 2^-20 of a turn for every position and frequency (to 2^-30 for
  * frequencies up to 1).
  *   q, k     [T, Hq, head_dim], [T, Hk, head_dim] bfloat16; token t starts at

@@ -276,9 +276,15 @@ int launch_rope(RopeParams p, bool inter, int sms, smd_stream_t stream) {
 template <int D>
 int launch_rope(const RopeParams& p, bool inter, int sms, smd_stream_t stream) {
     constexpr int kMany = 512 / D;  // tokens whose angles are one a thread
+    // Tokens of a block: one while SMs would idle, and, for few heads, four times as many once there are
+    // enough for all SMs (the angles are most of the work then). 128 columns, 1 / kMany / 4 kMany in us:
+    //   72 heads, 300 / 600 / 14000 tokens     4.4 / 5.1 / 18.8     7.0 / 6.3 / 23.1     104 / 81 / 99
+    //   24 heads, 300 / 600 / 14000            3.1 / 3.1 /  8.2     4.8 / 3.7 /  8.2      47 / 35 / 37
+    //   16 heads, 300 / 600 / 14000            2.7 / 3.1 /  6.4     4.4 / 3.6 /  6.4      41 / 31 / 27
+    //    5 heads, 300 / 2000 / 14000           2.6 / 2.9 /  4.2     7.1 / 6.0 /  5.3      35 / 27 / 12
     if (p.T < 2 * sms) return launch_rope<D, 1>(p, inter, sms, stream);
-    return p.H >= 16 ? launch_rope<D, kMany>(p, inter, sms, stream)
-                     : launch_rope<D, 4 * kMany>(p, inter, sms, stream);
+    return p.H >= 20 || p.T < 8 * kMany * sms ? launch_rope<D, kMany>(p, inter, sms, stream)
+                                              : launch_rope<D, 4 * kMany>(p, inter, sms, stream);
 }
 
 }  // namespace

@@ -170,3 +170,14 @@ def test_many_heads_another_stream_and_a_graph(cuda):
     torch.cuda.synchronize()
     check(buf[0], q, None, 0, pos, f, False)
     check(buf[1], k, None, 0, pos, f, False)
+
+
+@pytest.mark.parametrize("T,Hq,Hk,D,rot,axes,inter,norm", [
+    (5000, 3, 1, 128, 32, 2, False, True), (9800, 2, 1, 64, 16, 1, True, False), (2501, 2, 1, 256, 16, 3, False, True),
+    (4900, 19, 0, 128, 16, 1, True, True), (4900, 18, 2, 128, 16, 1, False, True)])
+def test_many_tokens_of_few_heads(cuda, T, Hq, Hk, D, rot, axes, inter, norm):
+    test_sizes_pairs_and_axes(cuda, T, Hq, Hk, D, rot, axes, inter, norm)
+
+
+def test_negative_positions_among_many_tokens_of_few_heads(cuda):
+    test_tokens_with_negative_positions_are_left_alone_also_in_place(cuda, 9800)
