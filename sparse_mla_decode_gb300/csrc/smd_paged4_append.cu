@@ -23,8 +23,9 @@
 // Measured (GB300, device time): 96 tokens of as many requests, 8 heads of 128 columns, 2.6 us (1.8
 // without bounds); 28 thousand tokens of 23 requests 35 us, 63% of the copy rate for the 146 MB (27
 // without bounds, 80%: the bounds read the keys again from L2 and follow the codes), 256 columns 62 (71%),
-// 64 columns in pages of 16 29 (38%). Read: 96 tokens 2.0 us, 28 thousand 31.5 (69%: conversions, 4 heads
-// on their way in a lane). Tried for the bounds: blocks of their own beside those of the codes 36 us, behind them
+// 64 columns in pages of 16 29 (38%). Read: 96 tokens 2.1 us, 28 thousand 24.9 (88%;
+// 256 columns 94%; stores of 16 bytes, two a lane, 30.7, so too where rows are 16 bytes off). Tried for
+// the append: loads of 32 bytes (36). For its bounds: blocks of their own beside those of the codes 36 us, behind them
 // 44 (the keys have left L2), keys kept in shared memory 41.
 #include "smd_internal.h"
 #include "smd_paged.h"
@@ -37,7 +38,8 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kChunk = 64;      // tokens of a block, where they are many
 constexpr int kMostPage = 256;  // tokens of a page
-constexpr int kAtOnce = 4;      // loads of a lane in flight
+constexpr int kAtOnce = 4;      // loads of a lane in flight (append)
+constexpr int kHeads = 8;       // heads of a lane in flight (read; 4: 5 to 10% slower up to 4000 tokens)
 
 struct Append4Params {
     const uint16_t* x[2];
@@ -351,7 +353,20 @@ struct Read4Params {
     int32_t pages, heads, P;
     int32_t first, sides;  // the first side that is read, and how many
     int32_t shares;        // units that share a token's heads
+    bool wide;             // rows are 32-byte aligned
 };
+
+// 32 bytes in one store (wide: 32-byte aligned) or two, each of which is half a sector a lane.
+__device__ __forceinline__ void store32(uint16_t* to, bool wide, const uint32_t (&w)[8]) {
+    if (wide) {
+        asm volatile("st.global.cs.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(w[0]),
+                     "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        __stcs(reinterpret_cast<uint4*>(to), make_uint4(w[0], w[1], w[2], w[3]));
+        __stcs(reinterpret_cast<uint4*>(to) + 1, make_uint4(w[4], w[5], w[6], w[7]));
+    }
+}
 
 // D / 16 lanes for each (token, side) and share of the heads: a block of 16 columns each.
 template <int D>
@@ -371,11 +386,11 @@ __global__ void __launch_bounds__(kThreads) read4_kernel(const Read4Params p) {
         p.scales[side] + (static_cast<int64_t>(page) * p.heads * p.P + o) * (D / 16) + i;
     uint16_t* const out = p.out[side] + t * p.out_stride[side] + 16 * i;
 #pragma unroll 1
-    for (int h0 = static_cast<int>(unit % p.shares); h0 < p.heads; h0 += kAtOnce * p.shares) {
-        uint2 codes[kAtOnce];
-        uint32_t scale[kAtOnce];
+    for (int h0 = static_cast<int>(unit % p.shares); h0 < p.heads; h0 += kHeads * p.shares) {
+        uint2 codes[kHeads];
+        uint32_t scale[kHeads];
 #pragma unroll
-        for (int j = 0; j < kAtOnce; ++j) {
+        for (int j = 0; j < kHeads; ++j) {
             const int h = h0 + j * p.shares;
             if (h < p.heads) {
                 codes[j] = __ldg(reinterpret_cast<const uint2*>(pool + h * st[1]));
@@ -383,7 +398,7 @@ __global__ void __launch_bounds__(kThreads) read4_kernel(const Read4Params p) {
             }
         }
 #pragma unroll
-        for (int j = 0; j < kAtOnce; ++j) {
+        for (int j = 0; j < kHeads; ++j) {
             const int h = h0 + j * p.shares;
             if (h >= p.heads) break;
             const float up = power(p.exps[side], h, 1);
@@ -406,9 +421,7 @@ __global__ void __launch_bounds__(kThreads) read4_kernel(const Read4Params p) {
                     : "r"(w[z]));
                 w[z] = bf16x2(a * up, b * up);
             }
-            uint4* const to = reinterpret_cast<uint4*>(out + h * D);
-            __stcs(to, make_uint4(w[0], w[1], w[2], w[3]));
-            __stcs(to + 1, make_uint4(w[4], w[5], w[6], w[7]));
+            store32(out + h * D, p.wide, w);
         }
     }
 }
@@ -436,7 +449,7 @@ int launch_append(const Append4Params& p, int sms, smd_stream_t stream) {
 
 template <int D>
 int launch_read(Read4Params p, int sms, smd_stream_t stream) {
-    // A token's heads go to one unit, kAtOnce at a time, unless that leaves SMs without work (96
+    // A token's heads go to one unit, kHeads at a time, unless that leaves SMs without work (96
     // tokens of 8 heads: 2.6 us by one unit or two, 1.8 by eight).
     const int64_t units = static_cast<int64_t>(p.T) * p.sides, want = static_cast<int64_t>(sms) * 2 * kThreads / (D / 16);
     const int64_t shares = (want + units - 1) / units;
@@ -519,6 +532,8 @@ extern "C" int smd_paged4_read(const smd_paged4_cache_t* cache, const int32_t* s
     p.out[1] = v;
     p.out_stride[0] = k_stride;
     p.out_stride[1] = v_stride;
+    p.wide = (k == nullptr || (aligned(k, 32) && k_stride % 16 == 0)) &&
+             (v == nullptr || (aligned(v, 32) && v_stride % 16 == 0));
     p.pages = cache->pages;
     p.heads = cache->heads;
     p.P = cache->page_size;

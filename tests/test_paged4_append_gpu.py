@@ -227,3 +227,29 @@ def test_a_pool_past_32_bit_offsets_and_a_graph(cuda):
     for t in out:
         assert np.array_equal(t.float().cpu().numpy().astype(np.float64), want.reshape(5, heads, D))
     assert int((c.k[:-1] != 0).sum()) == 0
+
+
+@pytest.mark.parametrize("D,heads,T", [(64, 3, 40), (128, 9, 300), (256, 1, 700), (128, 17, 5)])
+@pytest.mark.parametrize("off", [0, 8, 16, 24])
+def test_rows_read_to_every_alignment(cuda, D, heads, T, off):
+    """The same bits, and nothing beside the rows, whether rows lie 16 or 32 bytes apart from a sector."""
+    import torch
+    from sparse_mla_decode_gb300 import binding
+    rng = np.random.default_rng(D + heads)
+    cache = Cache4(8, -(-T // 32) + 1, heads, 32, D)
+    c = cache.to(cuda)
+    slots = rng.permutation(cache.pages * 32)[:T]
+    slots[T // 2] = -1
+    want = binding.paged4_read(c, i32(slots, cuda))
+    row = heads * D
+    for step in (row, row + 8, row + 16):
+        flat = [torch.full((T * step + 32,), 3.0, dtype=torch.bfloat16, device=cuda) for _ in "kv"]
+        out = [x[off:].as_strided((T, heads, D), (step, D, 1)) for x in flat]
+        binding.paged4_read(c, i32(slots, cuda), *out)
+        torch.cuda.synchronize()
+        for x, o, w in zip(flat, out, want):
+            keep = torch.ones(T, dtype=torch.bool, device=cuda)
+            keep[T // 2] = False
+            assert torch.equal(o[keep], w[keep]) and bool((o[~keep] == 3.0).all())
+            o.fill_(3.0)
+            assert bool((x == 3.0).all())
