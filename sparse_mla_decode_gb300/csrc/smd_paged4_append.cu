@@ -165,7 +165,10 @@ __device__ __forceinline__ void run_bounds(const Append4Params& p, int64_t t, in
     if (o > 0) was.read(bounds, D, 8 * i);
     uint32_t hi[4], lo[4];
     nothing_met(hi, lo);
-    scan_keys<4>(p.x[0] + t * p.x_stride[0] + head * D + 8 * i, p.x_stride[0], n, 1, hi, lo);
+    const uint16_t* const x = p.x[0] + t * p.x_stride[0] + head * D + 8 * i;
+    // Of a page's 64 keys 8 at a time; 4: 500 tokens of a request 8.0 us instead of 6.9.
+    if (n <= 2) scan_keys<2>(x, p.x_stride[0], n, 1, hi, lo);
+    else scan_keys<8>(x, p.x_stride[0], n, 1, hi, lo);
     write_bounds(bounds, D, 8 * i, was, hi, lo);
 }
 
@@ -430,12 +433,12 @@ template <int D>
 int launch_append(const Append4Params& p, int sms, smd_stream_t stream) {
     // Few tokens: lanes for each. Many: blocks by chunks of tokens. Few / many in us, 8 heads of 128
     // columns, pages of 64 (in brackets without bounds):
-    //   96 tokens of as many requests   2.6 /  8.3  ( 1.8 /  4.3)
-    //   3000 of as many                 7.4 / 13.5  ( 4.7 /  6.7)
-    //   8000 of as many                19.7 / 20.5  (10.1 /  9.7)
-    //   500 of one                      8.0 /  6.3  ( 2.3 /  4.3)
-    //   4000 of one, of 30             11.5 / 10.4, 11.7  ( 5.7 /  8.2)
-    //   16000 of one                   28.3 / 19.8  (18.9 / 15.2)
+    //   96 tokens of as many requests   2.7 /  8.3  ( 1.8 /  4.3)
+    //   3000 of as many                 7.4 / 13.5  ( 5.0 /  6.7)
+    //   8000 of as many                22.3 / 20.8  (10.9 /  9.7)
+    //   500 of one                      6.9 /  6.3  ( 2.2 /  4.3)
+    //   4000 of one, of 30             10.9 / 10.4, 11.7  ( 6.1 /  8.2)
+    //   16000 of one                   30.3 / 19.8  (21.8 / 15.3)
     const int64_t units = static_cast<int64_t>(p.T) * p.heads;
     if (units <= static_cast<int64_t>(sms) * 384)
         return launch_pdl(append4_few_kernel<D>,
