@@ -892,7 +892,7 @@ typedef struct {
     int32_t heads;
     int32_t page_size;
     int32_t head_dim;
-    uint64_t map[132];
+    uint64_t map[68];
 } smd_paged4_cache_t;
 
 /* Checks the description and fills in `map`. Host only. Returns SMD_OK,

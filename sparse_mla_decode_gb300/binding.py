@@ -78,7 +78,7 @@ class SmdPagedCache4(ctypes.Structure):
                 ("k_stride", ctypes.c_int64 * 3), ("v_stride", ctypes.c_int64 * 3),
                 ("pages", ctypes.c_int32), ("heads", ctypes.c_int32),
                 ("page_size", ctypes.c_int32), ("head_dim", ctypes.c_int32),
-                ("map", ctypes.c_uint64 * 132)]
+                ("map", ctypes.c_uint64 * 68)]
 
 
 class SmdError(RuntimeError):

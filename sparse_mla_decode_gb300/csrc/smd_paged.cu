@@ -170,17 +170,15 @@ extern "C" int smd_paged4_cache_init(smd_paged4_cache_t* c) {
         !aligned(c->v, 16) || !aligned(c->k_scales, 16) || !aligned(c->v_scales, 16) ||
         !aligned(c->k_exp, 4) || !aligned(c->v_exp, 4) || !aligned(c->bounds, 16))
         return SMD_ERR_ALIGN;
-    CUtensorMap maps[8] = {};
+    CUtensorMap maps[4];
     const CacheShape shape = shape_of(c);
-    for (int i = 0; i < (c->head_dim == 128 ? 2 : 1); ++i) {
-        const int box = i == 1 ? tc_box_tokens(c->page_size) : page_box_tokens(c->page_size, c->head_dim);
-        CUtensorMap* const m = maps + 4 * i;
-        if (!encode_codes(&m[0], c->k, c->k_stride, c->head_dim / 2, box, shape) ||
-            !encode_codes(&m[1], c->v, c->v_stride, c->head_dim / 2, box, shape) ||
-            !encode_scales(&m[2], c->k_scales, i == 1 ? 8 : 1, box, shape) ||
-            !encode_scales(&m[3], c->v_scales, i == 1 ? 8 : 1, box, shape))
-            return SMD_ERR_DEVICE;
-    }
+    const bool tc = c->head_dim == 128;
+    const int box = tc ? tc_box_tokens(c->page_size) : page_box_tokens(c->page_size, c->head_dim);
+    if (!encode_codes(&maps[0], c->k, c->k_stride, c->head_dim / 2, box, shape) ||
+        !encode_codes(&maps[1], c->v, c->v_stride, c->head_dim / 2, box, shape) ||
+        !encode_scales(&maps[2], c->k_scales, tc ? 8 : 1, box, shape) ||
+        !encode_scales(&maps[3], c->v_scales, tc ? 8 : 1, box, shape))
+        return SMD_ERR_DEVICE;
     std::memcpy(&c->map[1], maps, sizeof maps);
     c->map[0] = kPaged4Mark;
     return SMD_OK;

@@ -21,7 +21,7 @@ constexpr int kPagedMaxHeads = 128;  // query heads of a kv head
 // for the tcgen05 kernel.
 constexpr uint64_t kPagedMark = 0x736d645061676564ull, kPaged4Mark = 0x736d645061673465ull;
 static_assert(sizeof(CUtensorMap) == 128, "two maps and the mark fit smd_paged_cache_t::map");
-static_assert(sizeof(smd_paged4_cache_t::map) >= 8 * sizeof(CUtensorMap) + 8, "eight maps and the mark");
+static_assert(sizeof(smd_paged4_cache_t::map) >= 4 * sizeof(CUtensorMap) + 8, "four maps and the mark");
 
 inline bool paged_ready(const smd_paged_cache_t* c) { return c->map[0] == kPagedMark; }
 inline bool paged_ready(const smd_paged4_cache_t* c) { return c->map[0] == kPaged4Mark; }
