@@ -35,7 +35,7 @@
 //   the same with pages of 16 tokens, 8 / 16 / 32 rows           89 us / 94 us / 124 us
 //   64 listed pages in each of 64 requests, 8 / 16 / 32 rows     69 us 66% / 78 us 59% / 109 us 43%
 //   16 requests up to 65536 tokens, 8 / 16 / 32 rows             111 us 83% / 121 us 76% / 172 us 54%
-//   200 requests up to 300 tokens, 8 / 16 / 32 rows              32 us / 39 us / 63 us
+//   200 requests up to 300 tokens, 8 / 16 / 32 rows              29 us / 36 us / 57 us
 //   one request of 777 tokens, 8 / 16 / 32 rows                  12.6 us / 14.5 us / 17.5 us
 // At 8 rows instructions are issued in 59% of the cycles and the logic pipe is busy for 47% (V's
 // conversions are most of it); copies alone take 68 us of the 74. Start and joins are some 12 us, as in
@@ -310,6 +310,7 @@ __global__ void __launch_bounds__(S::threads, 1)
         const int c = static_cast<int>(at), e = find(c, S::unit_cost);
         const int nt = (prefix[e + 1] - prefix[e]) / p.x_units;
         const int rem = c - prefix[e] - S::unit_cost * p.x_units * e, x = rem / (nt + S::unit_cost);
+        if (uncut(nt, per)) return prefix[e] + x * nt;
         return prefix[e] + x * nt + max(rem - x * (nt + S::unit_cost) - S::unit_cost, 0);
     };
     // The workers' ranges: where one ends the next begins. Lane w has worker w's.

@@ -589,6 +589,13 @@ __device__ __forceinline__ void join_units(const PagedParams& p, uint32_t base, 
     }
 }
 
+// Whether a cut inside a unit of nt tiles moves to its begin, `per` being what a worker has: a join costs
+// more than a few tiles. 4-bit caches, no unit / up to 4 tiles / per / 6, too, in us: 5 requests of 33 to 64
+// tokens, 64 columns 11.3 / 8.8 / 8.8; 128 columns, 20 requests up to 600 tokens, 8 / 32 rows 14.7 / 13.0 / 13.0,
+// 22.3 / 18.2 / 18.2; 200 up to 300 32 / 29 / 29, 63 / 57 / 57; 500 up to 1000 - / 94 / 90, - / 213 / 204 (per / 2: 64 of
+// 1024 to 8192 81 for 74). (Results of E4M3 caches keep their bits: their cuts stay.)
+__device__ __forceinline__ bool uncut(int nt, int per) { return nt <= max(4, per / 6); }
+
 // Prefix sums of the entries' tiles of KT tokens: at least one for each unit, so that one without
 // tokens still writes its zeros. prefix [entries + 1], lens [entries], scan [warps]; the total.
 template <int KT, int THREADS>
@@ -705,6 +712,7 @@ __global__ void __launch_bounds__(kThreads, S::CTAS)
         const int c = static_cast<int>(at), e = find(c, kUnitCost);
         const int nt = (prefix[e + 1] - prefix[e]) / p.x_units;
         const int rem = c - prefix[e] - kUnitCost * p.x_units * e, x = rem / (nt + kUnitCost);
+        if (B4 && uncut(nt, per)) return prefix[e] + x * nt;
         return prefix[e] + x * nt + max(rem - x * (nt + kUnitCost) - kUnitCost, 0);
     };
     const int cut = tiles_before(static_cast<int64_t>(worker + (lane & 1)) * per);
