@@ -108,18 +108,6 @@ __device__ __forceinline__ bool worker_and(int id, bool v) {
 
 __device__ __forceinline__ bool worker_or(int id, bool v) { return !worker_and(id, !v); }
 
-// Whether phase `parity` of a barrier is complete; does not wait.
-__device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
 __device__ __forceinline__ uint32_t lds_volatile(uint32_t addr) {
     uint32_t v;
     asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
@@ -358,7 +346,7 @@ __global__ void __launch_bounds__(S::threads, 1)
             const int i = kk & (at_once - 1), s = kk % ST;
             if (i == 0) look(kk + mine);
             // The worker's waits are bounded, and the last that runs out stops this.
-            while (run && kk >= ST && !mbar_poll(bar_of(wk, kEmpty + s), (kk / ST - 1) & 1))
+            while (run && kk >= ST && !mbar_test(bar_of(wk, kEmpty + s), (kk / ST - 1) & 1))
                 run = lds_volatile(range_at + 4 * wk) == 0;
             run = __all_sync(0xffffffffu, run);
             if (!run) break;
