@@ -31,14 +31,14 @@
 // accumulators in tensor memory then come down by 2^(old - new)).
 //
 // Measured (GB300, device time; of the rate at which the GPU copies), pages of 64 tokens:
-//   64 requests of 1024 .. 8192 tokens, 8 / 16 / 32 / 64 rows    74 us 70% / 83 us 63% / 117 us 45% / 210 us 25%
+//   64 requests of 1024 .. 8192 tokens, 8 / 16 / 32 / 64 rows    73 us 70% / 82 us 63% / 115 us 45% / 208 us 26%
 //   the same with pages of 16 tokens, 8 / 16 / 32 rows           89 us / 94 us / 124 us
-//   64 listed pages in each of 64 requests, 8 / 16 / 32 rows     69 us 66% / 78 us 59% / 109 us 43%
-//   16 requests up to 65536 tokens, 8 / 16 / 32 rows             111 us 83% / 121 us 76% / 172 us 54%
+//   64 listed pages in each of 64 requests, 8 / 16 / 32 rows     69 us 66% / 78 us 59% / 108 us 43%
+//   16 requests up to 65536 tokens, 8 / 16 / 32 rows             110 us 83% / 121 us 76% / 170 us 54%
 //   200 requests up to 300 tokens, 8 / 16 / 32 rows              29 us / 36 us / 57 us
 //   one request of 777 tokens, 8 / 16 / 32 rows                  12.6 us / 14.5 us / 17.5 us
 // At 8 rows instructions are issued in 59% of the cycles and the logic pipe is busy for 47% (V's
-// conversions are most of it); copies alone take 68 us of the 74. Start and joins are some 12 us, as in
+// conversions are most of it); copies alone take 68 us of the 73. Start and joins are some 12 us, as in
 // smd_paged_decode.cu. At 32 rows three workers wait for one another's chains (51% of the issue slots).
 #include "smd_paged4_tc.h"
 
