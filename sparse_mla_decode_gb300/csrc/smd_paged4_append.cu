@@ -38,6 +38,7 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kChunk = 64;      // tokens of a block, where they are many
 constexpr int kMostPage = 256;  // tokens of a page
+constexpr int kFewUnits = 384;  // (token, head) pairs an SM up to which tokens count as few
 constexpr int kAtOnce = 4;      // loads of a lane in flight (append)
 constexpr int kHeads = 8;       // heads of a lane in flight (read; 4: 5 to 10% slower up to 4000 tokens)
 
@@ -440,7 +441,7 @@ int launch_append(const Append4Params& p, int sms, smd_stream_t stream) {
     //   4000 of one, of 30             10.9 / 10.4, 11.7  ( 6.1 /  8.2)
     //   16000 of one                   30.3 / 19.8  (21.8 / 15.3)
     const int64_t units = static_cast<int64_t>(p.T) * p.heads;
-    if (units <= static_cast<int64_t>(sms) * 384)
+    if (units <= static_cast<int64_t>(sms) * kFewUnits)
         return launch_pdl(append4_few_kernel<D>,
                           dim3(static_cast<unsigned>((units * (D / 8) + kThreads - 1) / kThreads)),
                           kThreads, 0, stream, p);
