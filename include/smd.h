@@ -1015,7 +1015,10 @@ int smd_qk_norm_rope(const uint16_t* q, int64_t q_stride, const uint16_t* k, int
  *            [0, 1).  (tokens and accept may be NULL where G = 1.)
  *   out_tokens  [R, G] int32: the a tokens that stay, the drawn one, then -1.
  *   accepted    [R] int32: a.   rejected  [R] int32: G - 1 - a, what smd_block_trim takes
- *            off the request's cache. Either may be NULL.
+ *            off a request that was given slots for all G tokens, those behind the end of its
+ *            drafts among them. One that was given n < G has n - 1 - a to take off, and one that
+ *            was given none (idle, or refused by smd_block_tables) nothing: taking `rejected` off
+ *            it would take tokens that it held before. Either may be NULL.
  * Bounds (SMD_ERR_SHAPE): R >= 0, 1 <= G <= 64, 1 <= V <= 2^22, strides >= V, R * G < 2^31.
  * Pointers are 4-byte aligned; rows of 16-byte steps are read faster.
  * Returns SMD_OK, SMD_ERR_NULL, SMD_ERR_SHAPE, SMD_ERR_ALIGN, SMD_ERR_DEVICE,

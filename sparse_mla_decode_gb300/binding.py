@@ -1448,8 +1448,9 @@ def verify_drafts(target, tokens, accept, sample, draft=None, out_tokens=None, a
     [R, G - 1] int32: the drafted ones (one outside the vocabulary ends a request's drafts); accept
     [R, G - 1] and sample [R] float32: random numbers from [0, 1); draft [R, G - 1, V] float32: what the
     drafted tokens were drawn from, or None (each was the only choice). Returns (out_tokens [R, G]: the
-    tokens that stay, the one drawn after them, then -1; accepted [R]; rejected [R], which block_trim takes
-    off), int32."""
+    tokens that stay, the one drawn after them, then -1; accepted [R]; rejected [R]: G - 1 - accepted, which
+    block_trim takes off requests that were granted G slots; of n < G granted ones it is n - 1 - accepted, and
+    nothing of none, as after a refusal of block_tables), int32."""
     import torch
 
     dev = _gpu(target, "target")

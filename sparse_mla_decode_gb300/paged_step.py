@@ -87,11 +87,16 @@ class PagedStep:
 
     def keep(self, target, tokens, accept, sample, draft=None):
         """Verification of the last G - 1 tokens that each request was granted (verify_drafts' arguments);
-        those that are refused come off, and their pages go back. Returns (out_tokens, accepted)."""
+        those that are refused come off, and their pages go back. A request that the last grant gave n < G tokens
+        has n - 1 drafts (tokens outside the vocabulary behind them); one that it gave none (idle, refused or
+        ended) keeps what it holds, and its results mean nothing. Returns (out_tokens, accepted)."""
         from . import binding
 
         a, b = self.now, 1 - self.now
         out, accepted, rejected = binding.verify_drafts(target, tokens, accept, sample, draft=draft)
+        # `rejected` counts G - 1 drafts for every request. Those that a request was not granted (its length
+        # grew by less than G over the grant) hold no slots; a drop below 0 takes nothing.
+        rejected += (self.lengths[a] - self.lengths[b]).sub_(target.shape[1]).clamp_(max=0)
         binding.block_trim(self.lengths[a], rejected, self.table, self.ring, self.state[a],
                            self.cache.page_size, new_lengths=self.lengths[b], new_state=self.state[b])
         self.now = b
