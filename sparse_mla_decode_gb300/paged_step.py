@@ -134,20 +134,28 @@ def main(argv=None) -> int:
     def random(n, h):
         return torch.randn(n, h, D, generator=g, device="cuda").bfloat16()
 
+    freqs = torch.exp(torch.arange(D // 2, device="cuda") * (-2 / D * math.log(10000.0)))
+    weight = torch.ones(D, dtype=torch.bfloat16, device="cuda")
+
+    def turn(q, k, positions):
+        """What is asked with and written: as given in 8 bits, normed and rotated in 4."""
+        if args.bits == 8:
+            return q, k
+        return binding.qk_norm_rope(q, k, positions, freqs, weight, weight)
+
     # The prompts, in pieces as a scheduler would admit them.
     left, T = lengths.clone(), 65536
     while int(left.sum()):
         share = torch.minimum(left, torch.tensor(T // R, device="cuda"))
-        starts, slots, _ = s.grant(share.int(), T)
+        starts, slots, positions = s.grant(share.int(), T)
         n = int(starts[-1])
-        s.write(random(n, heads), random(n, heads), slots[:n].contiguous())
+        k, _ = turn(random(n, heads), None, positions[:n])
+        s.write(k, random(n, heads), slots[:n].contiguous())
         left -= share
     assert int(s.status) == 0, "a request was refused"
 
     new = torch.full((R,), G, dtype=torch.int32, device="cuda")
     q, k, v = random(R * G, q_heads), random(R * G, heads), random(R * G, heads)
-    freqs = torch.exp(torch.arange(D // 2, device="cuda") * (-2 / D * math.log(10000.0)))
-    weight = torch.ones(D, dtype=torch.bfloat16, device="cuda")
     if G > 1:
         V = 32768
         target = torch.softmax(2 * torch.randn(R, G, V, generator=g, device="cuda"), -1)
@@ -157,9 +165,7 @@ def main(argv=None) -> int:
 
     def step():
         _, slots, positions = s.grant(new, R * G)
-        qt, kt = q, k
-        if args.bits == 4:
-            qt, kt = binding.qk_norm_rope(q, k, positions, freqs, weight, weight)
+        qt, kt = turn(q, k, positions)
         s.write(kt, v, slots)
         out = s.attend(qt, row_group=G)
         if G > 1:
@@ -185,9 +191,11 @@ def main(argv=None) -> int:
         times[name] = start.elapsed_time(end) * 1e3 / (2 * replays)
         assert int(s.status) == 0, "device status"
         if pages is not None:
-            _, lse = s.attend(q, row_group=G)
+            last = s.lengths[s.now][:, None] - G + torch.arange(G, dtype=torch.int32, device="cuda")
+            qt, _ = turn(q, None, last.flatten())  # the queries of the last G tokens
+            _, lse = s.attend(qt, row_group=G)
             s.pages = None
-            _, lse_all = s.attend(q, row_group=G)
+            _, lse_all = s.attend(qt, row_group=G)
             kept = torch.exp(lse - lse_all).mean()
         del result
     n = int(s.lengths[s.now].sum())
