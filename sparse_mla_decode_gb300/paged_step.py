@@ -196,7 +196,7 @@ def main(argv=None) -> int:
             _, lse = s.attend(qt, row_group=G)
             s.pages = None
             _, lse_all = s.attend(qt, row_group=G)
-            kept = torch.exp(lse - lse_all).mean()
+            kept = torch.exp(lse - lse_all)[lse_all > -math.inf].mean()  # of rows that see a token
         del result
     n = int(s.lengths[s.now].sum())
     print(f"{R} requests, {n} tokens ({n * heads * D * (2 if args.bits == 8 else 1.125) / 1e9:.2f} GB of keys and "

@@ -44,3 +44,12 @@ def test_the_command_norms_and_turns_all_keys_and_queries_of_a_4_bit_cache(cuda,
     assert all(id(q) in ours for q in asked), "queries"
     sizes = written[0].float().pow(2).mean(-1)
     assert bool(((sizes - 1).abs() < 0.02).all())  # a norm of 1, in bf16
+
+
+def test_the_share_is_of_rows_that_see_a_token(cuda, capsys):
+    """Requests shorter than a step's verify rows, the first of which see nothing."""
+    from sparse_mla_decode_gb300 import paged_step
+    assert paged_step.main(["--requests", "40", "--context", "1", "--steps", "1", "--pages", "4", "--bits", "4",
+                            "--drafts", "7"]) == 0
+    out = capsys.readouterr().out
+    assert "100.0% of the attention weight" in out and "nan" not in out
