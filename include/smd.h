@@ -758,7 +758,9 @@ int smd_paged_append(const smd_paged_cache_t* cache, const uint16_t* k, int64_t 
                      smd_stream_t stream);
 
 /* An upper bound, up to its rounding, of the products of a row's queries with
- * the keys of each page: for row b, kv head h and page j of its request,
+ * the keys of each page as they were appended (a stored key can be larger than it was, by half
+ * a step of E4M3, or, in 4 bits, by up to a fifth of the largest value of its block of 16 columns):
+ * for row b, kv head h and page j of its request,
  *   score[b, h, j] = BF16(max over the query heads i of h of
  *                    sum_c max(q[b,i,c], 0) * hi[c] + min(q[b,i,c], 0) * lo[c])
  * with hi, lo the bounds of the page: the larger of q * hi and q * lo in each

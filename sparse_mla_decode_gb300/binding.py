@@ -1127,7 +1127,8 @@ def _paged_rows(q, cache, table, lengths, row_group):
 def block_scores(q, cache: PagedCache | PagedCache4, table, lengths, row_group: int = 1, keep_first: int = 0,
                  keep_last: int = 0, out=None, stream=None):
     """The score of each page for each row and kv head (smd_block_scores): an
-    upper bound of q . k over the page's keys, the largest over the kv head's
+    upper bound of q . k over the page's keys as they were appended (rounding to the cache's
+    bits can lift a stored one above its page's bounds), the largest over the kv head's
     query heads. q [R * row_group, Hq, head_dim] bfloat16, table [R, width] and
     lengths [R] int32. Returns bfloat16 [R * row_group, heads, width], NaN past
     the pages a row sees; ``scores.flatten(0, 1)`` goes to topk_select."""

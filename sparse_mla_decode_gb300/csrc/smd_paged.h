@@ -17,8 +17,8 @@ constexpr int kPagedMaxHeads = 128;  // query heads of a kv head
 
 // What smd_paged_cache_init leaves in smd_paged_cache_t::map: a mark, then the
 // tensor maps of k and v (absent in a cache of bounds only). smd_paged4_cache_init: a mark of its
-// own, then the maps of k, v and their block scales for the mma.sync kernel, then, at 128 columns,
-// for the tcgen05 kernel.
+// own, then the maps of k, v and their block scales, with the boxes of the kernel that its columns
+// take (128: tcgen05, others: mma.sync).
 constexpr uint64_t kPagedMark = 0x736d645061676564ull, kPaged4Mark = 0x736d645061673465ull;
 static_assert(sizeof(CUtensorMap) == 128, "two maps and the mark fit smd_paged_cache_t::map");
 static_assert(sizeof(smd_paged4_cache_t::map) >= 4 * sizeof(CUtensorMap) + 8, "four maps and the mark");

@@ -20,7 +20,7 @@
 // tokens: the lanes whose token begins a run read its keys too; many: a block takes the runs that
 // begin in its chunk of tokens.
 //
-// Measured (GB300, device time): 96 tokens of as many requests, 8 heads of 128 columns, 2.6 us (1.8
+// Measured (GB300, device time): 96 tokens of as many requests, 8 heads of 128 columns, 2.4 to 2.6 us (1.8
 // without bounds); 28 thousand tokens of 23 requests 35 us, 63% of the copy rate for the 146 MB (27
 // without bounds, 80%: the bounds read the keys again from L2 and follow the codes), 256 columns 62 (71%),
 // 64 columns in pages of 16 29 (38%). Read: 96 tokens 2.1 us, 28 thousand 24.9 (88%;
@@ -432,14 +432,17 @@ __global__ void __launch_bounds__(kThreads) read4_kernel(const Read4Params p) {
 
 template <int D>
 int launch_append(const Append4Params& p, int sms, smd_stream_t stream) {
-    // Few tokens: lanes for each. Many: blocks by chunks of tokens. Few / many in us, 8 heads of 128
-    // columns, pages of 64 (in brackets without bounds):
-    //   96 tokens of as many requests   2.7 /  8.3  ( 1.8 /  4.3)
-    //   3000 of as many                 7.4 / 13.5  ( 5.0 /  6.7)
-    //   8000 of as many                22.3 / 20.8  (10.9 /  9.7)
-    //   500 of one                      6.9 /  6.3  ( 2.2 /  4.3)
-    //   4000 of one, of 30             10.9 / 10.4, 11.7  ( 6.1 /  8.2)
-    //   16000 of one                   30.3 / 19.8  (21.8 / 15.3)
+    // Few tokens: lanes for each. Many: blocks by chunks of tokens. The limit is one of units: which tokens
+    // continue one another is known to the GPU only. Just below it tokens of as many requests gain and prompts lose.
+    // Few / many in us, 8 heads of 128 columns, pages of 64 (in brackets without bounds):
+    //   96 tokens of as many requests   2.4 /  7.8  ( 1.8 /  4.3)
+    //   3000 of as many                 8.4 / 14.2  ( 5.3 /  7.1)
+    //   7000 of as many                18.5 / 22.2  (13.0 / 12.1)
+    //   8000 of as many                21.0 / 24.6  (14.5 / 13.5)
+    //   500 of one                      6.8 /  5.3  ( 2.2 /  4.3)
+    //   4000 of one                    11.9 / 10.3  ( 6.3 /  8.4)
+    //   7000 of one, of 30             18.0 / 12.8, 13.7  (11.6 / 10.6)
+    //   16000 of one                   33.8 / 20.7  (25.9 / 17.1)
     const int64_t units = static_cast<int64_t>(p.T) * p.heads;
     if (units <= static_cast<int64_t>(sms) * kFewUnits)
         return launch_pdl(append4_few_kernel<D>,

@@ -55,8 +55,8 @@ extern "C" int smd_paged4_decode_ex(const uint16_t* q, int64_t q_stride,
                           stream, force};
     return run_decode(call, shape_of(cache), p, [&](const PagedParams& p, int64_t tiles, int RT, int sms) {
         // 128 columns: tcgen05. mma.sync (smd_paged_decode.cuh), measured in its place with 64 requests of
-        // 1024 .. 8192 tokens, tcgen05 / mma.sync in us: pages of 64 tokens, 8 / 16 / 32 query rows 74 / 84,
-        // 83 / 111, 117 / 167; pages of 16 88 / 92, 94 / 119, 135 / 179; one request of 777 tokens 12.6 / 11.3.
+        // 1024 .. 8192 tokens, tcgen05 / mma.sync in us: pages of 64 tokens, 8 / 16 / 32 query rows 73 / 84,
+        // 82 / 111, 115 / 167; pages of 16 89 / 92, 94 / 119, 123 / 179; one request of 777 tokens 12.6 / 11.3.
         if (D == 128)
             return paged4_tc(p, maps, tc_box_tokens(cache->page_size), 8 * RT, sms, (tiles + 3) / 4, stream);
         const bool halves = page_box_tokens(cache->page_size, D) < (D == 256 ? 16 : 32);  // a tile spans two pages

@@ -22,8 +22,9 @@
 //
 // A worker's tile is a chain: scales, S^T, the weights, V, the product. The four workers of an SM (three
 // at 32 rows: 96, 104 and 152 columns of tensor memory each; V lies over the logits that were read) hide
-// one another's waits; two tiles' logits in flight for three workers were slower (98 us for 74 below), and so
-// were warps of one job each (K, V, weights) in turn on a pipeline's tiles (211 for 92 at 16 rows). Each worker has
+// one another's waits; two tiles' logits in flight for three workers were slower (98 us for 91, when one warp copied
+// for all workers; not measured since), and so were warps of one job each (K, V, weights) in turn on a pipeline's tiles
+// (211 for 92 at 16 rows, then, too). Each worker has
 // a warp for its copies, which looks up 4 to 32 tiles at once, a lane for each box: with one such warp for
 // all workers the round trips for table entries bound the kernel (91 us; 147 with pages of 16 tokens).
 // A thread has one token's logits: no reduction over tokens is needed but for the sums, once a unit,
@@ -32,7 +33,7 @@
 //
 // Measured (GB300, device time; of the rate at which the GPU copies), pages of 64 tokens:
 //   64 requests of 1024 .. 8192 tokens, 8 / 16 / 32 / 64 rows    73 us 70% / 82 us 63% / 115 us 45% / 208 us 26%
-//   the same with pages of 16 tokens, 8 / 16 / 32 rows           89 us / 94 us / 124 us
+//   the same with pages of 16 tokens, 8 / 16 / 32 rows           89 us / 94 us / 123 us
 //   64 listed pages in each of 64 requests, 8 / 16 / 32 rows     69 us 66% / 78 us 59% / 108 us 43%
 //   16 requests up to 65536 tokens, 8 / 16 / 32 rows             110 us 83% / 121 us 76% / 170 us 54%
 //   200 requests up to 300 tokens, 8 / 16 / 32 rows              29 us / 36 us / 57 us

@@ -20,7 +20,7 @@
 //
 // Measured (GB300, device time): 28 thousand tokens, 64 + 8 heads of 128 columns, three axes 165 us, 93% of the
 // copy rate (159 without norm; 256 columns 92%, 64 89%, 16 of 128 columns turning 89%); 1000 tokens 8.4
-// (66%: start); 96 tokens 3.3; 28 thousand tokens of 5 heads 28 (38%: angles). With 80 registers a thread
+// (66%: start); 96 tokens 3.3; 28 thousand tokens of 5 heads 28 (38%: angles and the phases around them). With 80 registers a thread
 // the kernel spills and takes 204.
 #include "smd_internal.h"
 #include "smd_paged.h"
